@@ -109,6 +109,22 @@ def _load():
     lib.iqp_debug_indexer_q_clock.restype = ctypes.c_int
     lib.iqp_device_clock_rates.argtypes = [c_p, c_p]
     lib.iqp_device_clock_rates.restype = ctypes.c_int
+    c_f32 = ctypes.c_float
+    lib.fp8_gemm_1x128_128x128.argtypes = [c_p, c_i64, c_p, c_i64, c_i64, c_p, c_i64, c_p, c_i64, c_i64, c_i64, c_i64,
+                                           c_p, c_i64, c_p]
+    lib.qk_norm_rope.argtypes = [c_p, c_i64, c_p, c_i64, c_i64, c_i32, c_i32, c_i32, c_i32, c_p, c_p, c_f32, c_p, c_p,
+                                 c_i64, c_p, c_i64, c_p, c_i64, c_i32, c_p]
+    batch_args = [c_p, c_i64, c_i32, c_p, c_p, c_i32]
+    lib.kv_cache_append_fp8.argtypes = [c_p, c_i64, c_p, c_i64, c_i64, c_i32, c_i32, c_p, c_p, c_p, c_p, c_i64, c_i32] + \
+        batch_args + [c_p]
+    lib.kv_cache_read_fp8.argtypes = [c_p, c_p, c_p, c_p, c_i64, c_i32, c_i32, c_i32] + batch_args + \
+        [c_p, c_i64, c_p, c_i64, c_i64, c_p]
+    lib.attention_fp8_kv.argtypes = [c_p, c_i64, c_i64, c_i32, c_i32, c_i32, c_p, c_p, c_p, c_p, c_i64, c_i32] + \
+        batch_args + [c_f32, c_i32, c_p, c_i64, c_p, c_i64, c_p]
+    for name in ("fp8_gemm_1x128_128x128", "qk_norm_rope", "kv_cache_append_fp8", "kv_cache_read_fp8", "attention_fp8_kv"):
+        getattr(lib, name).restype = ctypes.c_int
+    lib.attention_fp8_kv_workspace_bytes.argtypes = [c_i32]
+    lib.attention_fp8_kv_workspace_bytes.restype = c_i64
     return lib
 
 
@@ -654,3 +670,9 @@ def indexer_q_prep(x, w, w_scales, positions, cos_sin, n_heads: int = 64, rope_l
     a, a_scales = fp8_quant_1x128_ue8m0(x, stream=stream)
     return indexer_q_gemm_rope_fp4(a, a_scales, w, w_scales, positions, cos_sin, n_heads=n_heads,
                                    cos_sin_lanes=cos_sin_lanes, stream=stream, **conv)
+
+
+from . import layer as _layer  # noqa: E402  (it takes the library and the checks above)
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += _layer.__all__

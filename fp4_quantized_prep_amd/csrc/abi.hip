@@ -502,3 +502,204 @@ const char* iqp_status_string(int status) {
 int iqp_abi_version(void) { return IQP_ABI_VERSION; }
 
 }  // extern "C"
+
+namespace {
+
+// Checks of a ragged batch over the paged cache, shared by the cache's calls
+// and attention; fills b. T == 0 or S == 0 leaves nothing to do.
+int check_seq_batch(int64_t T, int32_t S, const int32_t* block_table, int64_t ld_table, int32_t max_blocks,
+                    const int32_t* seq_lens, const int32_t* cu_rows, int64_t n_blocks, int32_t block_size, int32_t Hk,
+                    int32_t D, iqp::SeqBatch& b) {
+  if (T < 0 || S < 0 || max_blocks < 0 || n_blocks < 0 || block_size < 0 || Hk < 0 || D < 0) return IQP_ERR_INVALID;
+  if (T == 0 || S == 0) return IQP_OK;
+  if (!block_table || !seq_lens || !cu_rows) return IQP_ERR_INVALID;
+  if (max_blocks == 0 || n_blocks == 0 || Hk == 0 || ld_table < max_blocks) return IQP_ERR_INVALID;
+  if (D != 64 && D != 128) return IQP_ERR_UNSUPPORTED;
+  if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128) return IQP_ERR_UNSUPPORTED;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_rows, 4)) return IQP_ERR_UNSUPPORTED;
+  if (T > 0x7FFFFFFF || Hk > 65535 || n_blocks > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  b.cu = cu_rows;
+  b.lens = seq_lens;
+  b.table = block_table;
+  b.ld_table = ld_table;
+  b.T = T;
+  b.n_blocks = n_blocks;
+  b.S = S;
+  b.max_blocks = max_blocks;
+  b.log_block = __builtin_ctz((unsigned)block_size);
+  return IQP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m, int64_t as_stride_w,
+                           const void* w, int64_t ldw, const uint8_t* w_scales, int64_t ld_ws, int64_t M, int64_t N,
+                           int64_t K, void* out, int64_t ldo, void* stream) {
+  if (M < 0 || N < 0 || K < 0) return IQP_ERR_INVALID;
+  if (M == 0 || N == 0) return IQP_OK;
+  if (!a || !a_scales || !w || !w_scales || !out) return IQP_ERR_INVALID;
+  if (K == 0 || lda < K || ldw < K || ldo < N) return IQP_ERR_INVALID;
+  if (K % 128) return IQP_ERR_UNSUPPORTED;
+  const int64_t nw = (K / 128 + 3) / 4;
+  if (check_scale_strides(M, nw, as_stride_m, as_stride_w) != IQP_OK || ld_ws < K / 128) return IQP_ERR_INVALID;
+  if (!aligned(a, 16) || lda % 16 || !aligned(w, 16) || ldw % 16 || !aligned(a_scales, 4) || !aligned(out, 2))
+    return IQP_ERR_UNSUPPORTED;
+  // a workgroup keeps a weight tile's scale bytes in one register (4 per lane)
+  // and addresses its tiles of up to 256 rows with 32-bit offsets
+  if (K / 128 > 256 || M > 0x7FFFFFFF || N > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  if (lda >= ((int64_t)1 << 23) || ldw >= ((int64_t)1 << 23)) return IQP_ERR_UNSUPPORTED;
+  if (as_stride_m >= ((int64_t)1 << 20) || nw * as_stride_w >= ((int64_t)1 << 28)) return IQP_ERR_UNSUPPORTED;
+  const int st = device_status();
+  if (st != IQP_OK) return st;
+  iqp::Fp8GemmArgs p{};
+  p.a = static_cast<const uint8_t*>(a);
+  p.lda = lda;
+  p.a_scales = a_scales;
+  p.as_sm = as_stride_m;
+  p.as_sw = as_stride_w;
+  p.w = static_cast<const uint8_t*>(w);
+  p.ldw = ldw;
+  p.w_scales = w_scales;
+  p.ld_ws = ld_ws;
+  p.M = M;
+  p.N = N;
+  p.nkb = (int32_t)(K / 128);
+  p.out = static_cast<uint16_t*>(out);
+  p.ldo = ldo;
+  p.wide_out = aligned(out, 16) && ldo % 8 == 0;
+  return from_hip(iqp::launch_fp8_gemm(p, static_cast<hipStream_t>(stream)));
+}
+
+int qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int64_t M, int32_t Hq, int32_t Hk, int32_t D,
+                 int32_t rope_dim, const void* q_weight, const void* k_weight, float eps, const int64_t* positions,
+                 const float* cos_sin, int64_t max_pos, void* q_out, int64_t ldqo, void* k_out, int64_t ldko,
+                 int32_t flags, void* stream) {
+  if (M < 0 || Hq < 0 || Hk < 0 || D < 0 || rope_dim < 0 || max_pos < 0 || !(eps >= 0.f)) return IQP_ERR_INVALID;
+  if (flags & ~IQP_ROPE_INTERLEAVED) return IQP_ERR_INVALID;
+  if (M == 0) return IQP_OK;
+  if (!q || !k || !q_weight || !k_weight || !positions || !cos_sin || !q_out || !k_out) return IQP_ERR_INVALID;
+  if (Hq == 0 || Hk == 0 || max_pos == 0 || rope_dim > D) return IQP_ERR_INVALID;
+  if (D != 64 && D != 128 && D != 256) return IQP_ERR_UNSUPPORTED;
+  if (rope_dim == 0 || rope_dim % 16) return IQP_ERR_UNSUPPORTED;
+  if (ldq < (int64_t)Hq * D || ldqo < (int64_t)Hq * D || ldk < (int64_t)Hk * D || ldko < (int64_t)Hk * D)
+    return IQP_ERR_INVALID;
+  if (!aligned(q, 16) || ldq % 8 || !aligned(k, 16) || ldk % 8 || !aligned(q_out, 16) || ldqo % 8 ||
+      !aligned(k_out, 16) || ldko % 8 || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 8) ||
+      !aligned(cos_sin, 16))
+    return IQP_ERR_UNSUPPORTED;
+  if (Hq > (1 << 20) || Hk > (1 << 20) || M > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  const int st = device_status();
+  if (st != IQP_OK) return st;
+  iqp::QkNormRopeArgs p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.q_weight = static_cast<const uint16_t*>(q_weight);
+  p.k_weight = static_cast<const uint16_t*>(k_weight);
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.max_pos = max_pos;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.ldqo = ldqo;
+  p.ldko = ldko;
+  p.M = M;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rope_dim = rope_dim;
+  p.eps = eps;
+  return from_hip(iqp::launch_qk_norm_rope(p, D, (flags & IQP_ROPE_INTERLEAVED) != 0, static_cast<hipStream_t>(stream)));
+}
+
+int kv_cache_append_fp8(const void* k, int64_t ldk, const void* v, int64_t ldv, int64_t T, int32_t Hk, int32_t D,
+                        void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales, int64_t n_blocks,
+                        int32_t block_size, const int32_t* block_table, int64_t ld_table, int32_t max_blocks,
+                        const int32_t* seq_lens, const int32_t* cu_rows, int32_t S, void* stream) {
+  iqp::KvAppendArgs p{};
+  int st = check_seq_batch(T, S, block_table, ld_table, max_blocks, seq_lens, cu_rows, n_blocks, block_size, Hk, D, p.seq);
+  if (st != IQP_OK || T == 0 || S == 0) return st;
+  if (!k || !v || !k_cache || !v_cache || !k_scales || !v_scales) return IQP_ERR_INVALID;
+  if (ldk < (int64_t)Hk * D || ldv < (int64_t)Hk * D) return IQP_ERR_INVALID;
+  if (!aligned(k, 16) || ldk % 8 || !aligned(v, 16) || ldv % 8 || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return IQP_ERR_UNSUPPORTED;
+  st = device_status();
+  if (st != IQP_OK) return st;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.ldk = ldk;
+  p.ldv = ldv;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.Hk = Hk;
+  return from_hip(iqp::launch_kv_append(p, D, static_cast<hipStream_t>(stream)));
+}
+
+int kv_cache_read_fp8(const void* k_cache, const void* v_cache, const uint8_t* k_scales, const uint8_t* v_scales,
+                      int64_t n_blocks, int32_t block_size, int32_t Hk, int32_t D, const int32_t* block_table,
+                      int64_t ld_table, int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_rows, int32_t S,
+                      void* k_out, int64_t ldk, void* v_out, int64_t ldv, int64_t T, void* stream) {
+  iqp::KvReadArgs p{};
+  int st = check_seq_batch(T, S, block_table, ld_table, max_blocks, seq_lens, cu_rows, n_blocks, block_size, Hk, D, p.seq);
+  if (st != IQP_OK || T == 0 || S == 0) return st;
+  if (!k_cache || !v_cache || !k_scales || !v_scales || !k_out || !v_out) return IQP_ERR_INVALID;
+  if (ldk < (int64_t)Hk * D || ldv < (int64_t)Hk * D) return IQP_ERR_INVALID;
+  if (!aligned(k_out, 16) || ldk % 8 || !aligned(v_out, 16) || ldv % 8 || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return IQP_ERR_UNSUPPORTED;
+  st = device_status();
+  if (st != IQP_OK) return st;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.ldk = ldk;
+  p.ldv = ldv;
+  p.Hk = Hk;
+  return from_hip(iqp::launch_kv_read(p, D, static_cast<hipStream_t>(stream)));
+}
+
+int64_t attention_fp8_kv_workspace_bytes(int32_t D) {
+  return D == 64 || D == 128 ? iqp::attention_workspace_bytes(D) : 0;
+}
+
+int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t Hk, int32_t D, const void* k_cache,
+                     const void* v_cache, const uint8_t* k_scales, const uint8_t* v_scales, int64_t n_blocks,
+                     int32_t block_size, const int32_t* block_table, int64_t ld_table, int32_t max_blocks,
+                     const int32_t* seq_lens, const int32_t* cu_rows, int32_t S, float scale, int32_t window, void* out,
+                     int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
+  iqp::AttnArgs p{};
+  if (Hq < 0 || window < 0 || !(scale > 0.f) || scale > 3e38f) return IQP_ERR_INVALID;
+  int st = check_seq_batch(T, S, block_table, ld_table, max_blocks, seq_lens, cu_rows, n_blocks, block_size, Hk, D, p.seq);
+  if (st != IQP_OK || T == 0 || S == 0) return st;
+  if (!q || !k_cache || !v_cache || !k_scales || !v_scales || !out || !workspace) return IQP_ERR_INVALID;
+  if (Hq == 0 || Hq % Hk || ldq < (int64_t)Hq * D || ldo < (int64_t)Hq * D) return IQP_ERR_INVALID;
+  if (workspace_bytes < iqp::attention_workspace_bytes(D)) return IQP_ERR_INVALID;
+  if (!aligned(q, 16) || ldq % 8 || !aligned(out, 16) || ldo % 8 || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(workspace, 256))
+    return IQP_ERR_UNSUPPORTED;
+  if (Hq > 65535) return IQP_ERR_UNSUPPORTED;
+  st = device_status();
+  if (st != IQP_OK) return st;
+  p.q = static_cast<const uint16_t*>(q);
+  p.ldq = ldq;
+  p.out = static_cast<uint16_t*>(out);
+  p.ldo = ldo;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.Hk = Hk;
+  p.group = Hq / Hk;
+  p.window = window;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.workspace = static_cast<uint8_t*>(workspace);
+  return from_hip(iqp::launch_attention(p, D, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -171,6 +171,112 @@ hipError_t launch_indexer_q_epilogue(const uint16_t* q, int64_t ldq, int64_t M, 
 hipError_t launch_fp8_quant_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldw, uint8_t* q, int64_t ldq,
                                    uint8_t* scales, int64_t ld_scales, hipStream_t stream);
 
+// --- the operators around an attention layer ---------------------------------
+
+// A ragged batch over the paged cache: sequence s has the rows cu[s] ..
+// cu[s + 1] - 1 of the batch's T rows, which are its last tokens: the last of
+// them is at position lens[s] - 1. Its token at position p lives at
+// p % 2^log_block of block table[s * ld_table + p / 2^log_block] (an entry
+// outside [0, n_blocks): not held).
+struct SeqBatch {
+  const int32_t* cu;        // [S + 1]
+  const int32_t* lens;      // [S]
+  const int32_t* table;     // [S, max_blocks], row stride ld_table
+  int64_t ld_table;
+  int64_t T;
+  int64_t n_blocks;
+  int32_t S;
+  int32_t max_blocks;
+  int32_t log_block;
+};
+
+// Arguments of the block-scaled FP8 product (validated on the host).
+struct Fp8GemmArgs {
+  const uint8_t* a;         // E4M3 [M, K], row stride lda bytes
+  int64_t lda;
+  const int32_t* a_scales;  // packed UE8M0 words, strides in words
+  int64_t as_sm, as_sw;
+  const uint8_t* w;         // E4M3 [N, K], row stride ldw bytes
+  int64_t ldw;
+  const uint8_t* w_scales;  // UE8M0 [ceil(N / 128), K / 128], row stride ld_ws
+  int64_t ld_ws;
+  int64_t M, N;
+  int32_t nkb;              // K / 128
+  uint16_t* out;            // bf16 [M, N], row stride ldo elements
+  int64_t ldo;
+  bool wide_out;            // 16-byte stores allowed (out and ldo aligned)
+};
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& args, hipStream_t stream);
+
+struct QkNormRopeArgs {
+  const uint16_t* q;        // bf16 [M, Hq * D], row stride ldq
+  const uint16_t* k;        // bf16 [M, Hk * D], row stride ldk
+  int64_t ldq, ldk;
+  const uint16_t* q_weight; // bf16 [D]
+  const uint16_t* k_weight;
+  const int64_t* positions; // [M]
+  const float* cos_sin;     // [max_pos, rope_dim]
+  int64_t max_pos;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int64_t ldqo, ldko;
+  int64_t M;
+  int32_t Hq, Hk, rope_dim;
+  float eps;
+};
+// D: 64, 128 or 256
+hipError_t launch_qk_norm_rope(const QkNormRopeArgs& args, int D, bool interleaved, hipStream_t stream);
+
+struct KvAppendArgs {
+  SeqBatch seq;
+  const uint16_t* k;        // bf16 [T, Hk * D], row stride ldk
+  const uint16_t* v;
+  int64_t ldk, ldv;
+  uint8_t* k_cache;         // E4M3 [n_blocks, Hk, B, D]
+  uint8_t* v_cache;         // E4M3 [n_blocks, Hk, D, B]
+  uint8_t* k_scales;        // UE8M0 [n_blocks, Hk]
+  uint8_t* v_scales;
+  int32_t Hk;
+};
+// D: 64 or 128
+hipError_t launch_kv_append(const KvAppendArgs& args, int D, hipStream_t stream);
+
+struct KvReadArgs {
+  SeqBatch seq;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  uint16_t* k_out;          // bf16 [T, Hk * D], row stride ldk
+  uint16_t* v_out;
+  int64_t ldk, ldv;
+  int32_t Hk;
+};
+hipError_t launch_kv_read(const KvReadArgs& args, int D, hipStream_t stream);
+
+// Arguments of attention over the FP8 cache (validated on the host).
+struct AttnArgs {
+  SeqBatch seq;
+  const uint16_t* q;        // bf16 [T, Hk * group * D], row stride ldq
+  int64_t ldq;
+  uint16_t* out;            // bf16, laid out alike, row stride ldo
+  int64_t ldo;
+  const uint8_t* k_cache;   // as in KvReadArgs
+  const uint8_t* v_cache;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  int32_t Hk, group;        // key heads, query heads per key head
+  int32_t window;           // 0: none
+  float scale_log2;         // softmax scale * log2(e)
+  uint8_t* workspace;       // attention_workspace_bytes(D)
+  int64_t max_rows;         // set by the launcher: the decode kernel leaves out sequences of more
+                            // rows (tokens * group)
+};
+// workgroups of the decode kernel: two for each of a full chip's 256 CUs
+constexpr int ATTN_WORKGROUPS = 512;
+int64_t attention_workspace_bytes(int D);
+hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream);
+
 // compute units of the current device (cached per device)
 int cu_count();
 

@@ -580,6 +580,145 @@ int iqp_debug_indexer_q_clock(const void* a, int64_t lda,
  */
 int iqp_device_clock_rates(int64_t* wall_clock_hz, int64_t* peak_shader_clock_hz);
 
+/*
+ * fp8_gemm_1x128_128x128 — block-scaled FP8 matrix product, bf16 out: the
+ * layer's other projections, on the operands of fp8_quant_1x128_ue8m0 and
+ * fp8_quant_weight_128x128_ue8m0.
+ *
+ *   out[m, n] = bf16( sum_j 2^(ea(m,j) + ew(n/128,j)) sum_{k in block j} A[m,k] W[n,k] )
+ * (float32 accumulation, one rounding to bf16).
+ *
+ *   a, lda, a_scales, as_stride_m, as_stride_w, w, ldw   as in
+ *              indexer_q_gemm_rope_fp4 (row strides multiples of 16, below
+ *              2^23 bytes; K a multiple of 128, at most 32768).
+ *   w          E4M3 [N, K]; N is any (the scales' last tile may be partial).
+ *   w_scales   UE8M0 [ceil(N/128), K/128], row stride ld_ws (bytes, >= K/128).
+ *   out        bf16 [M, N], row stride ldo (elements, >= N), 2-byte aligned
+ *              (16-byte stores where it is 16-byte aligned and ldo a multiple
+ *              of 8). Must not overlap the inputs.
+ * M == 0 or N == 0: no-op. The sum must fit float32, as there.
+ */
+int fp8_gemm_1x128_128x128(const void* a, int64_t lda,
+                           const int32_t* a_scales, int64_t as_stride_m, int64_t as_stride_w,
+                           const void* w, int64_t ldw, const uint8_t* w_scales, int64_t ld_ws,
+                           int64_t M, int64_t N, int64_t K, void* out, int64_t ldo, void* stream);
+
+/*
+ * qk_norm_rope — RMS norm of every query and key head, times its weights,
+ * then RoPE, in one pass.
+ *
+ * For every token m and head x of D values (queries with q_weight, keys with
+ * k_weight), in float32 with one rounding to bf16:
+ *   y_d = x_d / sqrt(mean(x^2) + eps) * weight_d
+ *   RoPE on dims [0, rope_dim) with the row positions[m] of cos_sin: pairs
+ *   (i, i + rope_dim/2), or with IQP_ROPE_INTERLEAVED (2i, 2i + 1), as in
+ *   indexer_q_rope_hadamard_fp4.
+ *
+ *   q, k       bf16 [M, Hq*D] and [M, Hk*D], row strides ldq, ldk (elements):
+ *              16-byte aligned, strides multiples of 8.
+ *   q_out, k_out   likewise, strides ldqo, ldko; may be q and k themselves (same
+ *              strides), otherwise must not overlap them.
+ *   q_weight, k_weight   bf16 [D], 16-byte aligned.
+ *   D          64, 128 or 256; rope_dim a multiple of 16, 16 to D; eps >= 0.
+ *   positions, cos_sin, max_pos   as in indexer_q_gemm_rope_fp4 (table of
+ *              rope_dim columns; positions outside it are clamped).
+ *   flags      0 or IQP_ROPE_INTERLEAVED, else IQP_ERR_INVALID.
+ */
+int qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int64_t M, int32_t Hq, int32_t Hk,
+                 int32_t D, int32_t rope_dim, const void* q_weight, const void* k_weight, float eps,
+                 const int64_t* positions, const float* cos_sin, int64_t max_pos,
+                 void* q_out, int64_t ldqo, void* k_out, int64_t ldko, int32_t flags, void* stream);
+
+/*
+ * The FP8 key/value cache of one layer: n_blocks blocks of block_size tokens
+ * (16, 32, 64 or 128), Hk key heads of D values (64 or 128):
+ *   k_cache   E4M3 [n_blocks, Hk, block_size, D]
+ *   v_cache   E4M3 [n_blocks, Hk, D, block_size] (a dim's tokens together, the
+ *             order in which attention multiplies them)
+ *   k_scales, v_scales   UE8M0 [n_blocks, Hk]: value = code * 2^(byte - 127)
+ * k_cache and v_cache 16-byte aligned. All contiguous.
+ *
+ * A batch of S sequences and T rows: rows cu_rows[s] .. cu_rows[s+1] - 1 are
+ * the last tokens of sequence s, which has seq_lens[s] tokens with them (row
+ * cu_rows[s] + i is position seq_lens[s] - (cu_rows[s+1] - cu_rows[s]) + i).
+ *   cu_rows      int32 [S + 1], non-decreasing from 0; values outside [0, T]
+ *                are clamped into it.
+ *   seq_lens     int32 [S].
+ *   block_table  int32 [S, max_blocks], row stride ld_table: position p of
+ *                sequence s is token p % block_size of block
+ *                block_table[s, p / block_size]. An entry outside [0,
+ *                n_blocks), a position of max_blocks * block_size or more, and a
+ *                position below 0 mean a token that is not held.
+ * These three arrays are read on the device: a call can be captured once and
+ * replayed with other lengths, up to the T rows and S sequences it was given.
+ * T == 0 or S == 0: no-op.
+ */
+
+/*
+ * kv_cache_append_fp8 — quantise new keys and values into the cache.
+ *
+ * For each block and head that rows of the batch fall into, with lo the first
+ * such token of the block and amax taken over those rows' values in it:
+ *   need = max(ceil(log2(amax / 448)), -22)            (the 1x128 quantizer's rule)
+ *   e    = need where lo == 0, else max(need, byte - 127)
+ *   code = E4M3 round-to-nearest-even of x * 2^-e;     byte = e + 127
+ * Where e > byte - 127 before the call, the codes of the block's tokens
+ * 0 .. lo - 1 become E4M3 RNE of code * 2^(byte - 127 - e). Tokens behind the
+ * last one written keep their codes (a sequence ends with the rows it is
+ * given). Rows that are not held are left out.
+ *
+ *   k, v       bf16 [T, Hk*D], row strides ldk, ldv (elements); 16-byte
+ *              aligned, strides multiples of 8. Finite.
+ * A block must not receive rows of two sequences in one call.
+ */
+int kv_cache_append_fp8(const void* k, int64_t ldk, const void* v, int64_t ldv, int64_t T, int32_t Hk, int32_t D,
+                        void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales,
+                        int64_t n_blocks, int32_t block_size,
+                        const int32_t* block_table, int64_t ld_table, int32_t max_blocks,
+                        const int32_t* seq_lens, const int32_t* cu_rows, int32_t S, void* stream);
+
+/*
+ * kv_cache_read_fp8 — the batch's rows read back from the cache as bf16
+ * (exact: a code has 4 significant bits).
+ *
+ *   k_out, v_out   bf16 [T, Hk*D], row strides ldk, ldv (elements); 16-byte
+ *                  aligned, strides multiples of 8. Rows of tokens that are not
+ *                  held, and rows behind cu_rows[S], are left as they were.
+ */
+int kv_cache_read_fp8(const void* k_cache, const void* v_cache, const uint8_t* k_scales, const uint8_t* v_scales,
+                      int64_t n_blocks, int32_t block_size, int32_t Hk, int32_t D,
+                      const int32_t* block_table, int64_t ld_table, int32_t max_blocks,
+                      const int32_t* seq_lens, const int32_t* cu_rows, int32_t S,
+                      void* k_out, int64_t ldk, void* v_out, int64_t ldv, int64_t T, void* stream);
+
+/*
+ * attention_fp8_kv — causal attention of bf16 queries over the FP8 cache.
+ *
+ * For the row at position p of a sequence and query head h, over the held
+ * tokens t <= p (and t > p - window where window > 0) of key head h / (Hq / Hk):
+ *   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q . k_t)
+ * with k_t, v_t the values the cache stands for; zeros where there is no such
+ * token. Scores, maxima and sums are float32; the weights w_t are rounded to
+ * fp16 for the second product, relative to the row's largest w_t 2^e_t (e_t the
+ * value exponent of t's block).
+ *
+ *   q, out     bf16 [T, Hq*D], row strides ldq, ldo (elements); 16-byte
+ *              aligned, strides multiples of 8; out must not overlap q. Rows
+ *              behind cu_rows[S] are left as they were.
+ *   Hq         a multiple of Hk (else IQP_ERR_INVALID); scale > 0.
+ *   workspace  attention_fp8_kv_workspace_bytes(D) bytes of device memory,
+ *              256-byte aligned; its contents do not matter before and mean
+ *              nothing after. Calls that share one must not overlap.
+ */
+int64_t attention_fp8_kv_workspace_bytes(int32_t D);
+int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                     const void* k_cache, const void* v_cache, const uint8_t* k_scales, const uint8_t* v_scales,
+                     int64_t n_blocks, int32_t block_size,
+                     const int32_t* block_table, int64_t ld_table, int32_t max_blocks,
+                     const int32_t* seq_lens, const int32_t* cu_rows, int32_t S,
+                     float scale, int32_t window, void* out, int64_t ldo,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* iqp_status_string(int status);
 
