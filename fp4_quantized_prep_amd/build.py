@@ -1,8 +1,9 @@
-"""Builds libiqprep.so (the HIP kernels and the C ABI) for gfx950 in-tree.
+"""Builds libiqprep.so (the HIP kernels and the C ABI) for gfx950 in-tree, and
+the host-only Python binding of the attention layer's calls (_binding.so).
 
     python fp4_quantized_prep_amd/build.py
 
-(run as a script: importing the package itself needs the built library).
+(run as a script: importing the package itself needs the built files).
 
 Compiles every csrc/*.hip with hipcc into fp4_quantized_prep_amd/libiqprep.so.
 hipcc cross-compiles, so no GPU is needed to build.
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libiqprep.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 ARCH = "gfx950"
 
 
@@ -73,7 +75,30 @@ def build(verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    build_binding(verbose)
     return LIB_PATH
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp against torch and libiqprep.so; host code only."""
+    import sysconfig
+
+    import torch
+    import torch.utils.cpp_extension as ext
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-I{INCLUDE}"] + [f"-isystem{d}" for d in ext.include_paths() + ["/opt/rocm/include", sysconfig.get_paths()["include"]]]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{torch_lib}", "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_hip",
+            f"-L{PKG_DIR}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the binding's build failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
 
 
 if __name__ == "__main__":

@@ -29,20 +29,14 @@
 //     A piece covers the end of one pair, whole pairs, and the start of
 //     another; whole pairs are finished at once, the rest go to the workspace as
 //     (max, sum, unnormalised output) and a second small launch joins them.
-#include "layer_common.h"
+#include "attention_common.h"
 
 namespace iqp {
 namespace {
 
-using namespace layer;
+using namespace attn;
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-
-constexpr int UNIT = 64;
 constexpr int DWAVES = 4;
-constexpr float LOWEST = -1e30f;     // below every score: the running maximum before the first token
 
 // What a workgroup needs of a sequence.
 struct Seq {
@@ -116,31 +110,6 @@ struct Partial {
   float m[16 * NT], l[16 * NT];
   float o[16 * NT][D];
 };
-
-__device__ __forceinline__ v8bf widen_bf16(uint32_t a, uint32_t b) {
-  typedef __bf16 v2 __attribute__((ext_vector_type(2)));
-  const v2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false), x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
-  const v2 x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false), x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
-  return v8bf{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
-}
-
-__device__ __forceinline__ v8h widen_f16(uint32_t a, uint32_t b) {
-  const v2h x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, false), x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, true);
-  const v2h x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, false), x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, true);
-  return v8h{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
-}
-
-// 16 bytes with those of tokens outside [lo, hi) cleared (byte j: token j)
-__device__ __forceinline__ v4u clear_outside(v4u v, int lo, int hi) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int a = min(max(lo - 4 * j, 0), 4), b = min(max(hi - 4 * j, 0), 4);
-    const uint32_t ma = a >= 4 ? 0u : 0xFFFFFFFFu << (8 * a);
-    const uint32_t mb = b >= 4 ? 0xFFFFFFFFu : (1u << (8 * b)) - 1u;
-    v[j] &= ma & mb;
-  }
-  return v;
-}
 
 template <int D, int NT>
 __global__ __launch_bounds__(DWAVES * 64)
@@ -369,7 +338,7 @@ void attention_decode_kernel(AttnArgs p) {
         for (int j = 0; j < 4; ++j) acc[j] += x[j] * a;
       }
       if (whole) {
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        const float inv = inverse_sum(sum);
         const int64_t tok = (row0 + r) / p.group;
         uint16_t* dst = p.out + (q.begin + tok) * p.ldo + ((int64_t)head * p.group + (row0 + r - tok * p.group)) * D + d;
         *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
@@ -432,7 +401,7 @@ void attention_join_kernel(AttnArgs p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] += v[j] * a;
     }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    const float inv = inverse_sum(sum);
     const int64_t tok = (row0 + r) / p.group;
     uint16_t* dst = p.out + (q.begin + tok) * p.ldo + ((int64_t)head * p.group + (row0 + r - tok * p.group)) * D + d;
     *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
@@ -452,17 +421,33 @@ hipError_t launch(const AttnArgs& p, hipStream_t stream) {
 
 }  // namespace
 
-int64_t attention_workspace_bytes(int D) {
+int64_t attention_decode_workspace_bytes(int D) {
   return (int64_t)ATTN_WORKGROUPS * 2 * (D == 64 ? sizeof(Partial<64, 2>) : sizeof(Partial<128, 2>));
 }
 
-hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream) {
-  AttnArgs p = args;
-  p.max_rows = (int64_t)1 << 62;
+hipError_t launch_attention_decode(const AttnArgs& p, int D, hipStream_t stream) {
   // two tiles of rows a wave once a sequence brings more than one on average
   const bool two = p.seq.T * p.group > 16 * (int64_t)p.seq.S;
   if (D == 64) return two ? launch<64, 2>(p, stream) : launch<64, 1>(p, stream);
   return two ? launch<128, 2>(p, stream) : launch<128, 1>(p, stream);
+}
+
+int64_t attention_workspace_bytes(int D) {
+  const int64_t a = attention_decode_workspace_bytes(D), b = attention_prefill_workspace_bytes(D);
+  return a > b ? a : b;
+}
+
+hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream) {
+  AttnArgs p = args;
+  if (p.seq.T <= ATTN_DECODE_TOKENS * (int64_t)p.seq.S) {
+    p.max_rows = (int64_t)1 << 62;
+    return launch_attention_decode(p, D, stream);
+  }
+  // a single sequence needs one kernel, whatever its number of rows turns out to be
+  p.max_rows = p.seq.S == 1 ? 0 : ATTN_DECODE_ROWS;
+  const hipError_t e = launch_attention_prefill(p, D, stream);
+  if (e != hipSuccess || p.seq.S == 1) return e;
+  return launch_attention_decode(p, D, stream);
 }
 
 }  // namespace iqp

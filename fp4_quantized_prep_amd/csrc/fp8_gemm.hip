@@ -173,14 +173,188 @@ void fp8_gemm_tile_kernel(Fp8GemmArgs p) {
   gemm_tile<TN, TM, WN, WM, NST>(p, lds);
 }
 
+// Stream kernel, for few tokens: the product is then a read of the weights. A
+// workgroup owns NT = 16 RT weight rows and all (at most 16 MT) tokens; its
+// WAVES waves share out the K blocks (wave w takes blocks w, w + WAVES, ...), so
+// that small N still spreads over many CUs and no second launch or workspace
+// joins partial sums. Each wave streams its blocks' weight and activation rows
+// through NST LDS stages of its own: no barrier in the loop, only the wave's
+// wait counts. Copies past the last block read zeros out of bounds, which
+// keeps the counts constant. The waves' sums meet in LDS at the end.
+// 16x16x128 MFMA: weight rows as its rows, tokens as its columns.
+template <int RT, int MT, int WAVES, int NST>
+constexpr int stream_lds_bytes() {
+  constexpr int ring = WAVES * NST * ((16 * RT + 16 * MT) * KB + 256);
+  constexpr int sums = WAVES * 16 * MT * (16 * RT + 4) * 4;
+  return ring > sums ? ring : sums;
+}
+
+template <int RT, int MT, int WAVES, int NST>
+__device__ __forceinline__ void gemm_stream(const Fp8GemmArgs& p, uint8_t* lds) {
+  constexpr int NT = 16 * RT, TOK = 16 * MT;
+  constexpr int STAGE = (NT + TOK) * KB + 256;      // weights, activations, scale words
+  constexpr int WC = NT / 8, AC = TOK / 8, NCOPY = WC + AC + 1;
+  constexpr uint32_t PAST = 0x40000000u;            // beyond every buffer here
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * NT;
+  const int64_t m0 = (int64_t)blockIdx.y * TOK;
+  const int nkb = p.nkb;
+  const int64_t wrows = p.N - n0 < NT ? p.N - n0 : NT, arows = p.M - m0 < TOK ? p.M - m0 : TOK;
+  const rsrc_t rw = make_rsrc(p.w + n0 * p.ldw, (uint64_t)wrows * p.ldw);
+  const rsrc_t ra = make_rsrc(p.a + m0 * p.lda, (uint64_t)arows * p.lda);
+  const int64_t nw = (nkb + 3) / 4;
+  const rsrc_t rs = make_rsrc(p.a_scales + m0 * p.as_sm, 4 * (uint64_t)((arows - 1) * p.as_sm + (nw - 1) * p.as_sw + 1));
+  // copy c moves rows 8 c + lane / 8, 16-byte chunk permuted by (row / 2) % 8
+  uint32_t vw[WC], va[AC];
+#pragma unroll
+  for (int c = 0; c < WC; ++c) {
+    const int r = 8 * c + (lane >> 3);
+    vw[c] = (uint32_t)(r * (int)p.ldw + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
+  }
+#pragma unroll
+  for (int c = 0; c < AC; ++c) {
+    const int r = 8 * c + (lane >> 3);
+    va[c] = (uint32_t)(r * (int)p.lda + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
+  }
+  const uint32_t vs = lane < TOK ? (uint32_t)(4 * lane * (int)p.as_sm) : PAST;
+  uint8_t* const ring = lds + wave * NST * STAGE;
+
+  // block i of this wave into stage st
+  auto copy = [&](int i, int st) __attribute__((always_inline)) {
+    const int j = wave + WAVES * i;
+    const uint32_t u = j < nkb ? (uint32_t)(KB * j) : PAST;
+    uint8_t* const b = ring + st * STAGE;
+#pragma unroll
+    for (int c = 0; c < WC; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(b + SLAB * c), 16, vw[c] + u, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < AC; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + NT * KB + SLAB * c), 16, va[c] + u, 0, 0, 0);
+    const uint32_t us = j < nkb ? (uint32_t)(4 * (j >> 2) * (int)p.as_sw) : PAST;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(b + (NT + TOK) * KB), 4, vs + us, 0, 0, 0);
+  };
+
+  const uint8_t* wsc = p.w_scales + n0 / 128 * p.ld_ws;
+  uint32_t wsc_lane = 0;
+  uint8_t wb[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) wb[b] = wsc[4 * lane + b < nkb ? 4 * lane + b : 0];
+#pragma unroll
+  for (int st = 0; st < NST; ++st) copy(st, st);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) wsc_lane |= (uint32_t)wb[b] << (8 * b);
+
+  v4f acc[RT][MT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[r][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int count = nkb > wave ? (nkb - wave + WAVES - 1) / WAVES : 0;
+  constexpr int WAIT = waitcnt_vm((NST - 1) * NCOPY);
+  const int swz = (col >> 1) & 7;
+  const int c0 = 16 * ((2 * g) ^ swz), c1 = 16 * ((2 * g + 1) ^ swz);
+  int st = 0;
+  for (int i = 0; i < count; ++i) {
+    __builtin_amdgcn_s_waitcnt(WAIT);
+    asm volatile("" ::: "memory");
+    const int j = wave + WAVES * i;
+    const uint8_t* const b = ring + st * STAGE;
+    const int ws = (int)((uint32_t)__builtin_amdgcn_readlane((int)wsc_lane, j >> 2) >> (8 * (j & 3)));
+    v8i fw[RT], fa[MT];
+    int as[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      as[t] = (int)(*reinterpret_cast<const uint32_t*>(b + (NT + TOK) * KB + 4 * (16 * t + col)) >> (8 * (j & 3)));
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const uint8_t* x = b + KB * (16 * r + col);
+      fw[r] = make_v8i(*reinterpret_cast<const v4u*>(x + c0), *reinterpret_cast<const v4u*>(x + c1));
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const uint8_t* x = b + NT * KB + KB * (16 * t + col);
+      fa[t] = make_v8i(*reinterpret_cast<const v4u*>(x + c0), *reinterpret_cast<const v4u*>(x + c1));
+    }
+    // the stage is read: refill it
+    __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    copy(i + NST, st);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        acc[r][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[r], fa[t], acc[r][t], 0, 0, 0, ws, 0, as[t]);
+    st = st + 1 < NST ? st + 1 : 0;
+  }
+
+  // the waves' sums, [wave][token][row], in the ring's place
+  __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
+  __syncthreads();
+  constexpr int PITCH = NT + 4;
+  float* const sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      *reinterpret_cast<v4f*>(sums + ((int64_t)wave * TOK + 16 * t + col) * PITCH + 16 * r + 4 * g) = acc[r][t];
+  __syncthreads();
+  for (int i = tid; i < (int)arows * (NT / 2); i += WAVES * 64) {
+    const int t = i / (NT / 2), n = 2 * (i % (NT / 2));
+    float lo = 0.f, hi = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const float* x = sums + (w * TOK + t) * PITCH + n;
+      lo += x[0];
+      hi += x[1];
+    }
+    const uint32_t d = layer::pack_bf16(lo, hi);
+    uint16_t* const dst = p.out + (m0 + t) * p.ldo + n0 + n;
+    if (p.wide_out && n0 + n + 1 < p.N) {
+      *reinterpret_cast<uint32_t*>(dst) = d;
+    } else {
+      if (n0 + n < p.N) dst[0] = (uint16_t)d;
+      if (n0 + n + 1 < p.N) dst[1] = (uint16_t)(d >> 16);
+    }
+  }
+}
+
+template <int RT, int MT, int WAVES, int NST>
+__global__ __launch_bounds__(WAVES * 64)
+void fp8_gemm_stream_kernel(Fp8GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[stream_lds_bytes<RT, MT, WAVES, NST>()];
+  gemm_stream<RT, MT, WAVES, NST>(p, lds);
+}
+
+template <int RT, int MT, int WAVES, int NST>
+hipError_t launch_stream(const Fp8GemmArgs& p, hipStream_t stream) {
+  const int64_t nt = (p.N + 16 * RT - 1) / (16 * RT), mt = (p.M + 16 * MT - 1) / (16 * MT);
+  if (nt > 0x7FFFFFFF || mt > 65535) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((fp8_gemm_stream_kernel<RT, MT, WAVES, NST>), dim3((unsigned)nt, (unsigned)mt), dim3(WAVES * 64), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <int TN, int TM, int WN, int WM, int NST>
+hipError_t launch_tile(const Fp8GemmArgs& p, hipStream_t stream) {
+  const int64_t total = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
+  const int64_t blocks = (total + 7) / 8 * 8;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TN, TM, WN, WM, NST>), dim3((unsigned)blocks), dim3(WN * WM * 64), 0, stream, p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& p, hipStream_t stream) {
-  const int64_t total = ((p.M + 127) / 128) * ((p.N + 127) / 128);
-  const int64_t blocks = (total + 7) / 8 * 8;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<128, 128, 2, 2, 2>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
-  return hipGetLastError();
+  if (p.M <= 16) return p.N >= 6144 ? launch_stream<2, 1, 8, 3>(p, stream) : launch_stream<1, 1, 4, 4>(p, stream);
+  if (p.M <= 32) return p.N >= 6144 ? launch_stream<2, 2, 8, 2>(p, stream) : launch_stream<1, 2, 4, 3>(p, stream);
+  if (p.M <= 64) return p.N >= 6144 ? launch_stream<2, 4, 4, 3>(p, stream) : launch_stream<1, 4, 4, 3>(p, stream);
+  if (p.M <= 128) return launch_stream<4, 4, 4, 2>(p, stream);
+  if (p.M <= 1024) return launch_tile<64, 64, 2, 2, 4>(p, stream);
+  return launch_tile<256, 256, 2, 4, 2>(p, stream);
 }
 
 }  // namespace iqp

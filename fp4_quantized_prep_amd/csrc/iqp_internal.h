@@ -269,11 +269,21 @@ struct AttnArgs {
   int32_t window;           // 0: none
   float scale_log2;         // softmax scale * log2(e)
   uint8_t* workspace;       // attention_workspace_bytes(D)
-  int64_t max_rows;         // set by the launcher: the decode kernel leaves out sequences of more
-                            // rows (tokens * group)
+  int64_t max_rows;         // set by the launcher: sequences of more rows (tokens * group) are the
+                            // prompt kernel's, the others the decode kernel's
 };
 // workgroups of the decode kernel: two for each of a full chip's 256 CUs
 constexpr int ATTN_WORKGROUPS = 512;
+// A batch of at most ATTN_DECODE_TOKENS tokens a sequence on average goes to the
+// decode kernel alone; otherwise its sequences of more than ATTN_DECODE_ROWS
+// rows go to the prompt kernel.
+constexpr int ATTN_DECODE_TOKENS = 4;
+constexpr int ATTN_DECODE_ROWS = 64;
+int64_t attention_decode_workspace_bytes(int D);
+int64_t attention_prefill_workspace_bytes(int D);
+hipError_t launch_attention_decode(const AttnArgs& args, int D, hipStream_t stream);
+hipError_t launch_attention_prefill(const AttnArgs& args, int D, hipStream_t stream);
+// both kernels' workspace is the same memory: their launches follow one another
 int64_t attention_workspace_bytes(int D);
 hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream);
 
