@@ -40,67 +40,124 @@ constexpr int DWAVES = 4;
 
 // What a workgroup needs of a sequence.
 struct Seq {
-  int64_t begin;      // its first row in the batch
-  int64_t n;          // its rows (tokens)
-  int64_t len;        // tokens held, those rows included
-  int64_t lo;         // first token that any of its rows sees
-  int64_t unit0;      // the unit of lo
-  int64_t units;      // units up to len
-  int64_t tiles;      // row tiles
+  SeqRows r;
+  int lo;             // first token that any of its rows sees
+  int unit0, units;   // the unit of lo; units up to its end
+  int tiles;          // row tiles
   int64_t work;       // tiles * Hk * units
 };
 
 template <int ROWS>
-__device__ __forceinline__ Seq get_seq(const AttnArgs& p, int s) {
+__device__ __forceinline__ Seq get_seq(const AttnArgs& p, const SeqRows& r) {
   Seq q;
-  q.begin = seq_begin(p.seq, s);
-  q.n = seq_begin(p.seq, s + 1) - q.begin;
-  q.len = p.seq.lens[s];
-  const int64_t held = (int64_t)p.seq.max_blocks << p.seq.log_block;
-  const int64_t rows = q.n * p.group;
-  q.lo = 0;
-  if (p.window > 0) {
-    q.lo = q.len - q.n - p.window + 1;
-    if (q.lo < 0) q.lo = 0;
-  }
-  const int64_t end = q.len < held ? q.len : held;
+  q.r = r;
+  const int64_t n = r.end - r.begin, rows = n * p.group, held = (int64_t)p.seq.max_blocks << p.seq.log_block;
+  const int64_t lo = p.window > 0 ? r.len - n - p.window + 1 : 0, end = r.len < held ? r.len : held;
+  q.lo = lo < 0 ? 0 : (int)lo;
   q.unit0 = q.lo / UNIT;
-  q.units = end > q.lo ? (end + UNIT - 1) / UNIT - q.unit0 : 0;
-  q.tiles = q.n > 0 && rows <= p.max_rows ? (rows + ROWS - 1) / ROWS : 0;
+  q.units = end > q.lo ? (int)((end + UNIT - 1) / UNIT) - q.unit0 : 0;
+  q.tiles = n > 0 && rows <= p.max_rows ? (int)((rows + ROWS - 1) / ROWS) : 0;
   if (q.tiles > 0 && q.units < 1) q.units = 1;    // rows that see nothing still get their zeros
-  q.work = q.tiles * p.Hk * q.units;
+  q.work = (int64_t)q.tiles * p.Hk * q.units;
   return q;
 }
 
-// total work, and the sequence and offset that unit `at` falls in (s = S: past
-// the end). Every wave computes it for itself, 64 sequences at a time.
-template <int ROWS>
-__device__ __forceinline__ int64_t locate(const AttnArgs& p, int64_t at, int& s_out, int64_t& base_out) {
+// the running sum of w over the lanes, and its total; in 32 bits where that holds it
+__device__ __forceinline__ int64_t scan(int64_t w, int64_t& total) {
   const int lane = threadIdx.x & 63;
-  int64_t total = 0;
-  s_out = p.seq.S;
-  base_out = 0;
-  for (int s0 = 0; s0 < p.seq.S; s0 += 64) {
-    const int64_t w = s0 + lane < p.seq.S ? get_seq<ROWS>(p, s0 + lane).work : 0;
-    int64_t sum = w;
+  if (__ballot(w >= (1 << 24)) == 0) {
+    int v = (int)w;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_up((long long)sum, d);
-      if (lane >= d) sum += o;
+      const int o = __shfl_up(v, d);
+      if (lane >= d) v += o;
     }
-    const uint64_t past = __ballot(total + sum > at && w > 0);
-    if (past != 0 && s_out == p.seq.S) {
-      const int f = __ffsll((unsigned long long)past) - 1;
-      s_out = s0 + f;
-      base_out = total + __shfl((long long)(sum - w), f);
-    }
-    total += __shfl((long long)sum, 63);
+    total = __builtin_amdgcn_readlane(v, 63);
+    return v;
   }
-  return total;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up((long long)w, d);
+    if (lane >= d) w += o;
+  }
+  total = __shfl((long long)w, 63);
+  return w;
 }
 
-__device__ __forceinline__ int64_t piece_of(const AttnArgs& p, int64_t total) {
-  const int64_t per = (total + ATTN_WORKGROUPS - 1) / ATTN_WORKGROUPS;
+// a / b of uniform values, a >= 0, b > 0
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The line of all units, sequence after sequence; within one, row tile by row
+// tile, key head by key head. Every wave walks it for itself.
+template <int ROWS>
+struct Line {
+  const AttnArgs& p;
+  SeqRows rows64;          // 64 sequences at hand, one a lane
+  int64_t sum;             // their units up to the lane's sequence
+  int chunk = 0, in_chunk = 0;
+  int64_t total = 0;       // units of the whole line
+  int64_t base = 0;        // units before sequence q
+  Seq q;
+
+  __device__ __forceinline__ explicit Line(const AttnArgs& p_) : p(p_) {
+    rows64 = lane_sequence(p.seq, 0);    // kept: most batches have no more
+    sum = scan(get_seq<ROWS>(p, rows64).work, total);
+    for (int s0 = 64; s0 < p.seq.S; s0 += 64) {
+      int64_t t;
+      scan(get_seq<ROWS>(p, lane_sequence(p.seq, s0)).work, t);
+      total += t;
+    }
+  }
+  // to the sequence that holds unit at (< total); once
+  __device__ __forceinline__ void seek(int64_t at) {
+    uint64_t past = __ballot(sum > at);
+    while (past == 0) {
+      base += __shfl((long long)sum, 63);
+      chunk += 64;
+      rows64 = lane_sequence(p.seq, chunk);
+      int64_t t;
+      sum = scan(get_seq<ROWS>(p, rows64).work, t);
+      past = __ballot(base + sum > at);
+    }
+    in_chunk = __ffsll((unsigned long long)past) - 1;
+    q = get_seq<ROWS>(p, sequence_of_lane(rows64, in_chunk));
+    base += __shfl((long long)sum, in_chunk) - q.work;
+  }
+  // to the sequence that owns row tile slot `item` (as find_sequence finds it); once
+  __device__ __forceinline__ void seek_item(int64_t item) {
+    constexpr int SHIFT = ROWS == 16 ? 4 : 5;
+    int64_t before = 0;
+    for (int s0 = 0;; s0 += 64) {
+      const int n = __popcll(__ballot(rows64.s < p.seq.S && item_key(rows64, p.group, SHIFT, 1) <= item));
+      if (n > 0) {
+        q = get_seq<ROWS>(p, sequence_of_lane(rows64, n - 1));
+        base = before + __shfl((long long)sum, n - 1) - q.work;
+      }
+      if (n < 64 || s0 + 64 >= p.seq.S) break;
+      int64_t t;
+      before += __shfl((long long)sum, 63);
+      rows64 = lane_sequence(p.seq, s0 + 64);
+      sum = scan(get_seq<ROWS>(p, rows64).work, t);
+    }
+  }
+  // on to the sequence that holds unit at (< total) from one at or before it
+  __device__ __forceinline__ void advance(int64_t at) {
+    while (at >= base + q.work) {
+      base += q.work;
+      if (++in_chunk == 64) {
+        in_chunk = 0;
+        chunk += 64;
+        rows64 = lane_sequence(p.seq, chunk);
+      }
+      q = get_seq<ROWS>(p, sequence_of_lane(rows64, in_chunk));
+    }
+  }
+};
+
+__device__ __forceinline__ int64_t piece_of(int64_t total) {
+  const int64_t per = (total + ATTN_WORKGROUPS - 1) / ATTN_WORKGROUPS;   // (a shift)
   return per < DWAVES ? DWAVES : per;     // at least a unit a wave
 }
 
@@ -112,7 +169,7 @@ struct Partial {
 };
 
 template <int D, int NT>
-__global__ __launch_bounds__(DWAVES * 64)
+__global__ __launch_bounds__(DWAVES * 64, D == 128 && NT == 2 ? 1 : 2)
 void attention_decode_kernel(AttnArgs p) {
   constexpr int ROWS = 16 * NT;
   constexpr int KP = D / 64;        // 64-dim groups: two MFMA steps each
@@ -125,30 +182,25 @@ void attention_decode_kernel(AttnArgs p) {
   const int col = lane & 15, g = lane >> 4;
   const int kg = col >> 2;          // 16-token group of the lane's key rows
 
-  int s;
-  int64_t base;
-  // (the total does not depend on the position asked for)
-  int s_first;
-  int64_t base_first;
-  const int64_t total = locate<ROWS>(p, 0, s_first, base_first);
-  const int64_t per = piece_of(p, total);
+  Line<ROWS> line(p);
+  const int64_t per = piece_of(line.total);
   int64_t at = (int64_t)blockIdx.x * per;
-  const int64_t stop = at + per < total ? at + per : total;
+  const int64_t stop = at + per < line.total ? at + per : line.total;
   if (at >= stop) return;
-  locate<ROWS>(p, at, s, base);
-  Seq q = get_seq<ROWS>(p, s);
+  line.seek(at);
 
   while (at < stop) {
-    while (at >= base + q.work) {   // on to the next sequence with work
-      base += q.work;
-      q = get_seq<ROWS>(p, ++s);
-    }
-    const int64_t pair = (at - base) / q.units;              // row tile and key head of the sequence
+    line.advance(at);
+    const Seq& q = line.q;
+    const int64_t base = line.base;
+    const int s = q.r.s;
+    const int64_t q_begin = q.r.begin, q_n = q.r.end - q.r.begin, q_len = q.r.len;
+    const int64_t pair = quotient(at - base, q.units);            // row tile and key head of the sequence
     const int64_t off = (at - base) - pair * q.units;
     const int64_t count = q.units - off < stop - at ? q.units - off : stop - at;
-    const int64_t tile = pair / p.Hk;
+    const int64_t tile = quotient(pair, p.Hk);
     const int head = (int)(pair - tile * p.Hk);
-    const int64_t row0 = tile * ROWS, rows = q.n * p.group;
+    const int64_t row0 = tile * ROWS, rows = q_n * p.group;
 
     // the queries, and which tokens each column sees: [see_lo, see_hi)
     v8bf fq[NT][2 * KP];
@@ -158,20 +210,20 @@ void attention_decode_kernel(AttnArgs p) {
       const int64_t r = row0 + 16 * t + col;
       const int64_t rc = r < rows ? r : rows - 1;
       const int64_t i = rc / p.group;
-      const uint16_t* src = p.q + (q.begin + i) * p.ldq + ((int64_t)head * p.group + (rc - i * p.group)) * D + 16 * g;
+      const uint16_t* src = p.q + (q_begin + i) * p.ldq + ((int64_t)head * p.group + (rc - i * p.group)) * D + 16 * g;
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
         fq[t][2 * k] = *reinterpret_cast<const v8bf*>(src + 64 * k);
         fq[t][2 * k + 1] = *reinterpret_cast<const v8bf*>(src + 64 * k + 8);
       }
-      const int64_t pos = q.len - q.n + i;
+      const int64_t pos = q_len - q_n + i;
       see_hi[t] = pos + 1;
       see_lo[t] = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
     }
     // every column sees the tokens of [all_lo, all_hi)
     const int64_t i_first = row0 / p.group, i_last = (row0 + ROWS - 1 < rows ? row0 + ROWS - 1 : rows - 1) / p.group;
-    const int64_t all_hi = q.len - q.n + i_first + 1;
-    const int64_t all_lo = p.window > 0 ? q.len - q.n + i_last + 1 - p.window : 0;
+    const int64_t all_hi = q_len - q_n + i_first + 1;
+    const int64_t all_lo = p.window > 0 ? q_len - q_n + i_last + 1 - p.window : 0;
     const int64_t tile_lo = p.window > 0 ? all_hi - p.window : 0;   // no column sees a token before this
 
     float m[NT], l[NT];
@@ -192,7 +244,7 @@ void attention_decode_kernel(AttnArgs p) {
       const int64_t bk = (t0 + 16 * kg) >> lb, bv = (t0 + 16 * g) >> lb;
       int64_t pk = bk < p.seq.max_blocks ? table[bk] : -1;
       int64_t pv = bv < p.seq.max_blocks ? table[bv] : -1;
-      const bool held = pv >= 0 && pv < p.seq.n_blocks && t0 + 16 * g < q.len;
+      const bool held = pv >= 0 && pv < p.seq.n_blocks && t0 + 16 * g < q_len;
       pk = pk >= 0 && pk < p.seq.n_blocks ? pk : 0;
       pv = pv >= 0 && pv < p.seq.n_blocks ? pv : 0;
       const int inside = (1 << lb) - 1;
@@ -228,7 +280,7 @@ void attention_decode_kernel(AttnArgs p) {
             sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, fq[t][2 * k + 1], sc[t][c], 0, 0, 0);
           }
         }
-      const bool edge = t0 < all_lo || t0 + UNIT > all_hi || t0 + UNIT > q.len;
+      const bool edge = t0 < all_lo || t0 + UNIT > all_hi || t0 + UNIT > q_len;
       // a block that is not held, or an edge: some token of the unit is out
       if (edge || __ballot(!held) != 0) {
         const int64_t tb = t0 + 16 * g;
@@ -244,7 +296,7 @@ void attention_decode_kernel(AttnArgs p) {
             }
         // whatever lies behind the sequence, before every row's window or in a
         // block that is not held must not reach the product: 0 * NaN
-        const int64_t vhi = held ? q.len - tb : 0, vlo = tile_lo - tb;
+        const int64_t vhi = held ? q_len - tb : 0, vlo = tile_lo - tb;
         const int hi = vhi > 16 ? 16 : (int)vhi, lo = vlo > 16 ? 16 : (int)vlo;
 #pragma unroll
         for (int d = 0; d < DT; ++d) vr[d] = clear_outside(vr[d], lo, hi);
@@ -339,8 +391,7 @@ void attention_decode_kernel(AttnArgs p) {
       }
       if (whole) {
         const float inv = inverse_sum(sum);
-        const int64_t tok = (row0 + r) / p.group;
-        uint16_t* dst = p.out + (q.begin + tok) * p.ldo + ((int64_t)head * p.group + (row0 + r - tok * p.group)) * D + d;
+        uint16_t* dst = p.out + row_offset(q_begin, row0 + r, head, p.group, D, p.ldo) + d;
         *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
       } else {
         *reinterpret_cast<v4f*>(&part->o[r][d]) = acc;
@@ -355,67 +406,139 @@ void attention_decode_kernel(AttnArgs p) {
   }
 }
 
-// Joins the pairs whose units went to more than one workgroup. A workgroup per
-// item = row tile (in the numbering of find_sequence) and key head.
+// Joins the pairs whose units went to more than one workgroup. Workgroup (x, z)
+// takes every gridDim.y-th row from z on of one pair: the pair that decode
+// workgroup x began and did not finish, or (BY_PAIR, where the pairs are fewer
+// than the decode workgroups) pair x itself. A group of D / 4 lanes sums up
+// partial results of a row: all of them where they are few (every group then
+// has a row of its own), else every JOIN-th, and the groups meet in LDS.
+constexpr int JOIN_THREADS = 256;
+
+// partial results first, first + step, ... <= w1 of row r, dims d .. d + 3;
+// AHEAD at a time, all loaded before the first is used
 template <int D, int NT>
-__global__ __launch_bounds__(256)
-void attention_join_kernel(AttnArgs p) {
-  constexpr int ROWS = 16 * NT;
-  const int tid = threadIdx.x;
-  int s_first;
-  int64_t base_first;
-  const int64_t total = locate<ROWS>(p, 0, s_first, base_first);
-  const int64_t per = piece_of(p, total);
-  const int64_t pair_item = blockIdx.x;                      // row tile slot
-  const int s = find_sequence(p.seq, pair_item, p.group, NT == 1 ? 4 : 5, 1);
-  const int64_t tile = pair_item - item_key(p.seq, s, p.group, NT == 1 ? 4 : 5, 1);
-  const Seq q = get_seq<ROWS>(p, s);
-  if (tile >= q.tiles) return;
-  // where the sequence's work begins
-  int64_t base = 0;
-  const int lane = tid & 63;
-  for (int s0 = 0; s0 < s; s0 += 64) {
-    int64_t w = s0 + lane < s ? get_seq<ROWS>(p, s0 + lane).work : 0;
+__device__ __forceinline__ void sum_partials(const Partial<D, NT>* parts, int64_t first, int64_t step, int64_t w0, int64_t w1,
+                                             int r, int d, float& mx, float& sum, v4f& acc) {
+  constexpr int AHEAD = 8;
+  mx = LOWEST;
+  sum = 0.f;
+  acc = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int64_t w = first; w <= w1; w += AHEAD * step) {
+    float m[AHEAD], l[AHEAD];
+    v4f v[AHEAD];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) w += __shfl_xor((long long)w, d);
-    base += w;
-  }
-  const int head = blockIdx.y;
-  const int64_t u0 = base + (tile * p.Hk + head) * q.units, u1 = u0 + q.units;
-  const int64_t w0 = u0 / per, w1 = (u1 - 1) / per;
-  if (w0 == w1) return;                                      // finished by its workgroup
-  const int64_t row0 = tile * ROWS, rows = q.n * p.group;
-  const Partial<D, NT>* parts = reinterpret_cast<const Partial<D, NT>*>(p.workspace);
-  for (int i = tid; i < ROWS * (D / 4); i += 256) {
-    const int r = i / (D / 4), d = 4 * (i % (D / 4));
-    if (row0 + r >= rows) break;
-    float mx = LOWEST;
-    for (int64_t w = w0; w <= w1; ++w) mx = fmaxf(mx, parts[2 * w + (w == w0 ? 1 : 0)].m[r]);
-    float sum = 0.f;
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t w = w0; w <= w1; ++w) {
-      const Partial<D, NT>& x = parts[2 * w + (w == w0 ? 1 : 0)];
-      const float a = __builtin_amdgcn_exp2f(x.m[r] - mx);
-      sum += x.l[r] * a;
-      const v4f v = *reinterpret_cast<const v4f*>(&x.o[r][d]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += v[j] * a;
+    for (int i = 0; i < AHEAD; ++i) {
+      m[i] = LOWEST;
+      l[i] = 0.f;
+      v[i] = v4f{0.f, 0.f, 0.f, 0.f};
+      const int64_t x = w + i * step;
+      if (x <= w1) {
+        const Partial<D, NT>& part = parts[2 * x + (x == w0 ? 1 : 0)];
+        m[i] = part.m[r];
+        l[i] = part.l[r];
+        v[i] = *reinterpret_cast<const v4f*>(&part.o[r][d]);
+      }
     }
+    float mn = mx;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, m[i]);
+    const float b = __builtin_amdgcn_exp2f(mx - mn);
+    mx = mn;
+    sum *= b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] *= b;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const float a = __builtin_amdgcn_exp2f(m[i] - mn);
+      sum += l[i] * a;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += v[i][j] * a;
+    }
+  }
+}
+
+template <int D, int NT, bool BY_PAIR>
+__global__ __launch_bounds__(JOIN_THREADS)
+void attention_join_kernel(AttnArgs p) {
+  constexpr int ROWS = 16 * NT, LANES = D / 4, JOIN = JOIN_THREADS / LANES;
+  __shared__ float lds_m[JOIN], lds_l[JOIN];
+  __shared__ __attribute__((aligned(16))) float lds_o[JOIN][D];
+  const int tid = threadIdx.x;
+  Line<ROWS> line(p);
+  const int64_t per = piece_of(line.total);
+  const Seq& q = line.q;
+  int64_t pair;                                              // of the sequence
+  if constexpr (BY_PAIR) {
+    const int64_t item = blockIdx.x / (unsigned)p.Hk;
+    line.seek_item(item);
+    const int64_t tile = item - item_key(q.r, p.group, NT == 1 ? 4 : 5, 1);
+    if (tile >= q.tiles) return;
+    pair = tile * p.Hk + blockIdx.x % (unsigned)p.Hk;
+  } else {
+    const int64_t last = (blockIdx.x + (int64_t)1) * per - 1;   // the workgroup's last unit
+    if (last >= line.total) return;
+    line.seek(last);
+    pair = quotient(last - line.base, q.units);
+  }
+  const int64_t u0 = line.base + pair * q.units, w0 = quotient(u0, per), w1 = quotient(u0 + q.units - 1, per);
+  if (w0 == w1 || (!BY_PAIR && w0 != blockIdx.x)) return;    // finished by its workgroup, or begun before this one
+  const int64_t tile = quotient(pair, p.Hk), rows = (int64_t)(q.r.end - q.r.begin) * p.group;
+  const int head = (int)(pair - tile * p.Hk);
+  const Partial<D, NT>* parts = reinterpret_cast<const Partial<D, NT>*>(p.workspace);
+  const int g = tid / LANES, d = 4 * (tid % LANES);
+  float mx, sum;
+  v4f acc;
+  auto finish = [&](int r) __attribute__((always_inline)) {
     const float inv = inverse_sum(sum);
-    const int64_t tok = (row0 + r) / p.group;
-    uint16_t* dst = p.out + (q.begin + tok) * p.ldo + ((int64_t)head * p.group + (row0 + r - tok * p.group)) * D + d;
+    uint16_t* dst = p.out + row_offset(q.r.begin, tile * ROWS + r, head, p.group, D, p.ldo) + d;
     *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+  };
+  if (w1 - w0 < 8) {
+    for (int r = blockIdx.y + gridDim.y * g; r < ROWS && tile * ROWS + r < rows; r += gridDim.y * JOIN) {
+      sum_partials<D, NT>(parts, w0, 1, w0, w1, r, d, mx, sum, acc);
+      finish(r);
+    }
+    return;
+  }
+  for (int r = blockIdx.y; r < ROWS && tile * ROWS + r < rows; r += gridDim.y) {
+    sum_partials<D, NT>(parts, w0 + g, JOIN, w0, w1, r, d, mx, sum, acc);
+    if (d == 0) {
+      lds_m[g] = mx;
+      lds_l[g] = sum;
+    }
+    *reinterpret_cast<v4f*>(&lds_o[g][d]) = acc;
+    __syncthreads();
+    if (g == 0) {
+      mx = lds_m[0];
+#pragma unroll
+      for (int i = 1; i < JOIN; ++i) mx = fmaxf(mx, lds_m[i]);
+      sum = 0.f;
+      acc = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < JOIN; ++i) {
+        const float a = __builtin_amdgcn_exp2f(lds_m[i] - mx);
+        sum += lds_l[i] * a;
+        const v4f v = *reinterpret_cast<const v4f*>(&lds_o[i][d]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += v[j] * a;
+      }
+      finish(r);
+    }
+    __syncthreads();
   }
 }
 
 template <int D, int NT>
 hipError_t launch(const AttnArgs& p, hipStream_t stream) {
-  const int64_t tiles = ((p.seq.T * p.group) >> (NT == 1 ? 4 : 5)) + p.seq.S;   // row tiles, at most
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((attention_decode_kernel<D, NT>), dim3(ATTN_WORKGROUPS), dim3(DWAVES * 64), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attention_join_kernel<D, NT>), dim3((unsigned)tiles, (unsigned)p.Hk), dim3(256), 0, stream, p);
+  const int64_t pairs = (((p.seq.T * p.group) >> (NT == 1 ? 4 : 5)) + p.seq.S) * p.Hk;   // at most
+  if (pairs <= ATTN_WORKGROUPS / 4)
+    // each may be in many pieces (8 heads of 131072 tokens: 64 each): a workgroup a row
+    hipLaunchKernelGGL((attention_join_kernel<D, NT, true>), dim3((unsigned)pairs, 16 * NT), dim3(JOIN_THREADS), 0, stream, p);
+  else
+    hipLaunchKernelGGL((attention_join_kernel<D, NT, false>), dim3(ATTN_WORKGROUPS, 2), dim3(JOIN_THREADS), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -49,14 +49,15 @@ struct Work {
 
 // Row tile `item` (numbering of find_sequence with 2^7 rows): false where there is none
 __device__ __forceinline__ bool find_work(const AttnArgs& p, int64_t item, Work& w) {
-  w.s = find_sequence(p.seq, item, p.group, 7, 1);
-  w.begin = seq_begin(p.seq, w.s);
-  w.n = seq_begin(p.seq, w.s + 1) - w.begin;
-  w.len = p.seq.lens[w.s];
+  const SeqRows q = find_sequence(p.seq, item, p.group, 7, 1);
+  w.s = q.s;
+  w.begin = q.begin;
+  w.n = q.end - q.begin;
+  w.len = q.len;
   w.rows = w.n * p.group;
   if (w.n <= 0 || w.rows <= p.max_rows) return false;
   const int64_t tiles = (w.rows + PROWS - 1) / PROWS;
-  const int64_t tile = item - item_key(p.seq, w.s, p.group, 7, 1);
+  const int64_t tile = item - item_key(q, p.group, 7, 1);
   if (tile >= tiles) return false;
   w.row0 = (tiles - 1 - tile) * PROWS;     // the longest first
   const int64_t last = w.row0 + PROWS < w.rows ? w.row0 + PROWS - 1 : w.rows - 1;
@@ -94,8 +95,9 @@ struct Prefill {
   };
   // a unit's granules: lane's granule is lane % 4
   struct Granules {
-    int blk;                // block number as the table has it (-1: past the table)
-    float kmul, ve, vinv;   // scale * 2^ke * log2 e, value exponent, 2^-ve
+    int blk;      // block number as the table has it (-1: past the table)
+    int ks, vs;   // its scale bytes, turned into factors where they are used: a unit after their
+                  // load, so that nothing waits for the codes loaded behind them
   };
 
   static __device__ __forceinline__ void run(const AttnArgs& p, int splits, uint8_t* lds) {
@@ -144,10 +146,8 @@ struct Prefill {
       Granules g;
       g.blk = blk;
       const int64_t at = (int64_t)(held_block(blk) ? blk : 0) * p.Hk + head;
-      const int ke = (int)p.k_scales[at] - 127, ve = (int)p.v_scales[at] - 127;
-      g.kmul = p.scale_log2 * pow2(min(max(ke, -126), 127));
-      g.ve = (float)ve;
-      g.vinv = pow2(min(max(-ve, -126), 127));
+      g.ks = p.k_scales[at];
+      g.vs = p.v_scales[at];
       return g;
     };
     // the thread's codes of unit u, whose blocks are in blk
@@ -218,9 +218,9 @@ struct Prefill {
         Codes next;
         const int blk1 = blk_next;
         if (u + 1 < units) {
-          next = load_codes(u + 1, blk1);
-          gn = load_granules(blk1);
           blk_next = load_block(u + 2);
+          gn = load_granules(blk1);
+          next = load_codes(u + 1, blk1);
         }
         const int t0 = u * UNIT;
         if (!idle && t0 < any_hi && t0 + UNIT > any_lo) {
@@ -243,9 +243,10 @@ struct Prefill {
           bool in[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            kmul[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g.kmul), i));
-            ve[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g.ve), i));
-            vinv[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g.vinv), i));
+            const int kb = __builtin_amdgcn_readlane(g.ks, i), vb = __builtin_amdgcn_readlane(g.vs, i);
+            kmul[i] = p.scale_log2 * pow2(max(kb - 127, -126));
+            ve[i] = (float)(vb - 127);
+            vinv[i] = pow2(min(127 - vb, 127));
             in[i] = held_block(__builtin_amdgcn_readlane(g.blk, i));
           }
           if (t0 + UNIT > all_hi || t0 < all_lo || !(in[0] && in[1] && in[2] && in[3])) {

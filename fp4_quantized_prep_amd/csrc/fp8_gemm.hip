@@ -4,43 +4,86 @@
 //   out[m, n] = sum_j 2^(ea(m, j) + ew(n / 128, j)) sum_{k in block j} A[m, k] W[n, k]
 // summed in float32 by the matrix cores, which apply the scales themselves,
 // and rounded to bf16 once.
+#include <type_traits>
+
 #include "iq_common.h"
 #include "layer_common.h"
 
 namespace iqp {
 namespace {
 
+constexpr int ROT = 32, ROT_STEP = 5;
 constexpr int SLAB = 1024;   // bytes of one wave-wide copy to LDS
 
 constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
-// Tile kernel: a workgroup computes TN weight rows x TM tokens with WN x WM
-// waves, all K blocks. Per 128-deep block both operand tiles and the tokens'
-// scale words are copied global -> LDS (8 whole rows of 128 bytes a copy, the
-// 16-byte chunks of LDS row r permuted by (r / 2) % 8 so that the operand reads
-// meet distinct banks), NST blocks in LDS. The product is computed transposed,
-// weight rows as the MFMA's rows; weight row n of a 32-row tile sits in LDS
-// row 8 ((n / 4) % 4) + 4 (n / 16) + n % 4 of it, so that a lane's sixteen
-// accumulators are sixteen consecutive n of one token: 32 bytes of output.
-template <int TN, int TM, int NST>
-constexpr int tile_lds_bytes() { return NST * (TN * KB + TM * KB + TM * 4); }
+// A wave's AN x AM accumulator tiles to bf16 rows: weight rows from n0 on,
+// tokens from m0 on, the lane's sixteen values of a tile consecutive.
+template <int AN, int AM>
+__device__ __forceinline__ void store_tile(const Fp8GemmArgs& p, const v16f (&acc)[AN][AM], int64_t n0, int64_t m0, int lane) {
+  const int row = lane & 31, half = lane >> 5;
+#pragma unroll
+  for (int u = 0; u < AM; ++u) {
+    const int64_t m = m0 + 32 * u + row;
+    if (m >= p.M) continue;
+#pragma unroll
+    for (int t = 0; t < AN; ++t) {
+      const int64_t n = n0 + 32 * t + 16 * half;
+      uint16_t* dst = p.out + m * p.ldo + n;
+      uint32_t d[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) d[r] = layer::pack_bf16(acc[t][u][2 * r], acc[t][u][2 * r + 1]);
+      if (p.wide_out && n + 16 <= p.N) {
+        *reinterpret_cast<v4u*>(dst) = v4u{d[0], d[1], d[2], d[3]};
+        *reinterpret_cast<v4u*>(dst + 8) = v4u{d[4], d[5], d[6], d[7]};
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (n + r < p.N) dst[r] = (uint16_t)(d[r >> 1] >> (16 * (r & 1)));
+      }
+    }
+  }
+}
 
-template <int TN, int TM, int WN, int WM, int NST>
+// Tile kernel: a workgroup computes TN weight rows x TM tokens with WK sets of
+// WN x WM waves. Set k takes the K blocks k, k + WK, ... through LDS stages of
+// its own (NST blocks of both operand tiles and the tokens' scale words), so that
+// a workgroup of few MFMAs a block needs one barrier for WK blocks; the sets'
+// sums meet in LDS at the end. Operands are copied global -> LDS, 8 whole rows
+// of 128 bytes a copy, the 16-byte chunks of LDS row r permuted by (r / 2) % 8
+// so that the operand reads meet distinct banks; copies past the last block read
+// zeros out of bounds, which keeps the wait counts constant. The product is
+// computed transposed, weight rows as the MFMA's rows; weight row n of a 32-row
+// tile sits in LDS row 8 ((n / 4) % 4) + 4 (n / 16) + n % 4 of it, so that a
+// lane's sixteen accumulators are sixteen consecutive n of one token: 32 bytes
+// of output.
+template <int TN, int TM, int WN, int WM, int WK, int NST>
+constexpr int tile_lds_bytes() {
+  constexpr int ring = WK * NST * (TN * KB + TM * KB + TM * 4), sums = (WK - 1) * TN * TM * 4;
+  return ring > sums ? ring : sums;
+}
+
+constexpr uint32_t PAST = 0x40000000u;   // an offset beyond every buffer here
+
+template <int TN, int TM, int WN, int WM, int WK, int NST>
 __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
-  constexpr int NW = WN * WM;
+  constexpr int NW = WN * WM;                           // waves of a set
   constexpr int AN = TN / 32 / WN, AM = TM / 32 / WM;   // 32x32 tiles of a wave
   constexpr int W_BYTES = TN * KB, A_BYTES = TM * KB, S_BYTES = TM * 4;
   constexpr int WC = W_BYTES / SLAB / NW, AC = A_BYTES / SLAB / NW;
-  constexpr int SC = (TM / 64 + NW - 1) / NW;           // scale-word copies of a wave (64 words each)
+  constexpr int SW = TM / 64;                           // scale-word copies of a set (64 words each)
+  constexpr int SC = (SW + NW - 1) / NW;                // of a wave (some may be made twice)
   constexpr int NCOPY = WC + AC + SC;
   static_assert(WC * NW * SLAB == W_BYTES && AC * NW * SLAB == A_BYTES, "whole slabs");
-  uint8_t* const lw = lds;
-  uint8_t* const la = lds + NST * W_BYTES;
-  uint8_t* const ls = la + NST * A_BYTES;
+  static_assert(AN <= 4 && 4 % AN == 0, "a wave's rows share their weight scales");
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int set = wave_all / NW, wave = wave_all % NW;
   const int wn = wave % WN, wm = wave / WN;
+  uint8_t* const lw = lds + set * NST * (W_BYTES + A_BYTES + S_BYTES);
+  uint8_t* const la = lw + NST * W_BYTES;
+  uint8_t* const ls = la + NST * A_BYTES;
   // one XCD (workgroup id mod 8) walks consecutive tiles, tokens first
   const int mt = (int)((p.M + TM - 1) / TM), nt = (int)((p.N + TN - 1) / TN);
   const int64_t total = (int64_t)mt * nt, per = (total + 7) / 8;
@@ -69,29 +112,41 @@ __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
     va[i] = (uint32_t)(r * (int)p.lda + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
   }
 #pragma unroll
-  for (int i = 0; i < SC; ++i) vs[i] = (uint32_t)(4 * (64 * ((wave + NW * i) % (TM / 64)) + lane) * (int)p.as_sm);
+  for (int i = 0; i < SC; ++i) vs[i] = (uint32_t)(4 * (64 * ((wave + NW * i) % SW) + lane) * (int)p.as_sm);
 
-  auto copy = [&](int j) __attribute__((always_inline)) {
-    const int st = j % NST;
-    const uint32_t u = (uint32_t)(KB * j);
-#pragma unroll
-    for (int i = 0; i < WC; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(lw + st * W_BYTES + SLAB * (wave + NW * i)), 16, vw[i] + u, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < AC; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(la + st * A_BYTES + SLAB * (wave + NW * i)), 16, va[i] + u, 0, 0, 0);
-    const uint32_t us = (uint32_t)(4 * (j >> 2) * (int)p.as_sw);
-#pragma unroll
-    for (int i = 0; i < SC; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(ls + st * S_BYTES + 256 * ((wave + NW * i) % (TM / 64))), 4, vs[i] + us, 0, 0, 0);
+  // the set's block i into stage i % NST
+  auto block_of = [&](int i) __attribute__((always_inline)) { return set + WK * i; };
+  // copy c (0 .. NCOPY - 1) of the set's block i into stage st
+  auto copy = [&](int i, int st, int c) __attribute__((always_inline)) {
+    const int j = block_of(i);
+    if (c < WC) {
+      const uint32_t u = j < nkb ? (uint32_t)(KB * j) : PAST;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(lw + st * W_BYTES + SLAB * (wave + NW * c)), 16, vw[c] + u, 0, 0, 0);
+    } else if (c < WC + AC) {
+      const uint32_t u = j < nkb ? (uint32_t)(KB * j) : PAST;
+      const int k = c - WC;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(la + st * A_BYTES + SLAB * (wave + NW * k)), 16, va[k] + u, 0, 0, 0);
+    } else {
+      const uint32_t u = j < nkb ? (uint32_t)(4 * (j >> 2) * (int)p.as_sw) : PAST;
+      const int k = c - WC - AC;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(ls + st * S_BYTES + 256 * ((wave + NW * k) % SW)), 4, vs[k] + u, 0, 0, 0);
+    }
   };
 
   // the weight scales of the wave's 128-row tile, 4 K blocks a lane
-  const int64_t wt = (n0 + AN * 32 * wn) / 128;
-  const uint8_t* wsc = p.w_scales + (wt < (p.N + 127) / 128 ? wt : (p.N + 127) / 128 - 1) * p.ld_ws;
+  const int64_t wt = (n0 + AN * 32 * wn) / 128, wt_last = (p.N + 127) / 128 - 1;
+  const uint8_t* wsc = p.w_scales + (wt < wt_last ? wt : wt_last) * p.ld_ws;
+  uint8_t wb[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) wb[b] = wsc[4 * lane + b < nkb ? 4 * lane + b : 0];
+#pragma unroll
+  for (int i = 0; i < NST; ++i)
+#pragma unroll
+    for (int c = 0; c < NCOPY; ++c) copy(i, i, c);
+  __builtin_amdgcn_sched_barrier(0);
   uint32_t wsc_lane = 0;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) wsc_lane |= (uint32_t)wsc[4 * lane + b < nkb ? 4 * lane + b : 0] << (8 * b);
+  for (int b = 0; b < 4; ++b) wsc_lane |= (uint32_t)wb[b] << (8 * b);
 
   v16f acc[AN][AM];
 #pragma unroll
@@ -101,76 +156,114 @@ __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
-#pragma unroll
-  for (int j = 0; j < NST - 1; ++j)
-    if (j < nkb) copy(j);
+  // Half-steps of 64: while the MFMAs of one run, the operands of the next are
+  // read. One barrier a block, between its halves: by then every wave has read
+  // all of block i, whose stage is refilled, and block i + 1 has landed (only
+  // the NST - 2 blocks after it may be in flight).
   constexpr int WAIT = waitcnt_vm((NST - 2) * NCOPY);
   const int row = lane & 31, swz = (row >> 1) & 7;
-  for (int j = 0; j < nkb; ++j) {
-    // block j has landed once only the later blocks' copies may be in flight
-    if (NST > 2 && j + NST - 2 < nkb)
-      __builtin_amdgcn_s_waitcnt(WAIT);
-    else
-      __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
-    block_barrier();   // block j landed for every wave, block j - 1 read by every wave
-    if (j + NST - 1 < nkb) copy(j + NST - 1);
-    const int st = j % NST;
-    const int ws = (int)((uint32_t)__builtin_amdgcn_readlane((int)wsc_lane, j >> 2) >> (8 * (j & 3)));
+  const int count = (nkb + WK - 1) / WK;
+  v8i fw[2][AN], fa[2][AM];
+  uint32_t as_word[AM];
+  auto read_half = [&](int st, auto khc) __attribute__((always_inline)) {
+    constexpr int kh = decltype(khc)::value;
+    const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
+#pragma unroll
+    for (int t = 0; t < AM; ++t) {
+      const uint8_t* b = la + st * A_BYTES + KB * (32 * (AM * wm + t) + row);
+      fa[kh][t] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
+    }
+#pragma unroll
+    for (int t = 0; t < AN; ++t) {
+      const uint8_t* b = lw + st * W_BYTES + KB * (32 * (AN * wn + t) + row);
+      fw[kh][t] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
+    }
+  };
+  auto read_scales = [&](int st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < AM; ++t) as_word[t] = *reinterpret_cast<const uint32_t*>(ls + st * S_BYTES + 4 * (32 * (AM * wm + t) + row));
+  };
+  using H0 = std::integral_constant<int, 0>;
+  using H1 = std::integral_constant<int, 1>;
+  {
+    constexpr int FIRST = waitcnt_vm((NST - 1) * NCOPY);
+    __builtin_amdgcn_s_waitcnt(FIRST);
+  }
+  block_barrier();
+  read_scales(0);
+  read_half(0, H0{});
+  for (int i = 0; i < count; ++i) {
+    const int st = i % NST, j = block_of(i);
+    const int ws = (int)((uint32_t)__builtin_amdgcn_readlane((int)wsc_lane, (j >> 2) & 63) >> (8 * (j & 3)));
     int as[AM];
 #pragma unroll
-    for (int t = 0; t < AM; ++t)
-      as[t] = (int)(*reinterpret_cast<const uint32_t*>(ls + st * S_BYTES + 4 * (32 * (AM * wm + t) + row)) >> (8 * (j & 3)));
+    for (int t = 0; t < AM; ++t) as[t] = (int)(as_word[t] >> (8 * (j & 3)));
+    read_half(st, H1{});
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int kh = 0; kh < 2; ++kh) {
-      const int c0 = 4 * kh + 2 * half;
-      v8i fw[AN], fa[AM];
+    for (int t = 0; t < AN; ++t)
 #pragma unroll
-      for (int t = 0; t < AN; ++t) {
-        const uint8_t* b = lw + st * W_BYTES + KB * (32 * (AN * wn + t) + row);
-        fw[t] = make_v8i(*reinterpret_cast<const v4u*>(b + 16 * (c0 ^ swz)), *reinterpret_cast<const v4u*>(b + 16 * ((c0 + 1) ^ swz)));
+      for (int u = 0; u < AM; ++u)
+        acc[t][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[0][t], fa[0][u], acc[t][u], 0, 0, 0, ws, 0, as[u]);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
+    __builtin_amdgcn_s_waitcnt(WAIT);
+    block_barrier();
+    const int st1 = st + 1 < NST ? st + 1 : 0;
+    read_scales(st1);
+    read_half(st1, H0{});
+    __builtin_amdgcn_sched_barrier(0);
+    // the copies one by one between the MFMAs: issued together they would hold
+    // the wave until the address unit has taken them all
+#pragma unroll
+    for (int t = 0; t < AN; ++t)
+#pragma unroll
+      for (int u = 0; u < AM; ++u) {
+        acc[t][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[1][t], fa[1][u], acc[t][u], 0, 0, 0, ws, 0, as[u]);
+#pragma unroll
+        for (int c = NCOPY * (t * AM + u) / (AN * AM); c < NCOPY * (t * AM + u + 1) / (AN * AM); ++c) copy(i + NST, st, c);
+        __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int t = 0; t < AM; ++t) {
-        const uint8_t* b = la + st * A_BYTES + KB * (32 * (AM * wm + t) + row);
-        fa[t] = make_v8i(*reinterpret_cast<const v4u*>(b + 16 * (c0 ^ swz)), *reinterpret_cast<const v4u*>(b + 16 * ((c0 + 1) ^ swz)));
-      }
+  }
+
+  if constexpr (WK > 1) {
+    // the other sets' sums, in the ring's place, in the accumulators' order
+    __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
+    __syncthreads();
+    float* const sums = reinterpret_cast<float*>(lds) + (int64_t)wave * (AN * AM * 1024) + 4 * lane;
+    if (set > 0) {
 #pragma unroll
       for (int t = 0; t < AN; ++t)
 #pragma unroll
         for (int u = 0; u < AM; ++u)
-          acc[t][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[t], fa[u], acc[t][u], 0, 0, 0, ws, 0, as[u]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            *reinterpret_cast<v4f*>(sums + (set - 1) * (TN * TM) + ((t * AM + u) * 4 + r) * 256) =
+                v4f{acc[t][u][4 * r], acc[t][u][4 * r + 1], acc[t][u][4 * r + 2], acc[t][u][4 * r + 3]};
     }
+    __syncthreads();
+    if (set > 0) return;
+#pragma unroll
+    for (int k = 0; k < WK - 1; ++k)
+#pragma unroll
+      for (int t = 0; t < AN; ++t)
+#pragma unroll
+        for (int u = 0; u < AM; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const v4f x = *reinterpret_cast<const v4f*>(sums + k * (TN * TM) + ((t * AM + u) * 4 + r) * 256);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t][u][4 * r + e] += x[e];
+          }
   }
-
-#pragma unroll
-  for (int u = 0; u < AM; ++u) {
-    const int64_t m = m0 + 32 * (AM * wm + u) + row;
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int t = 0; t < AN; ++t) {
-      const int64_t n = n0 + 32 * (AN * wn + t) + 16 * half;
-      uint16_t* dst = p.out + m * p.ldo + n;
-      uint32_t d[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) d[r] = layer::pack_bf16(acc[t][u][2 * r], acc[t][u][2 * r + 1]);
-      if (p.wide_out && n + 16 <= p.N) {
-        *reinterpret_cast<v4u*>(dst) = v4u{d[0], d[1], d[2], d[3]};
-        *reinterpret_cast<v4u*>(dst + 8) = v4u{d[4], d[5], d[6], d[7]};
-      } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (n + r < p.N) dst[r] = (uint16_t)(d[r >> 1] >> (16 * (r & 1)));
-      }
-    }
-  }
+  store_tile<AN, AM>(p, acc, n0 + 32 * AN * wn, m0 + 32 * AM * wm, lane);
 }
 
-template <int TN, int TM, int WN, int WM, int NST>
-__global__ __launch_bounds__(WN * WM * 64)
+template <int TN, int TM, int WN, int WM, int WK, int NST>
+__global__ __launch_bounds__(WN * WM * WK * 64)
 void fp8_gemm_tile_kernel(Fp8GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[tile_lds_bytes<TN, TM, NST>()];
-  gemm_tile<TN, TM, WN, WM, NST>(p, lds);
+  __shared__ __attribute__((aligned(16))) uint8_t lds[tile_lds_bytes<TN, TM, WN, WM, WK, NST>()];
+  gemm_tile<TN, TM, WN, WM, WK, NST>(p, lds);
 }
 
 // Stream kernel, for few tokens: the product is then a read of the weights. A
@@ -194,12 +287,12 @@ __device__ __forceinline__ void gemm_stream(const Fp8GemmArgs& p, uint8_t* lds) 
   constexpr int NT = 16 * RT, TOK = 16 * MT;
   constexpr int STAGE = (NT + TOK) * KB + 256;      // weights, activations, scale words
   constexpr int WC = NT / 8, AC = TOK / 8, NCOPY = WC + AC + 1;
-  constexpr uint32_t PAST = 0x40000000u;            // beyond every buffer here
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * NT;
   const int64_t m0 = (int64_t)blockIdx.y * TOK;
   const int nkb = p.nkb;
+  const int rot = (int)((blockIdx.x >> 3) * ROT_STEP % ROT) % nkb;
   const int64_t wrows = p.N - n0 < NT ? p.N - n0 : NT, arows = p.M - m0 < TOK ? p.M - m0 : TOK;
   const rsrc_t rw = make_rsrc(p.w + n0 * p.ldw, (uint64_t)wrows * p.ldw);
   const rsrc_t ra = make_rsrc(p.a + m0 * p.lda, (uint64_t)arows * p.lda);
@@ -222,8 +315,8 @@ __device__ __forceinline__ void gemm_stream(const Fp8GemmArgs& p, uint8_t* lds) 
 
   // block i of this wave into stage st
   auto copy = [&](int i, int st) __attribute__((always_inline)) {
-    const int j = wave + WAVES * i;
-    const uint32_t u = j < nkb ? (uint32_t)(KB * j) : PAST;
+    const int turn = wave + WAVES * i, j = turn + rot < nkb ? turn + rot : turn + rot - nkb;
+    const uint32_t u = turn < nkb ? (uint32_t)(KB * j) : PAST;
     uint8_t* const b = ring + st * STAGE;
 #pragma unroll
     for (int c = 0; c < WC; ++c)
@@ -231,7 +324,7 @@ __device__ __forceinline__ void gemm_stream(const Fp8GemmArgs& p, uint8_t* lds) 
 #pragma unroll
     for (int c = 0; c < AC; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + NT * KB + SLAB * c), 16, va[c] + u, 0, 0, 0);
-    const uint32_t us = j < nkb ? (uint32_t)(4 * (j >> 2) * (int)p.as_sw) : PAST;
+    const uint32_t us = turn < nkb ? (uint32_t)(4 * (j >> 2) * (int)p.as_sw) : PAST;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(b + (NT + TOK) * KB), 4, vs + us, 0, 0, 0);
   };
 
@@ -259,7 +352,7 @@ __device__ __forceinline__ void gemm_stream(const Fp8GemmArgs& p, uint8_t* lds) 
   for (int i = 0; i < count; ++i) {
     __builtin_amdgcn_s_waitcnt(WAIT);
     asm volatile("" ::: "memory");
-    const int j = wave + WAVES * i;
+    const int turn = wave + WAVES * i, j = turn + rot < nkb ? turn + rot : turn + rot - nkb;
     const uint8_t* const b = ring + st * STAGE;
     const int ws = (int)((uint32_t)__builtin_amdgcn_readlane((int)wsc_lane, j >> 2) >> (8 * (j & 3)));
     v8i fw[RT], fa[MT];
@@ -337,12 +430,12 @@ hipError_t launch_stream(const Fp8GemmArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int TN, int TM, int WN, int WM, int NST>
+template <int TN, int TM, int WN, int WM, int WK, int NST>
 hipError_t launch_tile(const Fp8GemmArgs& p, hipStream_t stream) {
   const int64_t total = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
   const int64_t blocks = (total + 7) / 8 * 8;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TN, TM, WN, WM, NST>), dim3((unsigned)blocks), dim3(WN * WM * 64), 0, stream, p);
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TN, TM, WN, WM, WK, NST>), dim3((unsigned)blocks), dim3(WN * WM * WK * 64), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -353,8 +446,8 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& p, hipStream_t stream) {
   if (p.M <= 32) return p.N >= 6144 ? launch_stream<2, 2, 8, 2>(p, stream) : launch_stream<1, 2, 4, 3>(p, stream);
   if (p.M <= 64) return p.N >= 6144 ? launch_stream<2, 4, 4, 3>(p, stream) : launch_stream<1, 4, 4, 3>(p, stream);
   if (p.M <= 128) return launch_stream<4, 4, 4, 2>(p, stream);
-  if (p.M <= 1024) return launch_tile<64, 64, 2, 2, 4>(p, stream);
-  return launch_tile<256, 256, 2, 4, 2>(p, stream);
+  if (p.M <= 1024) return launch_tile<64, 64, 2, 2, 1, 4>(p, stream);
+  return launch_tile<256, 256, 2, 4, 1, 2>(p, stream);
 }
 
 }  // namespace iqp

@@ -41,26 +41,26 @@ struct Share {
 };
 
 // Item -> sequence and block (see find_sequence: a sequence of n rows touches
-// at most floor((n - 2) / B) + 2 blocks). False where the item has no rows, or
-// the table holds no block there.
+// at most floor((n - 2) / B) + 2 blocks). False where the item has no rows. The
+// block is as the table has it: held(..) says whether the cache has it, asked
+// only after the loads that do not need it are on their way.
 __device__ __forceinline__ bool find_share(const SeqBatch& b, int64_t item, Share& out) {
-  if (b.S == 0) return false;
-  const int s = find_sequence(b, item, 1, b.log_block, 2);
-  const int64_t begin = seq_begin(b, s), end = seq_begin(b, s + 1);
-  const int64_t n = end - begin, len = b.lens[s];
-  if (n <= 0 || len <= 0) return false;
-  const int64_t first = len - n;                  // position of the first row (rows before position 0: left out)
-  const int64_t j = item - item_key(b, s, 1, b.log_block, 2);
-  const int64_t idx = (first >> b.log_block) + j;
+  const SeqRows q = find_sequence(b, item, 1, b.log_block, 2);
+  const int n = q.end - q.begin;
+  if (n <= 0 || q.len <= 0) return false;
+  const int64_t first = (int64_t)q.len - n;       // position of the first row (rows before position 0: left out)
+  const int64_t idx = (first >> b.log_block) + item - item_key(q, 1, b.log_block, 2);
   const int64_t base = idx << b.log_block;
-  if (idx < 0 || idx >= b.max_blocks || base >= len) return false;
-  out.block = b.table[(int64_t)s * b.ld_table + idx];
-  if (out.block < 0 || out.block >= b.n_blocks) return false;
+  if (idx < 0 || idx >= b.max_blocks || base >= q.len) return false;
   out.lo = first > base ? (int)(first - base) : 0;
-  out.hi = len - base < ((int64_t)1 << b.log_block) ? (int)(len - base) : 1 << b.log_block;
-  out.row = begin + (base + out.lo - first);
-  return out.lo < out.hi;
+  out.hi = q.len - base < ((int64_t)1 << b.log_block) ? (int)(q.len - base) : 1 << b.log_block;
+  if (out.lo >= out.hi) return false;
+  out.row = q.begin + (base + out.lo - first);
+  out.block = b.table[(int64_t)q.s * b.ld_table + idx];
+  return true;
 }
+
+__device__ __forceinline__ bool held(const SeqBatch& b, int64_t block) { return block >= 0 && block < b.n_blocks; }
 
 // four E4M3 codes times mul (a power of two <= 1), rounded to E4M3
 __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float mul) {
@@ -115,6 +115,7 @@ void kv_append_kernel(KvAppendArgs p) {
       x[1][i] = *reinterpret_cast<const v4u*>(p.v + (sh.row + r) * p.ldv + (int64_t)head * D + 8 * l);
     }
   }
+  if (!held(p.seq, sh.block)) return;               // uniform over the workgroup
   const int64_t slot = sh.block * p.Hk + head;
   int old[2] = {0, 0};
   if (sh.lo > 0) {
@@ -216,7 +217,7 @@ void kv_read_kernel(KvReadArgs p) {
   const int tid = threadIdx.x;
   const int head = blockIdx.y;
   Share sh;
-  if (!find_share(p.seq, blockIdx.x, sh)) return;   // uniform over the workgroup
+  if (!find_share(p.seq, blockIdx.x, sh) || !held(p.seq, sh.block)) return;   // uniform over the workgroup
   const int B = 1 << p.seq.log_block;
   const int64_t slot = sh.block * p.Hk + head;
   const uint8_t* const kb = p.k_cache + slot * B * D;

@@ -27,11 +27,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// first row of sequence s (s <= S) among the batch's T rows, kept inside them
-// whatever cu holds
-__device__ __forceinline__ int64_t seq_begin(const SeqBatch& b, int s) {
-  const int64_t v = b.cu[s];
-  return v < 0 ? 0 : (v > b.T ? b.T : v);
+// A row offset of the batch, kept inside its T rows whatever cu holds.
+__device__ __forceinline__ int clamp_row(const SeqBatch& b, int v) { return v < 0 ? 0 : (v > (int)b.T ? (int)b.T : v); }
+
+// A sequence: its rows begin .. end - 1 of the batch, and its length with them.
+struct SeqRows {
+  int s, begin, end, len;
+};
+
+// sequence s0 + lane of the batch (s = S and no rows past the last); one round
+// of loads
+__device__ __forceinline__ SeqRows lane_sequence(const SeqBatch& b, int s0) {
+  const int s = s0 + (int)(threadIdx.x & 63), c = s < b.S ? s : b.S - 1;
+  const int begin = b.cu[c], end = b.cu[c + 1], len = b.lens[c];
+  SeqRows q = {s < b.S ? s : b.S, clamp_row(b, begin), clamp_row(b, end), len};
+  if (s >= b.S) q.end = q.begin;
+  return q;
+}
+
+// lane's copy of v
+__device__ __forceinline__ SeqRows sequence_of_lane(const SeqRows& v, int lane) {
+  return {__builtin_amdgcn_readlane(v.s, lane), __builtin_amdgcn_readlane(v.begin, lane),
+          __builtin_amdgcn_readlane(v.end, lane), __builtin_amdgcn_readlane(v.len, lane)};
 }
 
 // The sequence whose range of work items holds `item`, where sequence s owns
@@ -39,23 +56,21 @@ __device__ __forceinline__ int64_t seq_begin(const SeqBatch& b, int s) {
 // key(s + 1). Since floor(a + b) >= floor(a) + floor(b), a sequence of n rows
 // owns at least floor(n mul / 2^shift) + slots items, so the grid needs only
 // the total number of rows and of sequences, and no prefix sum over the
-// sequences' own counts. Every lane of a wave gets the same answer: 64
-// sequences are looked at at once.
-__device__ __forceinline__ int64_t item_key(const SeqBatch& b, int s, int mul, int shift, int slots) {
-  return ((seq_begin(b, s) * mul) >> shift) + (int64_t)slots * s;
+// sequences' own counts. Every wave looks at 64 sequences at once and gets the
+// same answer (S >= 1).
+__device__ __forceinline__ int64_t item_key(const SeqRows& q, int mul, int shift, int slots) {
+  return (((int64_t)q.begin * mul) >> shift) + (int64_t)slots * q.s;
 }
 
-__device__ __forceinline__ int find_sequence(const SeqBatch& b, int64_t item, int mul, int shift, int slots) {
-  const int lane = threadIdx.x & 63;
-  int found = 0;
+__device__ __forceinline__ SeqRows find_sequence(const SeqBatch& b, int64_t item, int mul, int shift, int slots) {
+  SeqRows found = {0, 0, 0, 0};
   for (int s0 = 0; s0 < b.S; s0 += 64) {
-    const int s = s0 + lane;
-    const bool below = s < b.S && item_key(b, s, mul, shift, slots) <= item;
-    const int n = __popcll(__ballot(below));
-    found += n;
+    const SeqRows q = lane_sequence(b, s0);
+    const int n = __popcll(__ballot(q.s < b.S && item_key(q, mul, shift, slots) <= item));
+    if (n > 0) found = sequence_of_lane(q, n - 1);
     if (n < 64) break;
   }
-  return __builtin_amdgcn_readfirstlane(found > 0 ? found - 1 : 0);
+  return found;
 }
 
 }  // namespace layer

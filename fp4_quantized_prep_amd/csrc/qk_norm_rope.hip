@@ -40,8 +40,9 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// D values a head; PASSES groups of 64 / (D / 8) heads a wave
-template <int D, bool INTERLEAVED, int PASSES>
+// D values a head; PASSES groups of 64 / (D / 8) heads a wave; STREAM: loads
+// and stores past the caches
+template <int D, bool INTERLEAVED, int PASSES, bool STREAM>
 __global__ __launch_bounds__(NORM_WAVES * 64)
 void qk_norm_rope_kernel(QkNormRopeArgs p) {
   constexpr int LANES = D / 8;             // lanes of a head
@@ -61,9 +62,11 @@ void qk_norm_rope_kernel(QkNormRopeArgs p) {
   for (int i = 0; i < PASSES; ++i) {
     const int h = head0 + HEADS * i;
     x[i] = v4u{0u, 0u, 0u, 0u};
-    if (h < total)
-      x[i] = *reinterpret_cast<const v4u*>(h < p.Hq ? p.q + token * p.ldq + (int64_t)h * D + 8 * l
-                                                    : p.k + token * p.ldk + (int64_t)(h - p.Hq) * D + 8 * l);
+    if (h < total) {
+      const v4u* src = reinterpret_cast<const v4u*>(h < p.Hq ? p.q + token * p.ldq + (int64_t)h * D + 8 * l
+                                                             : p.k + token * p.ldk + (int64_t)(h - p.Hq) * D + 8 * l);
+      x[i] = STREAM ? __builtin_nontemporal_load(src) : *src;
+    }
   }
 
   int64_t pos = p.positions[token];
@@ -141,9 +144,14 @@ void qk_norm_rope_kernel(QkNormRopeArgs p) {
         out[j] = pack_bf16(y[2 * j] * c[2 * j] + lo * s[2 * j], y[2 * j + 1] * c[2 * j + 1] + hi * s[2 * j + 1]);
       }
     }
-    if (h < total)
-      *reinterpret_cast<v4u*>(is_q ? p.q_out + token * p.ldqo + (int64_t)h * D + 8 * l
-                                   : p.k_out + token * p.ldko + (int64_t)(h - p.Hq) * D + 8 * l) = out;
+    if (h < total) {
+      v4u* dst = reinterpret_cast<v4u*>(is_q ? p.q_out + token * p.ldqo + (int64_t)h * D + 8 * l
+                                             : p.k_out + token * p.ldko + (int64_t)(h - p.Hq) * D + 8 * l);
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(out, dst);
+      else
+        *dst = out;
+    }
   }
 }
 
@@ -151,17 +159,15 @@ template <int D, bool IL>
 hipError_t launch(const QkNormRopeArgs& p, hipStream_t stream) {
   constexpr int HEADS = 64 / (D / 8);
   const int total = p.Hq + p.Hk;
-  // one pass a wave while that still leaves CUs idle, four once every CU has
-  // several waves of four passes
-  const int64_t short_waves = p.M * ((total + HEADS - 1) / HEADS);
-  const bool four = short_waves >= (int64_t)cu_count() * 32;
-  const int per_token = four ? (total + 4 * HEADS - 1) / (4 * HEADS) : (total + HEADS - 1) / HEADS;
-  const int64_t blocks = (p.M * per_token + NORM_WAVES - 1) / NORM_WAVES;
+  // one pass a wave while that leaves fewer than 32 waves a CU, two above; past
+  // the caches what would not stay in them for its reader
+  const int64_t waves1 = p.M * ((total + HEADS - 1) / HEADS), waves2 = p.M * ((total + 2 * HEADS - 1) / (2 * HEADS));
+  const bool two = waves1 >= (int64_t)cu_count() * 32;
+  const bool past = p.M * total * D * 2 > ((int64_t)32 << 20);
+  const int64_t blocks = ((two ? waves2 : waves1) + NORM_WAVES - 1) / NORM_WAVES;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (four)
-    hipLaunchKernelGGL((qk_norm_rope_kernel<D, IL, 4>), dim3((unsigned)blocks), dim3(NORM_WAVES * 64), 0, stream, p);
-  else
-    hipLaunchKernelGGL((qk_norm_rope_kernel<D, IL, 1>), dim3((unsigned)blocks), dim3(NORM_WAVES * 64), 0, stream, p);
+  auto kern = !two ? qk_norm_rope_kernel<D, IL, 1, false> : (past ? qk_norm_rope_kernel<D, IL, 2, true> : qk_norm_rope_kernel<D, IL, 2, false>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(NORM_WAVES * 64), 0, stream, p);
   return hipGetLastError();
 }
 
