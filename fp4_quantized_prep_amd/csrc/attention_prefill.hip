@@ -23,6 +23,8 @@
 // XCD's L2 holds one head's cache, longest row tiles first. Few rows against a
 // long cache are split into Z pieces of the token range, joined by a second
 // launch.
+#include <type_traits>
+
 #include "attention_common.h"
 
 namespace iqp {
@@ -32,6 +34,7 @@ using namespace attn;
 
 constexpr int PWAVES = 4;
 constexpr int PROWS = 32 * PWAVES;     // rows of a workgroup
+constexpr float SLACK = 8.f;
 constexpr int SPLIT_GROUPS = 512;      // most workgroups of a split launch (partial results kept)
 
 template <int D>
@@ -68,6 +71,13 @@ __device__ __forceinline__ bool find_work(const AttnArgs& p, int64_t item, Work&
   return true;
 }
 
+// fmaxf of three in one instruction (the compiler would quiet each operand first)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // largest of a lane's value and its partner's (lane ^ 32)
 __device__ __forceinline__ float max_halves(float v) {
   const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -80,20 +90,24 @@ __device__ __forceinline__ float sum_halves(float v) {
 
 template <int D>
 struct Prefill {
+  static constexpr int U = UNIT, GR = U / 16;   // tokens of a unit, its granules
   static constexpr int KS = D / 16;             // MFMA steps of a score
-  static constexpr int DT = D / 32;             // output tiles
+  static constexpr int NA = U / 32;             // score tiles
   static constexpr int LOADS = D / 64;          // 16-byte pieces of keys (and of values) a thread and unit
-  static constexpr int K_BYTES = UNIT * D * 2, V_BYTES = D * UNIT * 2;
+  static constexpr int DT = D / 32;             // output tiles
+  static constexpr int K_BYTES = U * D * 2, V_BYTES = D * U * 2;
   static constexpr int LDS_BYTES = 2 * (K_BYTES + V_BYTES);
 
   // permutation of a key row's 16-byte chunks: rows of 256 bytes cover all
   // banks, rows of 128 half of them
   static __device__ __forceinline__ int key_swizzle(int tok) { return D == 128 ? tok & 15 : (tok >> 1) & 7; }
+  // and of a value row's (128 bytes: half of the banks)
+  static __device__ __forceinline__ int value_swizzle(int dim) { return (dim >> 1) & 7; }
 
   struct Codes {
     v4u k[LOADS], v[LOADS];
   };
-  // a unit's granules: lane's granule is lane % 4
+  // a unit's granules: lane's granule is lane % GR
   struct Granules {
     int blk;      // block number as the table has it (-1: past the table)
     int ks, vs;   // its scale bytes, turned into factors where they are used: a unit after their
@@ -116,32 +130,31 @@ struct Prefill {
 #pragma unroll
     for (int k = 0; k < KS; ++k) fq[k] = *reinterpret_cast<const v8bf*>(p.q + src + 16 * k + 8 * half);
     // tokens relative to the unit range's first, 32 bits wide
-    const int64_t u_lo = w.lo / UNIT, u_hi = w.hi > w.lo ? (w.hi + UNIT - 1) / UNIT : u_lo;
+    const int64_t u_lo = w.lo / U, u_hi = w.hi > w.lo ? (w.hi + U - 1) / U : u_lo;
     const int64_t u0 = u_lo + (u_hi - u_lo) * z / splits, u1 = u_lo + (u_hi - u_lo) * (z + 1) / splits;
-    const int64_t base = u0 * UNIT;
+    const int64_t base = u0 * U;
     const int units = (int)(u1 - u0);
     const int64_t pos = w.len - w.n + rc / p.group;
     const int see_hi = (int)(pos + 1 - base < -1 ? -1 : pos + 1 - base);
     const int64_t lo64 = p.window > 0 ? pos + 1 - p.window - base : -1;
     const int see_lo = (int)(lo64 < -1 ? -1 : lo64);
-    // of the wave's columns: what all of them see, and the last token any of them sees
+    // what all of the wave's columns see
     const int64_t wr0 = w.row0 + 32 * wave < w.rows ? w.row0 + 32 * wave : w.rows - 1;
     const int64_t wr1 = wr0 + 31 < w.rows ? wr0 + 31 : w.rows - 1;
     const int64_t p0 = w.len - w.n + wr0 / p.group - base, p1 = w.len - w.n + wr1 / p.group - base;
-    const int all_hi = (int)(p0 + 1 < -1 ? -1 : p0 + 1), any_hi = (int)(p1 + 1 < -1 ? -1 : p1 + 1);
-    const int64_t al = p.window > 0 ? p1 + 1 - p.window : -1, an = p.window > 0 ? p0 + 1 - p.window : -1;
-    const int all_lo = (int)(al < -1 ? -1 : al), any_lo = (int)(an < -1 ? -1 : an);
-    const bool idle = w.row0 + 32 * wave >= w.rows;      // no rows at all
+    const int all_hi = (int)(p0 + 1 < -1 ? -1 : p0 + 1);
+    const int64_t al = p.window > 0 ? p1 + 1 - p.window : -1;
+    const int all_lo = (int)(al < -1 ? -1 : al);
 
     const int32_t* const table = p.seq.table + (int64_t)w.s * p.seq.ld_table;
     const int lb = p.seq.log_block, inside = (1 << lb) - 1;
-    const int gr = lane & 3;
+    const int gr = lane & (GR - 1);
 
     auto load_block = [&](int u) __attribute__((always_inline)) {
-      const int64_t b = (base + (int64_t)u * UNIT + 16 * gr) >> lb;
+      const int64_t b = (base + (int64_t)u * U + 16 * gr) >> lb;
       return u < units && b < p.seq.max_blocks ? table[b] : -1;
     };
-    auto held_block = [&](int blk) __attribute__((always_inline)) { return blk >= 0 && blk < p.seq.n_blocks; };
+    auto held_block = [&](int blk) __attribute__((always_inline)) { return (unsigned)blk < (unsigned)p.seq.n_blocks; };
     auto load_granules = [&](int blk) __attribute__((always_inline)) {
       Granules g;
       g.blk = blk;
@@ -150,49 +163,52 @@ struct Prefill {
       g.vs = p.v_scales[at];
       return g;
     };
-    // the thread's codes of unit u, whose blocks are in blk
+    // the thread's codes of unit u, whose blocks are in blk. Keys: 16 dims of
+    // token tok + 256 i / PIECES; a wave's tokens lie in one granule, so the block
+    // is a scalar. (Units start at multiples of U: the token within its block is
+    // the sum of the unit's and the thread's.) Values: 16 tokens of a dim.
+    constexpr int PIECES = D / 16, KSTEP = 256 / PIECES, VSTEP = 256 / GR;   // rows between a thread's pieces
+    const int tok = tid / PIECES, piece = tid % PIECES, dim = tid / GR;
+    unsigned key_at[LOADS], value_at[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      key_at[i] = (unsigned)(((tok + KSTEP * i) & inside) * D + 16 * piece);
+      value_at[i] = (unsigned)(((dim + VSTEP * i) << lb) + ((16 * gr) & inside));
+    }
     auto load_codes = [&](int u, int blk) __attribute__((always_inline)) {
       Codes c;
-      const int64_t t0 = base + (int64_t)u * UNIT;
-      const int own = held_block(blk) ? blk : 0;
-      const uint8_t* vb = p.v_cache + ((((int64_t)own * p.Hk + head) * D) << lb) + ((t0 + 16 * gr) & inside);
+      const int t0 = (int)(base + (int64_t)u * U) & inside;
+      const unsigned own = held_block(blk) ? blk : 0;
+      const uint8_t* const vb = p.v_cache + ((((uint64_t)own * (unsigned)p.Hk + head) * D) << lb) + t0;
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        // keys: 16 dims of a token; a wave's tokens lie in one granule
-        constexpr int PIECES = D / 16;
-        const int x = tid + 256 * i;
-        const int tok = x / PIECES, piece = x % PIECES;
-        const int granule = (64 * wave + 256 * i) / PIECES / 16;
-        const int kb = __builtin_amdgcn_readlane(own, granule);
-        const uint8_t* ks = p.k_cache + (((int64_t)kb * p.Hk + head) << lb) * D + ((t0 + tok) & inside) * D + 16 * piece;
-        c.k[i] = *reinterpret_cast<const v4u*>(ks);
-        // values: 16 tokens of dim x / 4
-        c.v[i] = *reinterpret_cast<const v4u*>(vb + ((int64_t)(x >> 2) << lb));
+        const unsigned kb = __builtin_amdgcn_readlane(own, (64 * wave / PIECES + KSTEP * i) / 16);
+        c.k[i] = *reinterpret_cast<const v4u*>(p.k_cache + ((((uint64_t)kb * (unsigned)p.Hk + head) << lb) + t0) * D + key_at[i]);
+        c.v[i] = *reinterpret_cast<const v4u*>(vb + value_at[i]);
       }
       return c;
     };
-    auto store_codes = [&](int u, const Codes& c, bool held) __attribute__((always_inline)) {
-      uint8_t* const kl = lds + (u & 1) * (K_BYTES + V_BYTES);
-      uint8_t* const vl = kl + K_BYTES;
-      const int64_t t0 = base + (int64_t)u * UNIT + 16 * gr;
-      const int64_t hi64 = w.len - t0, lo64v = w.lo - t0;
-      const int hi = held ? (hi64 > 16 ? 16 : (int)hi64) : 0, lo = lo64v > 16 ? 16 : (int)(lo64v < 0 ? 0 : lo64v);
+    const int key_to = tok * (2 * D), value_to = K_BYTES + dim * (2 * U);
+    const int key_to0 = key_to + 16 * ((2 * piece) ^ key_swizzle(tok)), key_to1 = key_to + 16 * ((2 * piece + 1) ^ key_swizzle(tok));
+    const int value_to0 = value_to + 16 * ((2 * gr) ^ value_swizzle(dim)), value_to1 = value_to + 16 * ((2 * gr + 1) ^ value_swizzle(dim));
+    // the thread's codes of unit u to buffer BUF, widened
+    auto store_codes = [&](int u, Codes& c, int blk, auto buf) __attribute__((always_inline)) {
+      constexpr int BUF = decltype(buf)::value * (K_BYTES + V_BYTES);
+      // values behind the sequence, before the window or not held must not
+      // reach the product (0 * NaN)
+      const int64_t t0 = base + (int64_t)u * U;
+      if (t0 < w.lo || t0 + U > w.len || __ballot(!held_block(blk)) != 0) {
+        const int64_t hi64 = w.len - t0 - 16 * gr, lo64 = w.lo - t0 - 16 * gr;
+        const int hi = held_block(blk) ? (hi64 > 16 ? 16 : (int)hi64) : 0, lo = lo64 > 16 ? 16 : (int)(lo64 < 0 ? 0 : lo64);
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        constexpr int PIECES = D / 16;
-        const int x = tid + 256 * i;
-        const int tok = x / PIECES, piece = x % PIECES;
-        uint8_t* const kr = kl + tok * (2 * D);
-        *reinterpret_cast<v8bf*>(kr + 16 * ((2 * piece) ^ key_swizzle(tok))) = widen_bf16(c.k[i][0], c.k[i][1]);
-        *reinterpret_cast<v8bf*>(kr + 16 * ((2 * piece + 1) ^ key_swizzle(tok))) = widen_bf16(c.k[i][2], c.k[i][3]);
-        v4u v = c.v[i];
-        // behind the sequence, before the window or not held: must not reach
-        // the product (0 * NaN)
-        if (lo > 0 || hi < 16) v = clear_outside(v, lo, hi);
-        const int d = x >> 2;
-        uint8_t* const vr = vl + d * (2 * UNIT);
-        *reinterpret_cast<v8h*>(vr + 16 * ((2 * gr) ^ ((d >> 1) & 7))) = widen_f16(v[0], v[1]);
-        *reinterpret_cast<v8h*>(vr + 16 * ((2 * gr + 1) ^ ((d >> 1) & 7))) = widen_f16(v[2], v[3]);
+        for (int i = 0; i < LOADS; ++i) c.v[i] = clear_outside(c.v[i], lo, hi);
+      }
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {   // (KSTEP and VSTEP rows on, the swizzles are the same)
+        *reinterpret_cast<v8bf*>(lds + key_to0 + (BUF + KSTEP * i * 2 * D)) = widen_bf16(c.k[i][0], c.k[i][1]);
+        *reinterpret_cast<v8bf*>(lds + key_to1 + (BUF + KSTEP * i * 2 * D)) = widen_bf16(c.k[i][2], c.k[i][3]);
+        *reinterpret_cast<v8h*>(lds + value_to0 + (BUF + VSTEP * i * 2 * U)) = widen_f16(c.v[i][0], c.v[i][1]);
+        *reinterpret_cast<v8h*>(lds + value_to1 + (BUF + VSTEP * i * 2 * U)) = widen_f16(c.v[i][2], c.v[i][3]);
       }
     };
 
@@ -203,17 +219,139 @@ struct Prefill {
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[t][r] = 0.f;
 
-    // the key row of score row `col`, and the swizzle of the lane's operand reads
+    // the key row of score row `col`; operand reads: a lane's offsets within a
+    // buffer, everything else an immediate
     const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
+    int koff[KS], voff[GR];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) koff[k] = krow * (2 * D) + 16 * ((2 * k + half) ^ key_swizzle(krow));
+#pragma unroll
+    for (int i = 0; i < GR; ++i) voff[i] = K_BYTES + col * (2 * U) + 16 * ((2 * i + half) ^ value_swizzle(col));
+    // a unit's granules in scalar registers (so no floating-point values);
+    // granule 2 a + (r >> 3) holds score register r of tile a
+    struct Scales {
+      int kmul[GR];   // bits of scale * log2(e) * 2^(key exponent)
+      int vb[GR];     // value scale byte
+      int held;       // bit i: granule i is held
+    };
+    const int scale_bits = __builtin_amdgcn_readfirstlane(__float_as_int(p.scale_log2));
+    auto scales_of = [&](const Granules& g) __attribute__((always_inline)) {
+      Scales s;
+      s.held = 0;
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        // never 0, so that a masked score stays -inf: below 2^-100 every score is 0 to float32's last bit
+        const int e = (scale_bits >> 23) + __builtin_amdgcn_readlane(g.ks, i) - 127;
+        s.kmul[i] = (scale_bits & 0x7FFFFF) | (min(max(e, 27), 254) << 23);
+        s.vb[i] = __builtin_amdgcn_readlane(g.vs, i);
+        s.held |= held_block(__builtin_amdgcn_readlane(g.blk, i)) ? 1 << i : 0;
+      }
+      return s;
+    };
+    auto exponent_of = [&](const Scales& s, int i) __attribute__((always_inline)) { return (float)(s.vb[i] - 127); };
+    auto kmul_of = [&](const Scales& s, int i) __attribute__((always_inline)) { return __int_as_float(s.kmul[i]); };
+    auto vinv_of = [&](const Scales& s, int i) __attribute__((always_inline)) { return __int_as_float(max(254 - s.vb[i], 1) << 23); };
+
+    // unit u, whose codes are in buffer BUF of LDS
+    auto compute = [&](int u, const Scales& g, auto buf) __attribute__((always_inline)) {
+      constexpr int BUF = decltype(buf)::value * (K_BYTES + V_BYTES);
+      const int t0 = u * U;
+      // operands are read AHEAD MFMAs before their use
+      constexpr int AHEAD = 3, NQK = NA * KS, NPV = GR * DT;
+      auto key = [&](int j) __attribute__((always_inline)) {      // j = NA k + a
+        return *reinterpret_cast<const v8bf*>(lds + koff[j / NA] + (BUF + 32 * (j % NA) * 2 * D));
+      };
+      auto value = [&](int j) __attribute__((always_inline)) {    // j = DT i + t
+        return *reinterpret_cast<const v8h*>(lds + voff[j / DT] + (BUF + 32 * (j % DT) * 2 * U));
+      };
+      v16f sc[NA];
+      v8bf fk[NQK];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) fk[j] = key(j);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < NQK; ++j) {
+        const v16f zero = {};
+        sc[j % NA] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk[j], fq[j / NA], j < NA ? zero : sc[j % NA], 0, 0, 0);
+        if (j + AHEAD < NQK) fk[j + AHEAD] = key(j + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (t0 + U > all_hi || t0 < all_lo || g.held != (1 << GR) - 1) {
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int tok = t0 + 32 * a + 16 * (r >> 3) + 8 * half + (r & 7);
+            sc[a][r] = (g.held >> (2 * a + (r >> 3)) & 1) && tok >= see_lo && tok < see_hi ? sc[a][r] : -INFINITY;
+          }
+      }
+      // the maximum, granule by granule (one factor each)
+      float mx = LOWEST;
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        const v16f& x = sc[i >> 1];
+        const int r = 8 * (i & 1);
+        const float gm = max3(max3(x[r], x[r + 1], x[r + 2]), max3(x[r + 3], x[r + 4], x[r + 5]), max3(x[r + 6], x[r + 7], x[r + 7]));
+        mx = fmaxf(mx, __builtin_fmaf(gm, kmul_of(g, i), exponent_of(g, i)));
+      }
+      mx = max_halves(mx);
+      // m follows the maximum only where it rose by more than SLACK (log2):
+      // weights then stay below 2^SLACK, and what is summed is seldom rescaled
+      if (__ballot(mx > m + SLACK) != 0) {
+        const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= alpha;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[t][r] *= alpha;
+      }
+      // granule by granule: the probabilities of one beside the second product
+      // of the one before
+      v8h fp[GR], fv[NPV];
+      float km[GR], cm[GR], sum[GR] = {};
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        km[i] = kmul_of(g, i);
+        cm[i] = exponent_of(g, i) - m;
+      }
+      auto weights = [&](int i, int j) __attribute__((always_inline)) {   // scores j, j + 1 of granule i
+        const v16f& x = sc[i >> 1];
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(x[8 * (i & 1) + j], km[i], cm[i]));
+        const float z = __builtin_amdgcn_exp2f(__builtin_fmaf(x[8 * (i & 1) + j + 1], km[i], cm[i]));
+        const v2h h = {(_Float16)y, (_Float16)z};
+        sum[i] = __builtin_amdgcn_fdot2(h, v2h{1, 1}, sum[i], false);   // of the rounded weights, in float32
+        fp[i][j] = h[0];
+        fp[i][j + 1] = h[1];
+      };
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) fv[j] = value(j);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) weights(0, j);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < NPV; ++j) {
+        const int i = j / DT, t = j % DT;
+        o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fv[j], fp[i], o[t], 0, 0, 0);
+        if (j + AHEAD < NPV) fv[j + AHEAD] = value(j + AHEAD);
+        if (i + 1 < GR)
+#pragma unroll
+          for (int e = 8 * t / DT; e < 8 * (t + 1) / DT; e += 2) weights(i + 1, e);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < GR; ++i) l = __builtin_fmaf(sum[i], vinv_of(g, i), l);
+    };
+
     if (units > 0) {
       int blk = load_block(0), blk_next = load_block(1);
       Granules gn = load_granules(blk);
       {
-        const Codes c = load_codes(0, blk);
-        store_codes(0, c, held_block(blk));
+        Codes c = load_codes(0, blk);
+        store_codes(0, c, blk, std::integral_constant<int, 0>{});
       }
       __syncthreads();
-      for (int u = 0; u < units; ++u) {
+      auto unit = [&](int u, auto buf) __attribute__((always_inline)) {
         const Granules g = gn;
         Codes next;
         const int blk1 = blk_next;
@@ -222,94 +360,16 @@ struct Prefill {
           gn = load_granules(blk1);
           next = load_codes(u + 1, blk1);
         }
-        const int t0 = u * UNIT;
-        if (!idle && t0 < any_hi && t0 + UNIT > any_lo) {
-          const uint8_t* const kl = lds + (u & 1) * (K_BYTES + V_BYTES);
-          const uint8_t* const vl = kl + K_BYTES;
-          v16f sc[2];
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sc[a][r] = 0.f;
-            const uint8_t* const kr = kl + (32 * a + krow) * (2 * D);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              const v8bf fk = *reinterpret_cast<const v8bf*>(kr + 16 * ((2 * k + half) ^ key_swizzle(krow)));
-              sc[a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk, fq[k], sc[a], 0, 0, 0);
-            }
-          }
-          // granule 2 a + (r >> 3): scalars
-          float kmul[4], ve[4], vinv[4];
-          bool in[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kb = __builtin_amdgcn_readlane(g.ks, i), vb = __builtin_amdgcn_readlane(g.vs, i);
-            kmul[i] = p.scale_log2 * pow2(max(kb - 127, -126));
-            ve[i] = (float)(vb - 127);
-            vinv[i] = pow2(min(127 - vb, 127));
-            in[i] = held_block(__builtin_amdgcn_readlane(g.blk, i));
-          }
-          if (t0 + UNIT > all_hi || t0 < all_lo || !(in[0] && in[1] && in[2] && in[3])) {
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                const int i = 2 * a + (r >> 3);
-                const int tok = t0 + 32 * a + 16 * (r >> 3) + 8 * half + (r & 7);
-                sc[a][r] = in[i] && tok >= see_lo && tok < see_hi ? sc[a][r] * kmul[i] + ve[i] : -INFINITY;
-              }
-          } else {
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-              for (int r = 0; r < 16; ++r) sc[a][r] = sc[a][r] * kmul[2 * a + (r >> 3)] + ve[2 * a + (r >> 3)];
-          }
-          float mx = sc[0][0];
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sc[a][r]);
-          mx = fmaxf(m, max_halves(mx));
-          if (__ballot(mx > m) != 0) {     // some column's maximum rose: rescale
-            const float alpha = __builtin_amdgcn_exp2f(m - mx);
-            m = mx;
-            l *= alpha;
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-              for (int r = 0; r < 16; ++r) o[t][r] *= alpha;
-          }
-          v8h fp[2][2];
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              float x[8], sum = 0.f;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                x[j] = __builtin_amdgcn_exp2f(sc[a][8 * s + j] - m);
-                sum += x[j];
-              }
-              l += sum * vinv[2 * a + s];
-              fp[a][s] = v8h{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3],
-                             (_Float16)x[4], (_Float16)x[5], (_Float16)x[6], (_Float16)x[7]};
-            }
-#pragma unroll
-          for (int t = 0; t < DT; ++t) {
-            const int d = 32 * t + col;
-            const uint8_t* const vr = vl + d * (2 * UNIT);
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                const v8h fv = *reinterpret_cast<const v8h*>(vr + 16 * ((4 * a + 2 * s + half) ^ ((d >> 1) & 7)));
-                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fv, fp[a][s], o[t], 0, 0, 0);
-              }
-          }
-        }
-        if (u + 1 < units) store_codes(u + 1, next, held_block(blk1));
+        compute(u, scales_of(g), buf);
+        if (u + 1 < units) store_codes(u + 1, next, blk1, std::integral_constant<int, 1 - decltype(buf)::value>{});
         __syncthreads();   // unit u + 1 is in LDS; unit u is read by every wave
+      };
+      int u = 0;
+      for (; u + 1 < units; u += 2) {
+        unit(u, std::integral_constant<int, 0>{});
+        unit(u + 1, std::integral_constant<int, 1>{});
       }
+      if (u < units) unit(u, std::integral_constant<int, 0>{});
     }
 
     l = sum_halves(l);
@@ -341,7 +401,7 @@ struct Prefill {
 };
 
 template <int D>
-__global__ __launch_bounds__(PWAVES * 64, 2)
+__global__ __launch_bounds__(PWAVES * 64, D == 64 ? 3 : 2)
 void attention_prefill_kernel(AttnArgs p, int splits) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[Prefill<D>::LDS_BYTES];
   Prefill<D>::run(p, splits, lds);
