@@ -111,7 +111,9 @@ def _load():
     lib.iqp_device_clock_rates.restype = ctypes.c_int
     c_f32 = ctypes.c_float
     lib.fp8_gemm_1x128_128x128.argtypes = [c_p, c_i64, c_p, c_i64, c_i64, c_p, c_i64, c_p, c_i64, c_i64, c_i64, c_i64,
-                                           c_p, c_i64, c_p]
+                                           c_p, c_i64, c_p, c_i64, c_p]
+    lib.fp8_gemm_workspace_bytes.argtypes = [c_i64, c_i64, c_i64]
+    lib.fp8_gemm_workspace_bytes.restype = c_i64
     lib.qk_norm_rope.argtypes = [c_p, c_i64, c_p, c_i64, c_i64, c_i32, c_i32, c_i32, c_i32, c_p, c_p, c_f32, c_p, c_p,
                                  c_i64, c_p, c_i64, c_p, c_i64, c_i32, c_p]
     batch_args = [c_p, c_i64, c_i32, c_p, c_p, c_i32]

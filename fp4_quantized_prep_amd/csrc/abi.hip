@@ -534,10 +534,14 @@ int check_seq_batch(int64_t T, int32_t S, const int32_t* block_table, int64_t ld
 
 extern "C" {
 
+int64_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return M > 0 && N > 0 && K > 0 && iqp::fp8_gemm_splits(M, N, K) > 1 ? iqp::GEMM_WORKSPACE_BYTES : 0;
+}
+
 int fp8_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m, int64_t as_stride_w,
                            const void* w, int64_t ldw, const uint8_t* w_scales, int64_t ld_ws, int64_t M, int64_t N,
-                           int64_t K, void* out, int64_t ldo, void* stream) {
-  if (M < 0 || N < 0 || K < 0) return IQP_ERR_INVALID;
+                           int64_t K, void* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || workspace_bytes < 0) return IQP_ERR_INVALID;
   if (M == 0 || N == 0) return IQP_OK;
   if (!a || !a_scales || !w || !w_scales || !out) return IQP_ERR_INVALID;
   if (K == 0 || lda < K || ldw < K || ldo < N) return IQP_ERR_INVALID;
@@ -551,9 +555,14 @@ int fp8_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, 
   if (K / 128 > 256 || M > 0x7FFFFFFF || N > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
   if (lda >= ((int64_t)1 << 23) || ldw >= ((int64_t)1 << 23)) return IQP_ERR_UNSUPPORTED;
   if (as_stride_m >= ((int64_t)1 << 20) || nw * as_stride_w >= ((int64_t)1 << 28)) return IQP_ERR_UNSUPPORTED;
+  const bool split = workspace && iqp::fp8_gemm_splits(M, N, K) > 1;
+  if (split && workspace_bytes < iqp::GEMM_WORKSPACE_BYTES) return IQP_ERR_INVALID;
+  if (split && !aligned(workspace, 256)) return IQP_ERR_UNSUPPORTED;
   const int st = device_status();
   if (st != IQP_OK) return st;
   iqp::Fp8GemmArgs p{};
+  p.splits = split ? iqp::fp8_gemm_splits(M, N, K) : 1;
+  p.sums = static_cast<float*>(workspace);
   p.a = static_cast<const uint8_t*>(a);
   p.lda = lda;
   p.a_scales = a_scales;

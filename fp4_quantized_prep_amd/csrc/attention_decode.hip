@@ -157,8 +157,10 @@ struct Line {
 };
 
 __device__ __forceinline__ int64_t piece_of(int64_t total) {
-  const int64_t per = (total + ATTN_WORKGROUPS - 1) / ATTN_WORKGROUPS;   // (a shift)
-  return per < DWAVES ? DWAVES : per;     // at least a unit a wave
+  // down to a unit: a workgroup that walked several short pairs one after the
+  // other would take as long as it saves (19 sequences of up to 71
+  // tokens, 8 heads: 20 us with at least four units a workgroup, 10 with one)
+  return (total + ATTN_WORKGROUPS - 1) / ATTN_WORKGROUPS;
 }
 
 // one workgroup's partial result of a pair: max, sum, output of 16 NT rows
@@ -183,6 +185,7 @@ void attention_decode_kernel(AttnArgs p) {
   const int kg = col >> 2;          // 16-token group of the lane's key rows
 
   Line<ROWS> line(p);
+  if (line.total == 0) return;
   const int64_t per = piece_of(line.total);
   int64_t at = (int64_t)blockIdx.x * per;
   const int64_t stop = at + per < line.total ? at + per : line.total;
@@ -465,6 +468,7 @@ void attention_join_kernel(AttnArgs p) {
   __shared__ __attribute__((aligned(16))) float lds_o[JOIN][D];
   const int tid = threadIdx.x;
   Line<ROWS> line(p);
+  if (line.total == 0) return;                               // no sequence is this kernel's
   const int64_t per = piece_of(line.total);
   const Seq& q = line.q;
   int64_t pair;                                              // of the sequence
@@ -562,14 +566,15 @@ int64_t attention_workspace_bytes(int D) {
 
 hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream) {
   AttnArgs p = args;
-  if (p.seq.T <= ATTN_DECODE_TOKENS * (int64_t)p.seq.S) {
+  if (p.seq.T * p.group <= ATTN_DECODE_ROWS * (int64_t)p.seq.S) {
     p.max_rows = (int64_t)1 << 62;
     return launch_attention_decode(p, D, stream);
   }
-  // a single sequence needs one kernel, whatever its number of rows turns out to be
-  p.max_rows = p.seq.S == 1 ? 0 : ATTN_DECODE_ROWS;
+  // (a single sequence needs one kernel, whatever its number of rows turns out to be)
+  const bool alone = p.seq.S == 1 || ((int64_t)p.seq.max_blocks << p.seq.log_block) <= ATTN_SHORT_TABLE;
+  p.max_rows = alone ? 0 : ATTN_DECODE_ROWS;
   const hipError_t e = launch_attention_prefill(p, D, stream);
-  if (e != hipSuccess || p.seq.S == 1) return e;
+  if (e != hipSuccess || alone) return e;
   return launch_attention_decode(p, D, stream);
 }
 

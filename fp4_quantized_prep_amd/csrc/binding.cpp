@@ -72,7 +72,8 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, c10::Device dev) {
   return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
 }
 
-Tensor fp8_gemm(const Tensor& a, const Tensor& a_scales, const Tensor& w, const Tensor& w_scales, const OptTensor& out_) {
+Tensor fp8_gemm(const Tensor& a, const Tensor& a_scales, const Tensor& w, const Tensor& w_scales, const OptTensor& out_,
+                const OptTensor& workspace_) {
   const c10::Device dev = gpu_of(a, "a");
   require_codes(a, "a", dev, 2);
   require(a_scales, "a_scales", at::kInt, dev, 2);
@@ -97,9 +98,18 @@ Tensor fp8_gemm(const Tensor& a, const Tensor& a_scales, const Tensor& w, const 
     if (sm == 1) sw = M;
     else sw = 1;
   }
+  Tensor ws;
+  if (workspace_) {
+    ws = *workspace_;
+    require(ws, "workspace", at::kByte, dev, 1);
+    if (!ws.is_contiguous()) value_error("workspace must be contiguous");
+  } else if (const int64_t need = fp8_gemm_workspace_bytes(M, N, K)) {
+    ws = empty({need}, at::kByte, dev);
+  }
   run(fp8_gemm_1x128_128x128, "fp8_gemm_1x128_128x128", dev, a.const_data_ptr(), pitch(a), (const int32_t*)a_scales.const_data_ptr(),
       sm, sw, w.const_data_ptr(), pitch(w), (const uint8_t*)w_scales.const_data_ptr(), pitch(w_scales), M, N, K,
-      out.mutable_data_ptr(), M > 1 ? out.stride(0) : (N + 7) / 8 * 8);
+      out.mutable_data_ptr(), M > 1 ? out.stride(0) : (N + 7) / 8 * 8, ws.defined() ? ws.mutable_data_ptr() : nullptr,
+      ws.defined() ? (int64_t)ws.numel() : (int64_t)0);
   return out;
 }
 

@@ -18,30 +18,47 @@ constexpr int SLAB = 1024;   // bytes of one wave-wide copy to LDS
 constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
 // A wave's AN x AM accumulator tiles to bf16 rows: weight rows from n0 on,
-// tokens from m0 on, the lane's sixteen values of a tile consecutive.
+// tokens from m0 on, the lane's sixteen values of a tile consecutive. They pass
+// through the wave's part of LDS (store_bytes<AN>()), 32 tokens at a time, so
+// that a store covers whole stretches of a row: 16 bytes a lane where the
+// output's alignment allows it, else 2 bytes a lane, 64 consecutive values.
+template <int AN>
+constexpr int store_bytes() { return 32 * (64 * AN + 16); }
+
 template <int AN, int AM>
-__device__ __forceinline__ void store_tile(const Fp8GemmArgs& p, const v16f (&acc)[AN][AM], int64_t n0, int64_t m0, int lane) {
+__device__ __forceinline__ void store_tile(const Fp8GemmArgs& p, const v16f (&acc)[AN][AM], int64_t n0, int64_t m0, int lane,
+                                           uint8_t* lds) {
+  constexpr int PITCH = 64 * AN + 16, LANES = 4 * AN;   // bytes of a token's row; 16-byte pieces of it
   const int row = lane & 31, half = lane >> 5;
+  const int rows_n = p.N - n0 < 32 * AN ? (int)(p.N - n0) : 32 * AN;
 #pragma unroll
   for (int u = 0; u < AM; ++u) {
-    const int64_t m = m0 + 32 * u + row;
-    if (m >= p.M) continue;
+    const int64_t m = m0 + 32 * u;
+    const int rows_m = p.M - m < 32 ? (int)(p.M - m) : 32;
 #pragma unroll
     for (int t = 0; t < AN; ++t) {
-      const int64_t n = n0 + 32 * t + 16 * half;
-      uint16_t* dst = p.out + m * p.ldo + n;
       uint32_t d[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r) d[r] = layer::pack_bf16(acc[t][u][2 * r], acc[t][u][2 * r + 1]);
-      if (p.wide_out && n + 16 <= p.N) {
-        *reinterpret_cast<v4u*>(dst) = v4u{d[0], d[1], d[2], d[3]};
-        *reinterpret_cast<v4u*>(dst + 8) = v4u{d[4], d[5], d[6], d[7]};
-      } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (n + r < p.N) dst[r] = (uint16_t)(d[r >> 1] >> (16 * (r & 1)));
-      }
+      uint8_t* const to = lds + row * PITCH + 64 * t + 32 * half;
+      *reinterpret_cast<v4u*>(to) = v4u{d[0], d[1], d[2], d[3]};
+      *reinterpret_cast<v4u*>(to + 16) = v4u{d[4], d[5], d[6], d[7]};
     }
+    asm volatile("" ::: "memory");   // the wave's own writes, then its own reads: in order
+    if (p.wide_out && rows_n == 32 * AN) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 64 / LANES) {
+        const int r = i + lane / LANES, c = lane % LANES;
+        const v4u v = *reinterpret_cast<const v4u*>(lds + r * PITCH + 16 * c);
+        if (r < rows_m) *reinterpret_cast<v4u*>(p.out + (m + r) * p.ldo + n0 + 8 * c) = v;
+      }
+    } else {
+      for (int r = 0; r < rows_m; ++r)
+#pragma unroll
+        for (int c = 0; c < 32 * AN; c += 64)
+          if (c + lane < rows_n) p.out[(m + r) * p.ldo + n0 + c + lane] = *reinterpret_cast<const uint16_t*>(lds + r * PITCH + 2 * (c + lane));
+    }
+    asm volatile("" ::: "memory");
   }
 }
 
@@ -60,12 +77,13 @@ __device__ __forceinline__ void store_tile(const Fp8GemmArgs& p, const v16f (&ac
 template <int TN, int TM, int WN, int WM, int WK, int NST>
 constexpr int tile_lds_bytes() {
   constexpr int ring = WK * NST * (TN * KB + TM * KB + TM * 4), sums = (WK - 1) * TN * TM * 4;
-  return ring > sums ? ring : sums;
+  constexpr int out = WN * WM * store_bytes<TN / 32 / WN>();
+  return ring > sums ? (ring > out ? ring : out) : (sums > out ? sums : out);
 }
 
 constexpr uint32_t PAST = 0x40000000u;   // an offset beyond every buffer here
 
-template <int TN, int TM, int WN, int WM, int WK, int NST>
+template <int TN, int TM, int WN, int WM, int WK, int NST, bool SPLIT>
 __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
   constexpr int NW = WN * WM;                           // waves of a set
   constexpr int AN = TN / 32 / WN, AM = TM / 32 / WM;   // 32x32 tiles of a wave
@@ -84,18 +102,22 @@ __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
   uint8_t* const lw = lds + set * NST * (W_BYTES + A_BYTES + S_BYTES);
   uint8_t* const la = lw + NST * W_BYTES;
   uint8_t* const ls = la + NST * A_BYTES;
-  // one XCD (workgroup id mod 8) walks consecutive tiles, tokens first
+  // one XCD (workgroup id mod 8) walks consecutive tiles, tokens first; SPLIT:
+  // piece z of the K blocks of tile `tile`
   const int mt = (int)((p.M + TM - 1) / TM), nt = (int)((p.N + TN - 1) / TN);
-  const int64_t total = (int64_t)mt * nt, per = (total + 7) / 8;
-  const int64_t tile = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= per || tile >= total) return;
+  const int64_t total = (int64_t)mt * nt * (SPLIT ? p.splits : 1), per = (total + 7) / 8;
+  const int64_t item = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int64_t)(blockIdx.x >> 3) >= per || item >= total) return;
+  const int64_t tile = SPLIT ? item / p.splits : item;
   const int64_t n0 = tile / mt * TN, m0 = tile % mt * TM;
-  const int nkb = p.nkb;
+  // blocks [first, nkb)
+  const int z = SPLIT ? (int)(item - tile * p.splits) : 0;
+  const int first = SPLIT ? p.nkb * z / p.splits : 0, nkb = SPLIT ? p.nkb * (z + 1) / p.splits : p.nkb;
 
   const int64_t wrows = p.N - n0 < TN ? p.N - n0 : TN, arows = p.M - m0 < TM ? p.M - m0 : TM;
   const rsrc_t rw = make_rsrc(p.w + n0 * p.ldw, (uint64_t)wrows * p.ldw);
   const rsrc_t ra = make_rsrc(p.a + m0 * p.lda, (uint64_t)arows * p.lda);
-  const int64_t nw = (nkb + 3) / 4;
+  const int64_t nw = (p.nkb + 3) / 4;
   const rsrc_t rs = make_rsrc(p.a_scales + m0 * p.as_sm, 4 * (uint64_t)((arows - 1) * p.as_sm + (nw - 1) * p.as_sw + 1));
 
   // copies: slab i of this wave is LDS rows 8 (wave + NW i) + lane / 8
@@ -115,7 +137,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
   for (int i = 0; i < SC; ++i) vs[i] = (uint32_t)(4 * (64 * ((wave + NW * i) % SW) + lane) * (int)p.as_sm);
 
   // the set's block i into stage i % NST
-  auto block_of = [&](int i) __attribute__((always_inline)) { return set + WK * i; };
+  auto block_of = [&](int i) __attribute__((always_inline)) { return first + set + WK * i; };
   // copy c (0 .. NCOPY - 1) of the set's block i into stage st
   auto copy = [&](int i, int st, int c) __attribute__((always_inline)) {
     const int j = block_of(i);
@@ -162,7 +184,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
   // the NST - 2 blocks after it may be in flight).
   constexpr int WAIT = waitcnt_vm((NST - 2) * NCOPY);
   const int row = lane & 31, swz = (row >> 1) & 7;
-  const int count = (nkb + WK - 1) / WK;
+  const int count = (nkb - first + WK - 1) / WK;
   v8i fw[2][AN], fa[2][AM];
   uint32_t as_word[AM];
   auto read_half = [&](int st, auto khc) __attribute__((always_inline)) {
@@ -242,7 +264,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
                 v4f{acc[t][u][4 * r], acc[t][u][4 * r + 1], acc[t][u][4 * r + 2], acc[t][u][4 * r + 3]};
     }
     __syncthreads();
-    if (set > 0) return;
+    if (set == 0)
 #pragma unroll
     for (int k = 0; k < WK - 1; ++k)
 #pragma unroll
@@ -256,14 +278,69 @@ __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
             for (int e = 0; e < 4; ++e) acc[t][u][4 * r + e] += x[e];
           }
   }
-  store_tile<AN, AM>(p, acc, n0 + 32 * AN * wn, m0 + 32 * AM * wm, lane);
+  if constexpr (SPLIT) {
+    // the sums, in the accumulators' order, for fp8_gemm_join_kernel
+    static_assert(WK == 1, "a set of its own a piece");
+    float* const to = p.sums + (tile * p.splits + z) * (TN * TM) + wave * (AN * AM * 1024) + 4 * lane;
+#pragma unroll
+    for (int t = 0; t < AN; ++t)
+#pragma unroll
+      for (int u = 0; u < AM; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<v4f*>(to + ((t * AM + u) * 4 + r) * 256) =
+              v4f{acc[t][u][4 * r], acc[t][u][4 * r + 1], acc[t][u][4 * r + 2], acc[t][u][4 * r + 3]};
+    return;
+  }
+  // the ring's place again: every wave has read its operands (and sums), and no
+  // copy is in flight
+  __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
+  __syncthreads();
+  if (set > 0) return;
+  store_tile<AN, AM>(p, acc, n0 + 32 * AN * wn, m0 + 32 * AM * wm, lane, lds + wave * store_bytes<AN>());
 }
 
-template <int TN, int TM, int WN, int WM, int WK, int NST>
+template <int TN, int TM, int WN, int WM, int WK, int NST, bool SPLIT>
 __global__ __launch_bounds__(WN * WM * WK * 64)
 void fp8_gemm_tile_kernel(Fp8GemmArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[tile_lds_bytes<TN, TM, WN, WM, WK, NST>()];
-  gemm_tile<TN, TM, WN, WM, WK, NST>(p, lds);
+  gemm_tile<TN, TM, WN, WM, WK, NST, SPLIT>(p, lds);
+}
+
+// Adds up the pieces of a split tile, in their order, and stores it.
+template <int TN, int TM, int WN, int WM>
+__device__ __forceinline__ void gemm_join(const Fp8GemmArgs& p, uint8_t* lds) {
+  constexpr int AN = TN / 32 / WN, AM = TM / 32 / WM;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int mt = (int)((p.M + TM - 1) / TM);
+  const int64_t tile = blockIdx.x, n0 = tile / mt * TN, m0 = tile % mt * TM;
+  const float* const from = p.sums + tile * p.splits * (TN * TM) + wave * (AN * AM * 1024) + 4 * lane;
+  v16f acc[AN][AM];
+#pragma unroll
+  for (int t = 0; t < AN; ++t)
+#pragma unroll
+    for (int u = 0; u < AM; ++u)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[t][u][r] = 0.f;
+  for (int z = 0; z < p.splits; ++z)
+#pragma unroll
+    for (int t = 0; t < AN; ++t)
+#pragma unroll
+      for (int u = 0; u < AM; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const v4f x = *reinterpret_cast<const v4f*>(from + (int64_t)z * (TN * TM) + ((t * AM + u) * 4 + r) * 256);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][u][4 * r + e] += x[e];
+        }
+  store_tile<AN, AM>(p, acc, n0 + 32 * AN * (wave % WN), m0 + 32 * AM * (wave / WN), lane, lds + wave * store_bytes<AN>());
+}
+
+template <int TN, int TM, int WN, int WM>
+__global__ __launch_bounds__(WN * WM * 64)
+void fp8_gemm_join_kernel(Fp8GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[WN * WM * store_bytes<TN / 32 / WN>()];
+  gemm_join<TN, TM, WN, WM>(p, lds);
 }
 
 // Stream kernel, for few tokens: the product is then a read of the weights. A
@@ -435,18 +512,70 @@ hipError_t launch_tile(const Fp8GemmArgs& p, hipStream_t stream) {
   const int64_t total = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
   const int64_t blocks = (total + 7) / 8 * 8;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TN, TM, WN, WM, WK, NST>), dim3((unsigned)blocks), dim3(WN * WM * WK * 64), 0, stream, p);
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<TN, TM, WN, WM, WK, NST, false>), dim3((unsigned)blocks), dim3(WN * WM * WK * 64), 0, stream, p);
   return hipGetLastError();
+}
+
+// the 64x64 tile with its K blocks in p.splits pieces
+hipError_t launch_split(const Fp8GemmArgs& p, hipStream_t stream) {
+  const int64_t tiles = ((p.M + 63) / 64) * ((p.N + 63) / 64), blocks = (tiles * p.splits + 7) / 8 * 8;
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<64, 64, 2, 2, 1, 4, true>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((fp8_gemm_join_kernel<64, 64, 2, 2>), dim3((unsigned)tiles), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+// The kernels' time in us on a full MI355X, from the sizes alone. A workgroup's K
+// block takes a time of its own that more workgroups do not change until every
+// CU has one (the loop's copies, reads and barrier follow one another), and
+// each further 256 workgroups add to it. Measured over M 96 .. 4632, N 384 ..
+// 8192, K 640 .. 7168; us a block for up to 256 workgroups, for up to 512:
+//   64x64 0.32, 0.52;  128x64 0.42, 0.69;  128x128 four stages 0.56, 1.13;
+//   128x128 two stages 0.75, 0.9;  256x256 1.3, 2.6 (an area 16 times the first's)
+double tile_us(const Fp8GemmArgs& p, int TN, int TM, double fixed, double block, double more, int group) {
+  const int64_t tiles = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
+  const int64_t rounds = (tiles + 255) / 256;
+  const int64_t turns = (rounds + group - 1) / group;      // `group` workgroups share a CU
+  return turns * fixed + p.nkb * (turns * block + (rounds - turns) * more);
 }
 
 }  // namespace
 
+// Pieces that the K blocks of a product are split into (1: not split): where
+// few 64x64 tiles walk many blocks, as many as still give each a CU of its own,
+// down to eight blocks a piece, if that takes at least 16 blocks (5 us) off the
+// walk: the second launch and the sums' way through memory take 3.5 to 5.
+// Measured, split / not, us: 96x384x7168 10.0 / 18.1, 268x1024x7168 13.4 / 18.1,
+// 96x384x3200 8.4 / 9.7; 268x1024x3200 10.4 / 9.9 (not split), 268x2115x7168 17.9 / 19.1.
+int fp8_gemm_splits(int64_t M, int64_t N, int64_t K) {
+  if (M <= 64) return 1;
+  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64), nkb = K / 128;
+  int64_t z = GEMM_SPLIT_GROUPS / tiles;
+  if (z > nkb / 8) z = nkb / 8;
+  return z >= 2 && nkb - nkb / z >= 16 ? (int)z : 1;
+}
+
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& p, hipStream_t stream) {
+  // up to 64 tokens the product is a read of the weights; 16 or 32 rows of them a
+  // workgroup, by which of the two gives the CUs enough workgroups (measured at
+  // 16 tokens, 32 / 16 rows: N 7168, K 8192 13.6 / 15.6 us; N 1536, K 7168 5.8 / 5.1)
   if (p.M <= 16) return p.N >= 6144 ? launch_stream<2, 1, 8, 3>(p, stream) : launch_stream<1, 1, 4, 4>(p, stream);
   if (p.M <= 32) return p.N >= 6144 ? launch_stream<2, 2, 8, 2>(p, stream) : launch_stream<1, 2, 4, 3>(p, stream);
   if (p.M <= 64) return p.N >= 6144 ? launch_stream<2, 4, 4, 3>(p, stream) : launch_stream<1, 4, 4, 3>(p, stream);
-  if (p.M <= 128) return launch_stream<4, 4, 4, 2>(p, stream);
-  if (p.M <= 1024) return launch_tile<64, 64, 2, 2, 1, 4>(p, stream);
+  if (p.splits > 1) return launch_split(p, stream);
+  const double t64 = tile_us(p, 64, 64, 1.5, 0.31, 0.23, 2), t128x64 = tile_us(p, 128, 64, 2.0, 0.41, 0.3, 2),
+               t128 = tile_us(p, 128, 128, 3.0, 0.54, 0.54, 1), t128x2 = tile_us(p, 128, 128, 3.0, 0.73, 0.18, 2),
+               t256 = tile_us(p, 256, 256, 5.0, 1.28, 1.28, 1);
+  double best = t64;
+  if (t128x64 < best) best = t128x64;
+  if (t128 < best) best = t128;
+  if (t128x2 < best) best = t128x2;
+  if (t256 < best) best = t256;
+  if (best == t64) return launch_tile<64, 64, 2, 2, 1, 4>(p, stream);
+  if (best == t128x64) return launch_tile<128, 64, 2, 2, 1, 3>(p, stream);
+  if (best == t128) return launch_tile<128, 128, 2, 2, 1, 4>(p, stream);
+  if (best == t128x2) return launch_tile<128, 128, 2, 2, 1, 2>(p, stream);
   return launch_tile<256, 256, 2, 4, 1, 2>(p, stream);
 }
 

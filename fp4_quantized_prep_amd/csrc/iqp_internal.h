@@ -205,7 +205,13 @@ struct Fp8GemmArgs {
   uint16_t* out;            // bf16 [M, N], row stride ldo elements
   int64_t ldo;
   bool wide_out;            // 16-byte stores allowed (out and ldo aligned)
+  int32_t splits;           // pieces of the K blocks: fp8_gemm_splits(M, N, K), or 1 without a workspace
+  float* sums;              // workspace of a split product
 };
+// workgroups of a split product at most, each with a 64x64 tile of float32 sums
+constexpr int GEMM_SPLIT_GROUPS = 256;
+constexpr int64_t GEMM_WORKSPACE_BYTES = (int64_t)GEMM_SPLIT_GROUPS * 64 * 64 * 4;
+int fp8_gemm_splits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& args, hipStream_t stream);
 
 struct QkNormRopeArgs {
@@ -274,11 +280,12 @@ struct AttnArgs {
 };
 // workgroups of the decode kernel: two for each of a full chip's 256 CUs
 constexpr int ATTN_WORKGROUPS = 512;
-// A batch of at most ATTN_DECODE_TOKENS tokens a sequence on average goes to the
-// decode kernel alone; otherwise its sequences of more than ATTN_DECODE_ROWS
-// rows go to the prompt kernel.
-constexpr int ATTN_DECODE_TOKENS = 4;
+// Sequences of more than ATTN_DECODE_ROWS rows are the prompt kernel's, in a
+// batch that has more than that on average; else all are the decode kernel's.
 constexpr int ATTN_DECODE_ROWS = 64;
+// Where the table holds no more tokens than this, the prompt kernel takes such a
+// batch's short sequences too: their few units cost less than two more launches.
+constexpr int ATTN_SHORT_TABLE = 1024;
 int64_t attention_decode_workspace_bytes(int D);
 int64_t attention_prefill_workspace_bytes(int D);
 hipError_t launch_attention_decode(const AttnArgs& args, int D, hipStream_t stream);

@@ -9,7 +9,7 @@ import torch
 from . import _binding, _check, _lib
 
 __all__ = [
-    "fp8_gemm_1x128_128x128", "qk_norm_rope", "Fp8KvCache", "fp8_kv_cache", "kv_cache_append_fp8", "kv_cache_read_fp8",
+    "fp8_gemm_1x128_128x128", "fp8_gemm_workspace_bytes", "qk_norm_rope", "Fp8KvCache", "fp8_kv_cache", "kv_cache_append_fp8", "kv_cache_read_fp8",
     "attention_fp8_kv", "attention_fp8_kv_workspace_bytes", "attention_fp8_kv_workspace",
 ]
 
@@ -25,16 +25,24 @@ def _on(stream, tensor, fn, *args):
         return fn(*args)
 
 
-def fp8_gemm_1x128_128x128(a, a_scales, w, w_scales, out=None, stream=None):
+def fp8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of the workspace that :func:`fp8_gemm_1x128_128x128` can use (0: none)."""
+    return int(_lib.fp8_gemm_workspace_bytes(M, N, K))
+
+
+def fp8_gemm_1x128_128x128(a, a_scales, w, w_scales, out=None, workspace=None, stream=None):
     """Block-scaled FP8 product ``out = a w^T`` in bf16.
 
     a: E4M3 [M, K] (uint8 or float8_e4m3fn) and a_scales: the packed words from
     :func:`fp8_quant_1x128_ue8m0` (either layout); w: E4M3 [N, K], any N, and
     w_scales: uint8 [ceil(N/128), K/128] as :func:`fp8_quant_weight_128x128_ue8m0`
     gives them. Rows contiguous, any row strides that are multiples of 16.
-    Returns ``out``, bf16 [M, N] (rows contiguous where passed in).
+    workspace: a uint8 tensor of :func:`fp8_gemm_workspace_bytes` bytes for
+    products that are split over K (allocated here when None); calls that share
+    one must not overlap. Returns ``out``, bf16 [M, N] (rows contiguous where
+    passed in).
     """
-    args = (a, a_scales, w, w_scales, out)
+    args = (a, a_scales, w, w_scales, out, workspace)
     return _binding.fp8_gemm(*args) if stream is None else _on(stream, a, _binding.fp8_gemm, *args)
 
 

@@ -596,12 +596,20 @@ int iqp_device_clock_rates(int64_t* wall_clock_hz, int64_t* peak_shader_clock_hz
  *   out        bf16 [M, N], row stride ldo (elements, >= N), 2-byte aligned
  *              (16-byte stores where it is 16-byte aligned and ldo a multiple
  *              of 8). Must not overlap the inputs.
- * M == 0 or N == 0: no-op. The sum must fit float32, as there.
+ *   workspace  NULL, or fp8_gemm_workspace_bytes(M, N, K) bytes of device
+ *              memory, 256-byte aligned: with it a product of few output tiles
+ *              and many K blocks is split over K (two launches). Its contents do
+ *              not matter before and mean nothing after; calls that share one
+ *              must not overlap. Where that size is 0 it is not used.
+ * M == 0 or N == 0: no-op. The sum must fit float32, as there. The order in
+ * which K blocks are added depends on M, N, K and the workspace's presence only.
  */
+int64_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int fp8_gemm_1x128_128x128(const void* a, int64_t lda,
                            const int32_t* a_scales, int64_t as_stride_m, int64_t as_stride_w,
                            const void* w, int64_t ldw, const uint8_t* w_scales, int64_t ld_ws,
-                           int64_t M, int64_t N, int64_t K, void* out, int64_t ldo, void* stream);
+                           int64_t M, int64_t N, int64_t K, void* out, int64_t ldo,
+                           void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * qk_norm_rope — RMS norm of every query and key head, times its weights,

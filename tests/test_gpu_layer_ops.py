@@ -35,7 +35,7 @@ def exact_operands(g, M, N, K):
     return a, words.view(torch.int32), w, ws
 
 
-GEMM_SIZES = [(1, 128, 128), (1, 1536, 7168), (3, 131, 256), (16, 257, 640), (17, 384, 1536), (31, 96, 2048), (33, 1, 128),
+GEMM_SIZES = [(96, 140, 3200), (70, 64, 7168), (130, 515, 7168), (1, 128, 128), (1, 1536, 7168), (3, 131, 256), (16, 257, 640), (17, 384, 1536), (31, 96, 2048), (33, 1, 128),
               (64, 512, 896), (65, 130, 1536), (100, 2115, 512), (128, 128, 1024), (129, 256, 384), (200, 1000, 768),
               (257, 640, 1536), (513, 264, 128), (777, 515, 1280), (1100, 1536, 256)]
 
@@ -108,6 +108,28 @@ def test_gemm_strides_and_outputs(gpu_lib, M, N):
         want = torch.full_like(buf, 7.0)
         want[1:M + 1, first:first + N] = ref.cuda()
         assert torch.equal(buf, want), (pad, first)
+
+
+def test_gemm_split_with_and_without_a_workspace(gpu_lib):
+    """A product split over K: the caller's workspace holding anything, one too
+    small, and the same product without one through the C call."""
+    M, N, K = 100, 200, 4096
+    a, words, w, ws = exact_operands(gen(20), M, N, K)
+    ref = (R.dequant_rows(a, words) @ R.dequant_tiles(w, ws).T).to(torch.bfloat16)
+    need = gpu_lib.fp8_gemm_workspace_bytes(M, N, K)
+    assert need > 0
+    a, words, w, ws = a.cuda(), words.cuda(), w.cuda(), ws.cuda()
+    space = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        assert torch.equal(gpu_lib.fp8_gemm_1x128_128x128(a, words, w, ws, workspace=space).cpu(), ref)
+    with pytest.raises(gpu_lib.IqpError) as e:
+        gpu_lib.fp8_gemm_1x128_128x128(a, words, w, ws, workspace=space[:-256])
+    assert e.value.status == gpu_lib.IQP_ERR_INVALID
+    out = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    st = gpu_lib._lib.fp8_gemm_1x128_128x128(a.data_ptr(), K, words.data_ptr(), words.stride(0), 1, w.data_ptr(), K, ws.data_ptr(),
+                                             K // 128, M, N, K, out.data_ptr(), N, None, 0,
+                                             torch.cuda.current_stream().cuda_stream)
+    assert st == gpu_lib.IQP_OK and torch.equal(out.cpu(), ref)
 
 
 def test_gemm_is_deterministic_and_empty(gpu_lib):
@@ -324,6 +346,25 @@ def test_attention_single_tokens(gpu_lib, hq, h, d, block, window):
 def test_attention_rows(gpu_lib, lens, new, hq, h, d, block, window):
     print("attend rows", lens, new, hq, h, d, block, window, flush=True)
     attend(gpu_lib, gen(11, len(lens), lens[0], hq, d, window), lens, new, hq, h, d, block, window, nan_codes=True, tail=3)
+
+
+@pytest.mark.parametrize("lens,new", [([1500, 40, 1100], [200, 1, 90]), ([1300, 1200], [150, 130]), ([1030, 1, 5], [1, 1, 0]),
+                                      ([1100, 1080, 1], [70, 66, 1])])
+@pytest.mark.parametrize("hq,h,d,block", [(4, 2, 128, 64), (8, 1, 64, 32)])
+def test_attention_prompts_over_a_long_table(gpu_lib, lens, new, hq, h, d, block):
+    """Batches whose sequences go to two kernels, or to one of them alone."""
+    print("attend long table", lens, new, hq, h, d, block, flush=True)
+    attend(gpu_lib, gen(18, len(lens), lens[0], new[0], hq), lens, new, hq, h, d, block, 0, tail=1)
+
+
+def test_attention_many_sequences(gpu_lib):
+    """More sequences than a wave has lanes, some without rows."""
+    g = gen(19)
+    lens = [int(x) for x in g.integers(1, 90, 150)]
+    new = [int(x) for x in g.integers(0, 2, 150)]
+    attend(gpu_lib, g, lens, new, 4, 2, 64, 16, tail=2)
+    lens = [int(x) for x in g.integers(20, 60, 70)]
+    attend(gpu_lib, g, lens, [int(x) for x in g.integers(0, 20, 70)], 8, 2, 128, 16, window=30)
 
 
 def test_attention_long_sequence(gpu_lib):

@@ -18,8 +18,8 @@ def iqp():
 def test_gemm_refusals(iqp):
     inv, uns = iqp.IQP_ERR_INVALID, iqp.IQP_ERR_UNSUPPORTED
 
-    def call(a=16, lda=256, s=16, sm=1, sw=1, w=16, ldw=256, ws=16, ldws=2, M=1, N=130, K=256, o=16, ldo=136):
-        return iqp._lib.fp8_gemm_1x128_128x128(P(a), lda, P(s), sm, sw, P(w), ldw, P(ws), ldws, M, N, K, P(o), ldo, None)
+    def call(a=16, lda=256, s=16, sm=1, sw=1, w=16, ldw=256, ws=16, ldws=2, M=1, N=130, K=256, o=16, ldo=136, wk=0, wkb=0):
+        return iqp._lib.fp8_gemm_1x128_128x128(P(a), lda, P(s), sm, sw, P(w), ldw, P(ws), ldws, M, N, K, P(o), ldo, P(wk), wkb, None)
     for bad in (dict(M=-1), dict(N=-1), dict(K=-1), dict(a=0), dict(s=0), dict(w=0), dict(ws=0), dict(o=0), dict(K=0),
                 dict(lda=128), dict(ldw=128), dict(ldo=129), dict(ldws=1), dict(sm=3, sw=3), dict(M=4, sm=1, sw=2)):
         assert call(**bad) == inv, bad
@@ -27,6 +27,13 @@ def test_gemm_refusals(iqp):
                 dict(K=257 * 128, lda=257 * 128, ldw=257 * 128, ldws=257, sm=65), dict(lda=1 << 23), dict(ldw=1 << 23),
                 dict(sm=1 << 20), dict(M=1 << 31, sm=1, sw=1 << 31, ldo=136)):
         assert call(**bad) == uns, bad
+    # a product that is split: the workspace's size and alignment count
+    need = iqp.fp8_gemm_workspace_bytes(128, 256, 7168)
+    assert need > 0 and iqp.fp8_gemm_workspace_bytes(16, 256, 7168) == 0 and iqp.fp8_gemm_workspace_bytes(0, 256, 7168) == 0
+    big = dict(M=128, N=256, K=7168, lda=7168, ldw=7168, ldws=56, sm=14, ldo=256)
+    assert call(**big, wk=256, wkb=need - 1) == inv
+    assert call(**big, wk=128, wkb=need) == uns
+    assert call(wkb=-1) == inv
     assert call(M=0) == iqp.IQP_OK and call(N=0) == iqp.IQP_OK
 
 
