@@ -291,7 +291,7 @@ struct Prefill {
       for (int i = 0; i < GR; ++i) {
         const v16f& x = sc[i >> 1];
         const int r = 8 * (i & 1);
-        const float gm = max3(max3(x[r], x[r + 1], x[r + 2]), max3(x[r + 3], x[r + 4], x[r + 5]), max3(x[r + 6], x[r + 7], x[r + 7]));
+        const float gm = max3(max3(x[r], x[r + 1], x[r + 2]), max3(x[r + 3], x[r + 4], x[r + 5]), fmaxf(x[r + 6], x[r + 7]));
         mx = fmaxf(mx, __builtin_fmaf(gm, kmul_of(g, i), exponent_of(g, i)));
       }
       mx = max_halves(mx);
@@ -319,10 +319,12 @@ struct Prefill {
         const v16f& x = sc[i >> 1];
         const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(x[8 * (i & 1) + j], km[i], cm[i]));
         const float z = __builtin_amdgcn_exp2f(__builtin_fmaf(x[8 * (i & 1) + j + 1], km[i], cm[i]));
-        const v2h h = {(_Float16)y, (_Float16)z};
-        sum[i] = __builtin_amdgcn_fdot2(h, v2h{1, 1}, sum[i], false);   // of the rounded weights, in float32
-        fp[i][j] = h[0];
-        fp[i][j + 1] = h[1];
+        // float32, not the rounded weights: where another block's values are
+        // larger by many powers of two, fp16 holds a weight's share of the
+        // product, but not its share of the sum
+        sum[i] += y + z;
+        fp[i][j] = (_Float16)y;
+        fp[i][j + 1] = (_Float16)z;
       };
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) fv[j] = value(j);

@@ -385,21 +385,27 @@ def test_attention_rows_that_see_nothing(gpu_lib):
     attend(gpu_lib, gen(15), [40, 100, 60, 0, 3], [3, 2, 60, 2, 6], 4, 2, 64, 16, table=holes, nan_codes=True, window=20)
 
 
-def test_attention_value_scales_far_apart(gpu_lib):
+@pytest.mark.parametrize("lens,new", [([200], [1]), ([200, 180], [120, 100]), ([1300, 1200], [100, 120])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_value_scales_far_apart(gpu_lib, lens, new, d):
     """Neighbouring blocks whose value and key exponents differ by many powers
-    of two, and a block of zeros at the smallest exponent."""
-    g = gen(16)
-    lens, h, d, block = [200], 2, 64, 32
-    table, cu, n = make_batch(g, lens, [1], block)
+    of two, and a block of zeros at the smallest exponent: a token's share of
+    the sum must not depend on its value exponent."""
+    print("attend scales", lens, new, d, flush=True)
+    g = gen(16, d)
+    h, block = 2, 32
+    table, cu, n = make_batch(g, lens, new, block)
     ref = random_cache(g, n, h, block, d)
-    for i in range(7):
-        ref["vs"][int(table[0, i])] = [105, 140, 100, 127, 90, 150, 120][i]
-        ref["ks"][int(table[0, i])] = [120, 119, 110, 118, 120, 121, 117][i]
-    ref["v"][int(table[0, 0])] = 0
-    q = bf16(g, 1, 4, d)
+    for s in range(len(lens)):
+        for i in range(-(-lens[s] // block)):
+            ref["vs"][int(table[s, i])] = [105, 140, 100, 127, 90, 150, 120][i % 7]
+            ref["ks"][int(table[s, i])] = [120, 119, 110, 118, 120, 121, 117][i % 7]
+        ref["v"][int(table[s, 0])] = 0
+    q = bf16(g, cu[-1], 4, d)
     want, tol = R.attention(q, ref, table, lens, cu, d ** -0.5, 0)
     got = gpu_lib.attention_fp8_kv(q.cuda(), to_gpu(gpu_lib, ref), table.cuda(), ints(lens), ints(cu)).cpu().double()
-    assert bool(((got - want).abs() <= tol).all())
+    off = (got - want).abs()
+    assert bool((off <= tol).all()), float((off / tol.clamp_min(1e-300)).nan_to_num(1e9).max())
 
 
 def test_attention_scale_and_deterministic(gpu_lib):
