@@ -518,6 +518,7 @@ int check_seq_batch(int64_t T, int32_t S, const int32_t* block_table, int64_t ld
   if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128) return IQP_ERR_UNSUPPORTED;
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_rows, 4)) return IQP_ERR_UNSUPPORTED;
   if (T > 0x7FFFFFFF || Hk > 65535 || n_blocks > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  if ((int64_t)max_blocks * block_size > (1 << 30)) return IQP_ERR_UNSUPPORTED;   // positions in 32 bits, units of them too
   b.cu = cu_rows;
   b.lens = seq_lens;
   b.table = block_table;
@@ -553,8 +554,8 @@ int fp8_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, 
   // a workgroup keeps a weight tile's scale bytes in one register (4 per lane)
   // and addresses its tiles of up to 256 rows with 32-bit offsets
   if (K / 128 > 256 || M > 0x7FFFFFFF || N > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
-  if (lda >= ((int64_t)1 << 23) || ldw >= ((int64_t)1 << 23)) return IQP_ERR_UNSUPPORTED;
-  if (as_stride_m >= ((int64_t)1 << 20) || nw * as_stride_w >= ((int64_t)1 << 28)) return IQP_ERR_UNSUPPORTED;
+  if (lda > ((int64_t)1 << 22) || ldw > ((int64_t)1 << 22)) return IQP_ERR_UNSUPPORTED;
+  if (as_stride_m >= ((int64_t)1 << 19) || as_stride_w >= ((int64_t)1 << 27) / nw) return IQP_ERR_UNSUPPORTED;
   const bool split = workspace && iqp::fp8_gemm_splits(M, N, K) > 1;
   if (split && workspace_bytes < iqp::GEMM_WORKSPACE_BYTES) return IQP_ERR_INVALID;
   if (split && !aligned(workspace, 256)) return IQP_ERR_UNSUPPORTED;

@@ -36,7 +36,7 @@ def fp8_gemm_1x128_128x128(a, a_scales, w, w_scales, out=None, workspace=None, s
     a: E4M3 [M, K] (uint8 or float8_e4m3fn) and a_scales: the packed words from
     :func:`fp8_quant_1x128_ue8m0` (either layout); w: E4M3 [N, K], any N, and
     w_scales: uint8 [ceil(N/128), K/128] as :func:`fp8_quant_weight_128x128_ue8m0`
-    gives them. Rows contiguous, any row strides that are multiples of 16.
+    gives them. Rows contiguous, row strides any multiples of 16 up to 2^22.
     workspace: a uint8 tensor of :func:`fp8_gemm_workspace_bytes` bytes for
     products that are split over K (allocated here when None); calls that share
     one must not overlap. Returns ``out``, bf16 [M, N] (rows contiguous where
@@ -92,7 +92,7 @@ def kv_cache_append_fp8(k, v, cache, block_table, seq_lens, cu_rows, stream=None
     sequence s, whose length with them is ``seq_lens[s]``. block_table: int32
     [S, max_blocks], the block that holds each ``block_size`` positions. Where a
     block is begun earlier its exponent may grow, and its earlier codes are then
-    rounded again. A block must not be written for two sequences in one call.
+    rounded again. No block may be written through two table entries in one call.
     Returns the cache.
     """
     args = (k, v, *cache, block_table, seq_lens, cu_rows)

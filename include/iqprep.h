@@ -589,8 +589,9 @@ int iqp_device_clock_rates(int64_t* wall_clock_hz, int64_t* peak_shader_clock_hz
  * (float32 accumulation, one rounding to bf16).
  *
  *   a, lda, a_scales, as_stride_m, as_stride_w, w, ldw   as in
- *              indexer_q_gemm_rope_fp4 (row strides multiples of 16, below
- *              2^23 bytes; K a multiple of 128, at most 32768).
+ *              indexer_q_gemm_rope_fp4, with row strides that are multiples
+ *              of 16 up to 2^22, as_stride_m below 2^19 and as_stride_w below
+ *              2^27 / ceil(K/512); K a multiple of 128, at most 32768.
  *   w          E4M3 [N, K]; N is any (the scales' last tile may be partial).
  *   w_scales   UE8M0 [ceil(N/128), K/128], row stride ld_ws (bytes, >= K/128).
  *   out        bf16 [M, N], row stride ldo (elements, >= N), 2-byte aligned
@@ -655,8 +656,8 @@ int qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int64_t
  *   block_table  int32 [S, max_blocks], row stride ld_table: position p of
  *                sequence s is token p % block_size of block
  *                block_table[s, p / block_size]. An entry outside [0,
- *                n_blocks), a position of max_blocks * block_size or more, and a
- *                position below 0 mean a token that is not held.
+ *                n_blocks), a position of max_blocks * block_size or more (at
+ *                most 2^30), and a position below 0 mean a token that is not held.
  * These three arrays are read on the device: a call can be captured once and
  * replayed with other lengths, up to the T rows and S sequences it was given.
  * T == 0 or S == 0: no-op.
@@ -677,7 +678,8 @@ int qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int64_t
  *
  *   k, v       bf16 [T, Hk*D], row strides ldk, ldv (elements); 16-byte
  *              aligned, strides multiples of 8. Finite.
- * A block must not receive rows of two sequences in one call.
+ * No block may be named by two of the table entries that a call's rows fall
+ * into, of two sequences or of one.
  */
 int kv_cache_append_fp8(const void* k, int64_t ldk, const void* v, int64_t ldv, int64_t T, int32_t Hk, int32_t D,
                         void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales,
@@ -708,7 +710,9 @@ int kv_cache_read_fp8(const void* k_cache, const void* v_cache, const uint8_t* k
  * with k_t, v_t the values the cache stands for; zeros where there is no such
  * token. Scores, maxima and sums are float32; the weights w_t are rounded to
  * fp16 for the second product, relative to the row's largest w_t 2^e_t (e_t the
- * value exponent of t's block).
+ * value exponent of t's block). The value exponents that a row sees may lie up to
+ * 100 apart (always so where no value written exceeds 2^86): beyond that the
+ * smaller ones' weights are lost from the sum.
  *
  *   q, out     bf16 [T, Hq*D], row strides ldq, ldo (elements); 16-byte
  *              aligned, strides multiples of 8; out must not overlap q. Rows

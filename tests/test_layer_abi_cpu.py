@@ -25,7 +25,8 @@ def test_gemm_refusals(iqp):
         assert call(**bad) == inv, bad
     for bad in (dict(K=200), dict(a=8), dict(w=8), dict(lda=264), dict(ldw=264), dict(s=18), dict(o=17),
                 dict(K=257 * 128, lda=257 * 128, ldw=257 * 128, ldws=257, sm=65), dict(lda=1 << 23), dict(ldw=1 << 23),
-                dict(sm=1 << 20), dict(M=1 << 31, sm=1, sw=1 << 31, ldo=136)):
+                dict(lda=(1 << 22) + 16), dict(ldw=(1 << 22) + 16), dict(sm=1 << 20), dict(sm=1 << 19),
+                dict(M=2, sm=1, sw=1 << 27), dict(M=1 << 31, sm=1, sw=1 << 31, ldo=136)):
         assert call(**bad) == uns, bad
     # a product that is split: the workspace's size and alignment count
     need = iqp.fp8_gemm_workspace_bytes(128, 256, 7168)
@@ -60,7 +61,8 @@ def batch(n=5, b=64, table=16, ldt=4, mb=4, lens=16, cu=16, S=2):
 
 BATCH_INVALID = (dict(n=-1), dict(b=-16), dict(mb=-1), dict(S=-1), dict(table=0), dict(lens=0), dict(cu=0), dict(mb=0),
                  dict(n=0), dict(ldt=3))
-BATCH_UNSUPPORTED = (dict(b=48), dict(b=8), dict(b=256), dict(table=18), dict(lens=18), dict(cu=18), dict(n=1 << 31))
+BATCH_UNSUPPORTED = (dict(b=48), dict(b=8), dict(b=256), dict(table=18), dict(lens=18), dict(cu=18), dict(n=1 << 31),
+                     dict(mb=(1 << 24) + 1, ldt=1 << 25))
 
 
 def test_append_refusals(iqp):
