@@ -191,11 +191,9 @@ struct Prefill {
     const int key_to = tok * (2 * D), value_to = K_BYTES + dim * (2 * U);
     const int key_to0 = key_to + 16 * ((2 * piece) ^ key_swizzle(tok)), key_to1 = key_to + 16 * ((2 * piece + 1) ^ key_swizzle(tok));
     const int value_to0 = value_to + 16 * ((2 * gr) ^ value_swizzle(dim)), value_to1 = value_to + 16 * ((2 * gr + 1) ^ value_swizzle(dim));
-    // the thread's codes of unit u to buffer BUF, widened
-    auto store_codes = [&](int u, Codes& c, int blk, auto buf) __attribute__((always_inline)) {
-      constexpr int BUF = decltype(buf)::value * (K_BYTES + V_BYTES);
-      // values behind the sequence, before the window or not held must not
-      // reach the product (0 * NaN)
+    // values behind the sequence, before the window or not held must not reach
+    // the product (0 * NaN)
+    auto clear_codes = [&](int u, Codes& c, int blk) __attribute__((always_inline)) {
       const int64_t t0 = base + (int64_t)u * U;
       if (t0 < w.lo || t0 + U > w.len || __ballot(!held_block(blk)) != 0) {
         const int64_t hi64 = w.len - t0 - 16 * gr, lo64 = w.lo - t0 - 16 * gr;
@@ -203,13 +201,16 @@ struct Prefill {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) c.v[i] = clear_outside(c.v[i], lo, hi);
       }
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {   // (KSTEP and VSTEP rows on, the swizzles are the same)
-        *reinterpret_cast<v8bf*>(lds + key_to0 + (BUF + KSTEP * i * 2 * D)) = widen_bf16(c.k[i][0], c.k[i][1]);
-        *reinterpret_cast<v8bf*>(lds + key_to1 + (BUF + KSTEP * i * 2 * D)) = widen_bf16(c.k[i][2], c.k[i][3]);
-        *reinterpret_cast<v8h*>(lds + value_to0 + (BUF + VSTEP * i * 2 * U)) = widen_f16(c.v[i][0], c.v[i][1]);
-        *reinterpret_cast<v8h*>(lds + value_to1 + (BUF + VSTEP * i * 2 * U)) = widen_f16(c.v[i][2], c.v[i][3]);
-      }
+    };
+    // piece j (0 .. 4 LOADS - 1) of the thread's codes to buffer BUF, widened
+    // (KSTEP and VSTEP rows on, the swizzles are the same)
+    auto store_codes = [&](const Codes& c, int j, auto buf) __attribute__((always_inline)) {
+      constexpr int BUF = decltype(buf)::value * (K_BYTES + V_BYTES);
+      const int i = j >> 2;
+      if ((j & 3) == 0) *reinterpret_cast<v8bf*>(lds + key_to0 + (BUF + KSTEP * i * 2 * D)) = widen_bf16(c.k[i][0], c.k[i][1]);
+      if ((j & 3) == 1) *reinterpret_cast<v8bf*>(lds + key_to1 + (BUF + KSTEP * i * 2 * D)) = widen_bf16(c.k[i][2], c.k[i][3]);
+      if ((j & 3) == 2) *reinterpret_cast<v8h*>(lds + value_to0 + (BUF + VSTEP * i * 2 * U)) = widen_f16(c.v[i][0], c.v[i][1]);
+      if ((j & 3) == 3) *reinterpret_cast<v8h*>(lds + value_to1 + (BUF + VSTEP * i * 2 * U)) = widen_f16(c.v[i][2], c.v[i][3]);
     };
 
     float m = LOWEST, l = 0.f;
@@ -252,8 +253,10 @@ struct Prefill {
     auto kmul_of = [&](const Scales& s, int i) __attribute__((always_inline)) { return __int_as_float(s.kmul[i]); };
     auto vinv_of = [&](const Scales& s, int i) __attribute__((always_inline)) { return __int_as_float(max(254 - s.vb[i], 1) << 23); };
 
-    // unit u, whose codes are in buffer BUF of LDS
-    auto compute = [&](int u, const Scales& g, auto buf) __attribute__((always_inline)) {
+    // unit u, whose codes are in buffer BUF of LDS; beside the score MFMAs the
+    // next unit's codes go to the other buffer, then the one's after it are loaded
+    auto compute = [&](int u, const Scales& g, const Codes& next, auto buf, auto load) __attribute__((always_inline)) {
+      using Other = std::integral_constant<int, 1 - decltype(buf)::value>;
       constexpr int BUF = decltype(buf)::value * (K_BYTES + V_BYTES);
       const int t0 = u * U;
       // operands are read AHEAD MFMAs before their use
@@ -274,8 +277,12 @@ struct Prefill {
         const v16f zero = {};
         sc[j % NA] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk[j], fq[j / NA], j < NA ? zero : sc[j % NA], 0, 0, 0);
         if (j + AHEAD < NQK) fk[j + AHEAD] = key(j + AHEAD);
+#pragma unroll
+        for (int e = 4 * LOADS * j / NQK; e < 4 * LOADS * (j + 1) / NQK; ++e) store_codes(next, e, Other{});
         __builtin_amdgcn_sched_barrier(0);
       }
+      load();
+      __builtin_amdgcn_sched_barrier(0);
       if (t0 + U > all_hi || t0 < all_lo || g.held != (1 << GR) - 1) {
 #pragma unroll
         for (int a = 0; a < NA; ++a)
@@ -323,6 +330,7 @@ struct Prefill {
         // larger by many powers of two, fp16 holds a weight's share of the
         // product, but not its share of the sum
         sum[i] += y + z;
+        asm volatile("" : "+v"(sum[i]));   // here, beside the MFMAs, not behind them
         fp[i][j] = (_Float16)y;
         fp[i][j + 1] = (_Float16)z;
       };
@@ -346,24 +354,35 @@ struct Prefill {
     };
 
     if (units > 0) {
-      int blk = load_block(0), blk_next = load_block(1);
-      Granules gn = load_granules(blk);
+      int blk1 = load_block(1), blk2;        // the next unit's blocks, and the one's after it
+      Granules g0, g1;
+      Codes c;
       {
-        Codes c = load_codes(0, blk);
-        store_codes(0, c, blk, std::integral_constant<int, 0>{});
+        const int blk0 = load_block(0);
+        g0 = load_granules(blk0);
+        c = load_codes(0, blk0);
+        blk2 = load_block(2);
+        clear_codes(0, c, blk0);
+#pragma unroll
+        for (int j = 0; j < 4 * LOADS; ++j) store_codes(c, j, std::integral_constant<int, 0>{});
+      }
+      if (units > 1) {
+        g1 = load_granules(blk1);
+        c = load_codes(1, blk1);
       }
       __syncthreads();
       auto unit = [&](int u, auto buf) __attribute__((always_inline)) {
-        const Granules g = gn;
-        Codes next;
-        const int blk1 = blk_next;
-        if (u + 1 < units) {
-          blk_next = load_block(u + 2);
-          gn = load_granules(blk1);
-          next = load_codes(u + 1, blk1);
-        }
-        compute(u, scales_of(g), buf);
-        if (u + 1 < units) store_codes(u + 1, next, blk1, std::integral_constant<int, 1 - decltype(buf)::value>{});
+        const Granules g = g0;
+        if (u + 1 < units) clear_codes(u + 1, c, blk1);
+        g0 = g1;
+        compute(u, scales_of(g), c, buf, [&]() __attribute__((always_inline)) {
+          blk1 = blk2;
+          if (u + 2 < units) {
+            g1 = load_granules(blk1);
+            c = load_codes(u + 2, blk1);
+            blk2 = load_block(u + 3);
+          }
+        });
         __syncthreads();   // unit u + 1 is in LDS; unit u is read by every wave
       };
       int u = 0;
