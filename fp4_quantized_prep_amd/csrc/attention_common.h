@@ -53,6 +53,106 @@ __device__ __forceinline__ int64_t row_offset(int64_t begin, int64_t row, int he
   return (begin + i) * ld + ((int64_t)head * group + (row - i * group)) * D;
 }
 
+// Joining partial results (max, sum and unnormalised output of a row, each
+// relative to its own max). A group of D / 4 lanes sums up those of a row: all of
+// them where they are few (every group then has a row of its own), else every
+// JOIN-th, and the groups meet in LDS.
+constexpr int JOIN_THREADS = 256;
+template <int D>
+constexpr int join_groups() { return JOIN_THREADS / (D / 4); }
+
+template <int D>
+struct JoinSpace {
+  float m[join_groups<D>()], l[join_groups<D>()];
+  float o[join_groups<D>()][D];
+};
+
+struct RowSum {
+  float m, l;
+  v4f o;
+};
+
+// part(first), part(first + step), ... below part(n), dims d .. d + 3 of row r;
+// AHEAD at a time, all loaded before the first is used
+template <class Part>
+__device__ __forceinline__ RowSum sum_partials(const Part& part, int first, int step, int n, int r, int d) {
+  constexpr int AHEAD = 8;
+  RowSum s = {LOWEST, 0.f, v4f{0.f, 0.f, 0.f, 0.f}};
+  for (int w = first; w < n; w += AHEAD * step) {
+    float m[AHEAD], l[AHEAD];
+    v4f v[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      m[i] = LOWEST;
+      l[i] = 0.f;
+      v[i] = v4f{0.f, 0.f, 0.f, 0.f};
+      if (w + i * step < n) {
+        const auto& x = part(w + i * step);
+        m[i] = x.m[r];
+        l[i] = x.l[r];
+        v[i] = *reinterpret_cast<const v4f*>(&x.o[r][d]);
+      }
+    }
+    float mn = s.m;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, m[i]);
+    const float b = __builtin_amdgcn_exp2f(s.m - mn);
+    s.m = mn;
+    s.l *= b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s.o[j] *= b;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const float a = __builtin_amdgcn_exp2f(m[i] - mn);
+      s.l += l[i] * a;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s.o[j] += v[i][j] * a;
+    }
+  }
+  return s;
+}
+
+// Rows r0, r0 + step, ... < rows of n partial results part(0 .. n - 1);
+// finish(r, d, l, o) gets a row's sum and dims d .. d + 3 of its output
+template <int D, class Part, class Finish>
+__device__ __forceinline__ void join_rows(JoinSpace<D>& lds, int r0, int step, int rows, int n, const Part& part, const Finish& finish) {
+  constexpr int LANES = D / 4, JOIN = join_groups<D>();
+  const int g = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
+  if (n <= 8) {
+    for (int r = r0 + step * g; r < rows; r += step * JOIN) {
+      const RowSum s = sum_partials(part, 0, 1, n, r, d);
+      finish(r, d, s.l, s.o);
+    }
+    return;
+  }
+  for (int r = r0; r < rows; r += step) {
+    RowSum s = sum_partials(part, g, JOIN, n, r, d);
+    if (d == 0) {
+      lds.m[g] = s.m;
+      lds.l[g] = s.l;
+    }
+    *reinterpret_cast<v4f*>(&lds.o[g][d]) = s.o;
+    __syncthreads();
+    if (g == 0) {
+      s.m = lds.m[0];
+#pragma unroll
+      for (int i = 1; i < JOIN; ++i) s.m = fmaxf(s.m, lds.m[i]);
+      s.l = 0.f;
+      s.o = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < JOIN; ++i) {
+        const float a = __builtin_amdgcn_exp2f(lds.m[i] - s.m);
+        s.l += lds.l[i] * a;
+        const v4f v = *reinterpret_cast<const v4f*>(&lds.o[i][d]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s.o[j] += v[j] * a;
+      }
+      finish(r, d, s.l, s.o);
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace attn
 }  // namespace
 }  // namespace iqp

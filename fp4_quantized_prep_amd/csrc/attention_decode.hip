@@ -412,61 +412,12 @@ void attention_decode_kernel(AttnArgs p) {
 // Joins the pairs whose units went to more than one workgroup. Workgroup (x, z)
 // takes every gridDim.y-th row from z on of one pair: the pair that decode
 // workgroup x began and did not finish, or (BY_PAIR, where the pairs are fewer
-// than the decode workgroups) pair x itself. A group of D / 4 lanes sums up
-// partial results of a row: all of them where they are few (every group then
-// has a row of its own), else every JOIN-th, and the groups meet in LDS.
-constexpr int JOIN_THREADS = 256;
-
-// partial results first, first + step, ... <= w1 of row r, dims d .. d + 3;
-// AHEAD at a time, all loaded before the first is used
-template <int D, int NT>
-__device__ __forceinline__ void sum_partials(const Partial<D, NT>* parts, int64_t first, int64_t step, int64_t w0, int64_t w1,
-                                             int r, int d, float& mx, float& sum, v4f& acc) {
-  constexpr int AHEAD = 8;
-  mx = LOWEST;
-  sum = 0.f;
-  acc = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int64_t w = first; w <= w1; w += AHEAD * step) {
-    float m[AHEAD], l[AHEAD];
-    v4f v[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      m[i] = LOWEST;
-      l[i] = 0.f;
-      v[i] = v4f{0.f, 0.f, 0.f, 0.f};
-      const int64_t x = w + i * step;
-      if (x <= w1) {
-        const Partial<D, NT>& part = parts[2 * x + (x == w0 ? 1 : 0)];
-        m[i] = part.m[r];
-        l[i] = part.l[r];
-        v[i] = *reinterpret_cast<const v4f*>(&part.o[r][d]);
-      }
-    }
-    float mn = mx;
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, m[i]);
-    const float b = __builtin_amdgcn_exp2f(mx - mn);
-    mx = mn;
-    sum *= b;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] *= b;
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const float a = __builtin_amdgcn_exp2f(m[i] - mn);
-      sum += l[i] * a;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += v[i][j] * a;
-    }
-  }
-}
-
+// than the decode workgroups) pair x itself.
 template <int D, int NT, bool BY_PAIR>
 __global__ __launch_bounds__(JOIN_THREADS)
 void attention_join_kernel(AttnArgs p) {
-  constexpr int ROWS = 16 * NT, LANES = D / 4, JOIN = JOIN_THREADS / LANES;
-  __shared__ float lds_m[JOIN], lds_l[JOIN];
-  __shared__ __attribute__((aligned(16))) float lds_o[JOIN][D];
-  const int tid = threadIdx.x;
+  constexpr int ROWS = 16 * NT;
+  __shared__ __attribute__((aligned(16))) JoinSpace<D> lds;
   Line<ROWS> line(p);
   if (line.total == 0) return;                               // no sequence is this kernel's
   const int64_t per = piece_of(line.total);
@@ -488,48 +439,16 @@ void attention_join_kernel(AttnArgs p) {
   if (w0 == w1 || (!BY_PAIR && w0 != blockIdx.x)) return;    // finished by its workgroup, or begun before this one
   const int64_t tile = quotient(pair, p.Hk), rows = (int64_t)(q.r.end - q.r.begin) * p.group;
   const int head = (int)(pair - tile * p.Hk);
-  const Partial<D, NT>* parts = reinterpret_cast<const Partial<D, NT>*>(p.workspace);
-  const int g = tid / LANES, d = 4 * (tid % LANES);
-  float mx, sum;
-  v4f acc;
-  auto finish = [&](int r) __attribute__((always_inline)) {
-    const float inv = inverse_sum(sum);
-    uint16_t* dst = p.out + row_offset(q.r.begin, tile * ROWS + r, head, p.group, D, p.ldo) + d;
-    *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
-  };
-  if (w1 - w0 < 8) {
-    for (int r = blockIdx.y + gridDim.y * g; r < ROWS && tile * ROWS + r < rows; r += gridDim.y * JOIN) {
-      sum_partials<D, NT>(parts, w0, 1, w0, w1, r, d, mx, sum, acc);
-      finish(r);
-    }
-    return;
-  }
-  for (int r = blockIdx.y; r < ROWS && tile * ROWS + r < rows; r += gridDim.y) {
-    sum_partials<D, NT>(parts, w0 + g, JOIN, w0, w1, r, d, mx, sum, acc);
-    if (d == 0) {
-      lds_m[g] = mx;
-      lds_l[g] = sum;
-    }
-    *reinterpret_cast<v4f*>(&lds_o[g][d]) = acc;
-    __syncthreads();
-    if (g == 0) {
-      mx = lds_m[0];
-#pragma unroll
-      for (int i = 1; i < JOIN; ++i) mx = fmaxf(mx, lds_m[i]);
-      sum = 0.f;
-      acc = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < JOIN; ++i) {
-        const float a = __builtin_amdgcn_exp2f(lds_m[i] - mx);
-        sum += lds_l[i] * a;
-        const v4f v = *reinterpret_cast<const v4f*>(&lds_o[i][d]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] += v[j] * a;
-      }
-      finish(r);
-    }
-    __syncthreads();
-  }
+  const Partial<D, NT>* parts = reinterpret_cast<const Partial<D, NT>*>(p.workspace) + 2 * w0;
+  const int64_t left = rows - tile * ROWS;
+  join_rows<D>(
+      lds, blockIdx.y, gridDim.y, left < ROWS ? (int)left : ROWS, (int)(w1 - w0) + 1,
+      [&](int i) __attribute__((always_inline)) -> const Partial<D, NT>& { return parts[2 * i + (i == 0 ? 1 : 0)]; },
+      [&](int r, int d, float sum, v4f acc) __attribute__((always_inline)) {
+        const float inv = inverse_sum(sum);
+        uint16_t* dst = p.out + row_offset(q.r.begin, tile * ROWS + r, head, p.group, D, p.ldo) + d;
+        *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+      });
 }
 
 template <int D, int NT>

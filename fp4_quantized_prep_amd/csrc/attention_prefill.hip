@@ -428,34 +428,26 @@ void attention_prefill_kernel(AttnArgs p, int splits) {
   Prefill<D>::run(p, splits, lds);
 }
 
-// Joins the pieces of a split launch: a workgroup per row tile, key head and 16 rows
+// Joins the pieces of a split launch: workgroup (x, y) takes every gridDim.y-th
+// row from y on of row tile and key head x
 template <int D>
-__global__ __launch_bounds__(256)
+__global__ __launch_bounds__(JOIN_THREADS)
 void attention_prefill_join_kernel(AttnArgs p, int splits) {
+  __shared__ __attribute__((aligned(16))) JoinSpace<D> lds;
   const int64_t item = blockIdx.x / (unsigned)p.Hk;
   const int head = (int)(blockIdx.x % (unsigned)p.Hk);
   Work w;
   if (!find_work(p, item, w)) return;
-  const PartialTile<D>* const parts = reinterpret_cast<const PartialTile<D>*>(p.workspace);
-  for (int i = threadIdx.x; i < 16 * (D / 4); i += 256) {
-    const int r = 16 * blockIdx.y + i / (D / 4), d = 4 * (i % (D / 4));
-    if (w.row0 + r >= w.rows) break;
-    float mx = LOWEST;
-    for (int z = 0; z < splits; ++z) mx = fmaxf(mx, parts[(item * splits + z) * p.Hk + head].m[r]);
-    float sum = 0.f;
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    for (int z = 0; z < splits; ++z) {
-      const PartialTile<D>& x = parts[(item * splits + z) * p.Hk + head];
-      const float a = __builtin_amdgcn_exp2f(x.m[r] - mx);
-      sum += x.l[r] * a;
-      const v4f v = *reinterpret_cast<const v4f*>(&x.o[r][d]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += v[j] * a;
-    }
-    const float inv = inverse_sum(sum);
-    uint16_t* const dst = p.out + row_offset(w.begin, w.row0 + r, head, p.group, D, p.ldo) + d;
-    *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
-  }
+  const PartialTile<D>* const parts = reinterpret_cast<const PartialTile<D>*>(p.workspace) + item * splits * p.Hk + head;
+  const int64_t left = w.rows - w.row0;
+  join_rows<D>(
+      lds, blockIdx.y, gridDim.y, left < PROWS ? (int)left : PROWS, splits,
+      [&](int z) __attribute__((always_inline)) -> const PartialTile<D>& { return parts[(int64_t)z * p.Hk]; },
+      [&](int r, int d, float sum, v4f acc) __attribute__((always_inline)) {
+        const float inv = inverse_sum(sum);
+        uint16_t* const dst = p.out + row_offset(w.begin, w.row0 + r, head, p.group, D, p.ldo) + d;
+        *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+      });
 }
 
 template <int D>
@@ -471,7 +463,7 @@ hipError_t launch(const AttnArgs& p, hipStream_t stream) {
   hipLaunchKernelGGL((attention_prefill_kernel<D>), dim3((unsigned)(pairs * splits)), dim3(PWAVES * 64), 0, stream, p, (int)splits);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL((attention_prefill_join_kernel<D>), dim3((unsigned)pairs, PROWS / 16), dim3(256), 0, stream, p, (int)splits);
+  hipLaunchKernelGGL((attention_prefill_join_kernel<D>), dim3((unsigned)pairs, 16), dim3(JOIN_THREADS), 0, stream, p, (int)splits);
   return hipGetLastError();
 }
 
