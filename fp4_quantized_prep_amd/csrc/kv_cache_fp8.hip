@@ -70,6 +70,9 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float mul) {
   return (uint32_t)r;
 }
 
+// the bytes of a dword below n
+__device__ __forceinline__ uint32_t byte_mask(int n) { return n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u; }
+
 // eight E4M3 codes times mul, as bf16
 __device__ __forceinline__ v4u widen8(v2u c, float mul) {
   v4u o;
@@ -117,10 +120,20 @@ void kv_append_kernel(KvAppendArgs p) {
   }
   if (!held(p.seq, sh.block)) return;               // uniform over the workgroup
   const int64_t slot = sh.block * p.Hk + head;
+  uint8_t* const kb = p.k_cache + slot * B * D;
+  uint8_t* const vb = p.v_cache + slot * B * D;
   int old[2] = {0, 0};
   if (sh.lo > 0) {
     old[0] = (int)p.k_scales[slot] - 127;
     old[1] = (int)p.v_scales[slot] - 127;
+  }
+  // 16 tokens of a value dim, c of them from c0 to c1, are a piece; the thread's
+  // first one, if it holds codes that stay: on its way while the maximum is found
+  const int c0 = sh.lo >> 4, c1 = (sh.hi + 15) >> 4;
+  v4u kept = {0u, 0u, 0u, 0u};
+  {
+    const int c = c0 + tid % (c1 - c0), d = tid / (c1 - c0);
+    if (d < D && (sh.lo > 16 * c || sh.hi < 16 * c + 16)) kept = *reinterpret_cast<const v4u*>(vb + d * B + 16 * c);
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
@@ -150,8 +163,6 @@ void kv_append_kernel(KvAppendArgs p) {
     p.v_scales[slot] = (uint8_t)(e[1] + 127);
   }
 
-  uint8_t* const kb = p.k_cache + slot * B * D;
-  uint8_t* const vb = p.v_cache + slot * B * D;
   // keys: the new rows, then the earlier ones where the exponent grew
   const float km = pow2(-e[0]), vm = pow2(-e[1]);
 #pragma unroll
@@ -176,35 +187,25 @@ void kv_append_kernel(KvAppendArgs p) {
     }
   }
   __syncthreads();
-  // values: 16 tokens of a dim at a time; a piece that lies inside what is
-  // written goes out whole, the others byte by byte
+  // values, piece by piece: what is neither new nor rescaled goes back as it was
   const float mul = grown[1] ? pow2(max(old[1] - e[1], -126)) : 1.f;
-  const int from = grown[1] ? 0 : sh.lo;            // the first token whose code is written
-  const int c0 = from >> 4, c1 = (sh.hi + 15) >> 4;
-  for (int i = tid; i < D * (c1 - c0); i += KV_THREADS) {
-    const int c = c0 + i % (c1 - c0), d = i / (c1 - c0);
+  const int first = grown[1] ? 0 : c0;              // the first piece that is written
+  for (int i = tid; i < D * (c1 - first); i += KV_THREADS) {
+    const int c = first + i % (c1 - first), d = i / (c1 - first);
     uint8_t* const dst = vb + d * B + 16 * c;
     const uint32_t* src = reinterpret_cast<const uint32_t*>(turned + d * (MAX_B + PAD) + 16 * c);
     const int a = sh.lo - 16 * c, z = sh.hi - 16 * c;     // bytes [a, z) are new
     v4u w = {src[0], src[1], src[2], src[3]};
-    if (a > 0) {                                           // bytes before a: the old codes
-      const v4u o = *reinterpret_cast<const v4u*>(dst);
+    if (a > 0 || z < 16) {
+      const v4u o = i == tid && !grown[1] ? kept : *reinterpret_cast<const v4u*>(dst);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t g = rescale4(o[j], mul);
-        const int keep = min(max(a - 4 * j, 0), 4);
-        const uint32_t mask = keep >= 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
-        w[j] = (g & mask) | (w[j] & ~mask);
+        const uint32_t below = byte_mask(a - 4 * j), upto = byte_mask(z - 4 * j);
+        const uint32_t g = grown[1] ? rescale4(o[j], mul) : o[j];
+        w[j] = (g & below) | (w[j] & upto & ~below) | (o[j] & ~upto);
       }
     }
-    const int b0 = max(from - 16 * c, 0), b1 = min(z, 16);
-    if (b0 == 0 && b1 == 16) {
-      *reinterpret_cast<v4u*>(dst) = w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (j >= b0 && j < b1) dst[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
-    }
+    *reinterpret_cast<v4u*>(dst) = w;
   }
 }
 
