@@ -71,6 +71,9 @@ __device__ __forceinline__ bool find_work(const AttnArgs& p, int64_t item, Work&
   return true;
 }
 
+// bits 0 .. n - 1, none below 0, all from 32 on
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : (1u << (n < 0 ? 0 : n)) - 1u; }
+
 // fmaxf of three in one instruction (the compiler would quiet each operand first)
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -284,12 +287,17 @@ struct Prefill {
       load();
       __builtin_amdgcn_sched_barrier(0);
       if (t0 + U > all_hi || t0 < all_lo || g.held != (1 << GR) - 1) {
+        // a bit a token: those of the unit that the row sees, the lane's 8 of each
+        // granule, the held granules'; then two instructions a score
+        const uint32_t w0 = below(see_hi - t0) & ~below(see_lo - t0), w1 = below(see_hi - t0 - 32) & ~below(see_lo - t0 - 32);
+        const uint32_t bits = __builtin_amdgcn_perm(w1, w0, 0x06040200u + 0x01010101u * half) &
+                              (((uint32_t)g.held * 0x00204081u & 0x01010101u) * 255u);
 #pragma unroll
         for (int a = 0; a < NA; ++a)
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int tok = t0 + 32 * a + 16 * (r >> 3) + 8 * half + (r & 7);
-            sc[a][r] = (g.held >> (2 * a + (r >> 3)) & 1) && tok >= see_lo && tok < see_hi ? sc[a][r] : -INFINITY;
+            const uint32_t sees = (uint32_t)((int)(bits << (31 - (16 * a + r))) >> 31);
+            sc[a][r] = __uint_as_float((sees & __float_as_uint(sc[a][r])) | (~sees & 0xFF800000u));   // or -inf
           }
       }
       // the maximum, granule by granule (one factor each)
