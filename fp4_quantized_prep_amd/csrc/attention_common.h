@@ -46,6 +46,12 @@ __device__ __forceinline__ v4u clear_outside(v4u v, int lo, int hi) {
 // 1 / sum of a row's weights: 0 where it saw nothing, NaN kept
 __device__ __forceinline__ float inverse_sum(float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); }
 
+// the most tokens that a row can see
+inline int64_t reach(const AttnArgs& p) {
+  const int64_t held = (int64_t)p.seq.max_blocks << p.seq.log_block;
+  return p.window > 0 && p.window < held ? p.window : held;
+}
+
 // Where row `row` (token-major: token * group + query head of the group) of key
 // head `head` lies in q and out: element offset for row stride ld.
 __device__ __forceinline__ int64_t row_offset(int64_t begin, int64_t row, int head, int group, int D, int64_t ld) {

@@ -490,7 +490,7 @@ hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream) {
     return launch_attention_decode(p, D, stream);
   }
   // (a single sequence needs one kernel, whatever its number of rows turns out to be)
-  const bool alone = p.seq.S == 1 || ((int64_t)p.seq.max_blocks << p.seq.log_block) <= ATTN_SHORT_TABLE;
+  const bool alone = p.seq.S == 1 || reach(p) <= ATTN_SHORT_REACH;
   p.max_rows = alone ? 0 : ATTN_DECODE_ROWS;
   const hipError_t e = launch_attention_prefill(p, D, stream);
   if (e != hipSuccess || alone) return e;

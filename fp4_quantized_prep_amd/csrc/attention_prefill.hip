@@ -461,12 +461,12 @@ void attention_prefill_join_kernel(AttnArgs p, int splits) {
 template <int D>
 hipError_t launch(const AttnArgs& p, hipStream_t stream) {
   const int64_t items = ((p.seq.T * p.group) >> 7) + p.seq.S, pairs = items * p.Hk;
-  // split where the row tiles leave CUs idle and the table allows for pieces of
+  // split where the row tiles leave CUs idle and the rows see enough for pieces of
   // at least four units (200 rows of 8 heads over 2 after 1800 tokens: 17.4 us, with
   // eight units 21.5; with up to 1024 workgroups instead of 512, 1250 rows of
   // 32 heads over 4, D 64, take 44 us instead of 35: the partial results' way
   // through memory costs more than the CUs gain)
-  const int64_t longest = ((int64_t)p.seq.max_blocks << p.seq.log_block) / (4 * UNIT);
+  const int64_t longest = reach(p) / (4 * UNIT);
   int64_t splits = SPLIT_GROUPS / pairs;
   if (splits > longest) splits = longest;
   if (splits < 1) splits = 1;

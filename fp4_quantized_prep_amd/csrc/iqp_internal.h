@@ -283,9 +283,10 @@ constexpr int ATTN_WORKGROUPS = 512;
 // Sequences of more than ATTN_DECODE_ROWS rows are the prompt kernel's, in a
 // batch that has more than that on average; else all are the decode kernel's.
 constexpr int ATTN_DECODE_ROWS = 64;
-// Where the table holds no more tokens than this, the prompt kernel takes such a
-// batch's short sequences too: their few units cost less than two more launches.
-constexpr int ATTN_SHORT_TABLE = 1024;
+// Where a row sees no more tokens than this (the table, or the window), the prompt
+// kernel takes such a batch's short sequences too: their few units cost less than
+// two more launches that mostly find nothing (9 us where they find nothing at all).
+constexpr int ATTN_SHORT_REACH = 1024;
 int64_t attention_decode_workspace_bytes(int D);
 int64_t attention_prefill_workspace_bytes(int D);
 hipError_t launch_attention_decode(const AttnArgs& args, int D, hipStream_t stream);

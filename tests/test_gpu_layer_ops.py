@@ -357,6 +357,16 @@ def test_attention_prompts_over_a_long_table(gpu_lib, lens, new, hq, h, d, block
     attend(gpu_lib, gen(18, len(lens), lens[0], new[0], hq), lens, new, hq, h, d, block, 0, tail=1)
 
 
+@pytest.mark.parametrize("window", [100, 700])
+@pytest.mark.parametrize("hq,h,d", [(4, 2, 128), (8, 1, 64)])
+def test_attention_short_window_in_a_long_table(gpu_lib, hq, h, d, window):
+    """A window that keeps a batch with short sequences in one kernel, and a
+    single sequence whose rows see too little to be split far."""
+    print("attend window", hq, d, window, flush=True)
+    attend(gpu_lib, gen(21, hq, window), [1500, 1203, 1100, 40], [200, 1, 90, 3], hq, h, d, 64, window, tail=2, nan_codes=True)
+    attend(gpu_lib, gen(22, hq, window), [2000], [70], hq, h, d, 16, window)
+
+
 def test_attention_many_sequences(gpu_lib):
     """More sequences than a wave has lanes, some without rows."""
     g = gen(19)
