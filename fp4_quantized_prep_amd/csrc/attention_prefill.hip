@@ -1,17 +1,21 @@
 // Attention of many query rows per sequence (prompts and their continuations)
 // over the FP8 key/value cache: the formula of attention_decode.hip.
 //
-// Matrix-core bound: 4 D operations a visible (row, token) pair. A workgroup of
-// four waves takes 128 rows (query heads of one key head by tokens, 32 a wave)
-// and walks the visible tokens in units of 64:
-//   * the unit's codes are loaded once (16 bytes a lane), widened once (keys
-//     to bf16, values to fp16, both exact) and put in LDS, two units deep with one
-//     barrier a unit, while the previous unit is computed;
+// Bound by the matrix cores and the vector instructions of the softmax
+// together: 4 D operations a visible (row, token) pair on the former, about five
+// instructions on the latter, which take as long at D 128 and twice as long at
+// D 64. A workgroup's four waves take 128 rows (query heads of one key head by
+// tokens, 32 a wave) and walk the visible tokens in units of 64:
+//   * a unit's codes are loaded once (16 bytes a lane) two units ahead, widened
+//     once (keys to bf16, values to fp16, both exact) and put in LDS beside the
+//     score MFMAs of the unit before; one barrier a unit;
 //   * 32x32x16 MFMAs, tokens as the rows of the score product and dims as the
 //     rows of the second one, query rows as columns of both. Score row
 //     8 a + 4 h + b is token 16 (a / 2) + 8 h + 4 (a % 2) + b of its 32, so that
 //     lane half h holds 8 consecutive tokens of each 16 and its scores are
-//     already the second product's operand: probabilities never leave the lane;
+//     already the second product's operand: probabilities never leave the lane.
+//     The weights of 16 tokens are computed beside the second product of the 16
+//     before;
 //   * a unit's four 16-token granules lie in one block each, so block numbers,
 //     scales and whether they are held are scalars. Key scales multiply the
 //     scores, value exponents go into the probabilities' exponents (see
@@ -20,9 +24,13 @@
 //     bytes, c ^ (row / 2) % 8 in rows of 128), so that the 16
 //     lanes of a read cycle meet distinct banks.
 // Workgroups are numbered with the key head fastest, so that with 8 heads an
-// XCD's L2 holds one head's cache, longest row tiles first. Few rows against a
-// long cache are split into Z pieces of the token range, joined by a second
-// launch.
+// XCD's L2 holds one head's cache, longest row tiles first. Where there are few,
+// SETS = 2 gives a workgroup eight waves, of which four take the first half of
+// the tokens and four the second, joined in LDS; where there are very few, the
+// token range is split into Z pieces, joined by a second launch.
+//
+// Measured: 4632 tokens, 64 heads of 128 over 8: 380 us, 0.92 PFLOP/s (MFMAs alone
+// 190 us of it; a large bf16 product of the library reaches 1.39).
 #include <type_traits>
 
 #include "attention_common.h"
@@ -91,7 +99,7 @@ __device__ __forceinline__ float sum_halves(float v) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
-template <int D>
+template <int D, int SETS>
 struct Prefill {
   static constexpr int U = UNIT, GR = U / 16;   // tokens of a unit, its granules
   static constexpr int KS = D / 16;             // MFMA steps of a score
@@ -99,7 +107,7 @@ struct Prefill {
   static constexpr int LOADS = D / 64;          // 16-byte pieces of keys (and of values) a thread and unit
   static constexpr int DT = D / 32;             // output tiles
   static constexpr int K_BYTES = U * D * 2, V_BYTES = D * U * 2;
-  static constexpr int LDS_BYTES = 2 * (K_BYTES + V_BYTES);
+  static constexpr int SET_BYTES = 2 * (K_BYTES + V_BYTES), LDS_BYTES = SETS * SET_BYTES;
 
   // permutation of a key row's 16-byte chunks: rows of 256 bytes cover all
   // banks, rows of 128 half of them
@@ -117,9 +125,11 @@ struct Prefill {
                   // load, so that nothing waits for the codes loaded behind them
   };
 
-  static __device__ __forceinline__ void run(const AttnArgs& p, int splits, uint8_t* lds) {
-    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
+  static __device__ __forceinline__ void run(const AttnArgs& p, int splits, uint8_t* lds_all) {
+    const int tid = threadIdx.x % (64 * PWAVES), lane = tid & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int set = SETS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * PWAVES));
+    uint8_t* const lds = lds_all + set * SET_BYTES;
     const int head = (int)(blockIdx.x % (unsigned)p.Hk);
     const int64_t rest = blockIdx.x / (unsigned)p.Hk;
     const int z = (int)(rest % splits);
@@ -134,9 +144,12 @@ struct Prefill {
     for (int k = 0; k < KS; ++k) fq[k] = *reinterpret_cast<const v8bf*>(p.q + src + 16 * k + 8 * half);
     // tokens relative to the unit range's first, 32 bits wide
     const int64_t u_lo = w.lo / U, u_hi = w.hi > w.lo ? (w.hi + U - 1) / U : u_lo;
-    const int64_t u0 = u_lo + (u_hi - u_lo) * z / splits, u1 = u_lo + (u_hi - u_lo) * (z + 1) / splits;
+    const int64_t cuts = (int64_t)SETS * splits, cut = (int64_t)SETS * z + set;
+    const int64_t u0 = u_lo + (u_hi - u_lo) * cut / cuts, u1 = u_lo + (u_hi - u_lo) * (cut + 1) / cuts;
     const int64_t base = u0 * U;
     const int units = (int)(u1 - u0);
+    // rounds of the workgroup: a set with a unit less computes one of which nothing is held
+    const int turns = SETS == 1 ? units : (int)((u_hi - u_lo + cuts - 1) / cuts);
     const int64_t pos = w.len - w.n + rc / p.group;
     const int see_hi = (int)(pos + 1 - base < -1 ? -1 : pos + 1 - base);
     const int64_t lo64 = p.window > 0 ? pos + 1 - p.window - base : -1;
@@ -361,7 +374,7 @@ struct Prefill {
       for (int i = 0; i < GR; ++i) l = __builtin_fmaf(sum[i], vinv_of(g, i), l);
     };
 
-    if (units > 0) {
+    if (turns > 0) {
       int blk1 = load_block(1), blk2;        // the next unit's blocks, and the one's after it
       Granules g0, g1;
       Codes c;
@@ -374,18 +387,18 @@ struct Prefill {
 #pragma unroll
         for (int j = 0; j < 4 * LOADS; ++j) store_codes(c, j, std::integral_constant<int, 0>{});
       }
-      if (units > 1) {
+      if (turns > 1) {
         g1 = load_granules(blk1);
         c = load_codes(1, blk1);
       }
       __syncthreads();
       auto unit = [&](int u, auto buf) __attribute__((always_inline)) {
         const Granules g = g0;
-        if (u + 1 < units) clear_codes(u + 1, c, blk1);
+        if (u + 1 < turns) clear_codes(u + 1, c, blk1);
         g0 = g1;
         compute(u, scales_of(g), c, buf, [&]() __attribute__((always_inline)) {
           blk1 = blk2;
-          if (u + 2 < units) {
+          if (u + 2 < turns) {
             g1 = load_granules(blk1);
             c = load_codes(u + 2, blk1);
             blk2 = load_block(u + 3);
@@ -394,13 +407,40 @@ struct Prefill {
         __syncthreads();   // unit u + 1 is in LDS; unit u is read by every wave
       };
       int u = 0;
-      for (; u + 1 < units; u += 2) {
+      for (; u + 1 < turns; u += 2) {
         unit(u, std::integral_constant<int, 0>{});
         unit(u + 1, std::integral_constant<int, 1>{});
       }
-      if (u < units) unit(u, std::integral_constant<int, 0>{});
+      if (u < turns) unit(u, std::integral_constant<int, 0>{});
     }
 
+    if constexpr (SETS > 1) {
+      // the sets' results, lane for lane: the second's go through LDS
+      constexpr int THREADS = 64 * PWAVES;
+      v4f* const to = reinterpret_cast<v4f*>(lds_all) + tid;
+      float* const stats = reinterpret_cast<float*>(lds_all + 16 * THREADS * 4 * DT) + tid;
+      if (set > 0) {
+        stats[0] = m;
+        stats[THREADS] = l;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+          for (int a = 0; a < 4; ++a) to[(4 * t + a) * THREADS] = v4f{o[t][4 * a], o[t][4 * a + 1], o[t][4 * a + 2], o[t][4 * a + 3]};
+      }
+      __syncthreads();
+      if (set > 0) return;
+      const float m1 = stats[0], mn = fmaxf(m, m1), a0 = __builtin_amdgcn_exp2f(m - mn), a1 = __builtin_amdgcn_exp2f(m1 - mn);
+      m = mn;
+      l = l * a0 + stats[THREADS] * a1;
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const v4f x = to[(4 * t + a) * THREADS];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][4 * a + e] = o[t][4 * a + e] * a0 + x[e] * a1;
+        }
+    }
     l = sum_halves(l);
     if (row >= w.rows) return;
     if (splits == 1) {
@@ -429,11 +469,11 @@ struct Prefill {
   }
 };
 
-template <int D>
-__global__ __launch_bounds__(PWAVES * 64, D == 64 ? 3 : 2)
+template <int D, int SETS>
+__global__ __launch_bounds__(SETS * PWAVES * 64, D == 64 && SETS == 1 ? 3 : 2)
 void attention_prefill_kernel(AttnArgs p, int splits) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[Prefill<D>::LDS_BYTES];
-  Prefill<D>::run(p, splits, lds);
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Prefill<D, SETS>::LDS_BYTES];
+  Prefill<D, SETS>::run(p, splits, lds);
 }
 
 // Joins the pieces of a split launch: workgroup (x, y) takes every gridDim.y-th
@@ -461,17 +501,25 @@ void attention_prefill_join_kernel(AttnArgs p, int splits) {
 template <int D>
 hipError_t launch(const AttnArgs& p, hipStream_t stream) {
   const int64_t items = ((p.seq.T * p.group) >> 7) + p.seq.S, pairs = items * p.Hk;
-  // split where the row tiles leave CUs idle and the rows see enough for pieces of
-  // at least four units (200 rows of 8 heads over 2 after 1800 tokens: 17.4 us, with
-  // eight units 21.5; with up to 1024 workgroups instead of 512, 1250 rows of
-  // 32 heads over 4, D 64, take 44 us instead of 35: the partial results' way
-  // through memory costs more than the CUs gain)
+  // Up to 128 workgroups: split, into pieces of at least four units where the rows
+  // may see that many (200 rows of 8 heads over 2 after 1800 tokens: 17.4 us, with
+  // eight units 21.5; with up to 1024 workgroups instead of 512, 1250 rows of 32
+  // heads over 4, D 64, take 44 us instead of 35: the partial results' way
+  // through memory costs more than the CUs gain). Up to 512, which leave CUs a
+  // workgroup or two: two sets of waves in each (us with two sets / one / split:
+  // 1000 rows of 32 heads over 4, D 128, 26.4 / - / 36.4; 1500 rows over 8 heads
+  // 37 / 43 / 57; 1250 rows, D 64, 28 / 33 / 43). More: one set (4632 rows of
+  // 64 heads 382, with two sets 428).
   const int64_t longest = reach(p) / (4 * UNIT);
-  int64_t splits = SPLIT_GROUPS / pairs;
+  int64_t splits = pairs > 128 ? 1 : SPLIT_GROUPS / pairs;
   if (splits > longest) splits = longest;
   if (splits < 1) splits = 1;
+  const bool two = splits == 1 && pairs <= 512;
   if (pairs * splits > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attention_prefill_kernel<D>), dim3((unsigned)(pairs * splits)), dim3(PWAVES * 64), 0, stream, p, (int)splits);
+  if (two)
+    hipLaunchKernelGGL((attention_prefill_kernel<D, 2>), dim3((unsigned)(pairs * splits)), dim3(2 * PWAVES * 64), 0, stream, p, (int)splits);
+  else
+    hipLaunchKernelGGL((attention_prefill_kernel<D, 1>), dim3((unsigned)(pairs * splits)), dim3(PWAVES * 64), 0, stream, p, (int)splits);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   hipLaunchKernelGGL((attention_prefill_join_kernel<D>), dim3((unsigned)pairs, 16), dim3(JOIN_THREADS), 0, stream, p, (int)splits);

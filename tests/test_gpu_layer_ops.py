@@ -357,6 +357,15 @@ def test_attention_prompts_over_a_long_table(gpu_lib, lens, new, hq, h, d, block
     attend(gpu_lib, gen(18, len(lens), lens[0], new[0], hq), lens, new, hq, h, d, block, 0, tail=1)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_prompts_that_fill_the_chip(gpu_lib, d):
+    """So many row tiles that a workgroup has one set of waves and no split."""
+    print("attend many tiles", d, flush=True)
+    g = gen(23, d)
+    lens = [int(x) for x in g.integers(66, 200, 18)]
+    attend(gpu_lib, g, lens, [min(n, 66 + i) for i, n in enumerate(lens)], 32, 32, d, 32, tail=1, nan_codes=True)
+
+
 @pytest.mark.parametrize("window", [100, 700])
 @pytest.mark.parametrize("hq,h,d", [(4, 2, 128), (8, 1, 64)])
 def test_attention_short_window_in_a_long_table(gpu_lib, hq, h, d, window):
