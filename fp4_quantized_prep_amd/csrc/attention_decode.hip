@@ -171,7 +171,7 @@ struct Partial {
 };
 
 template <int D, int NT>
-__global__ __launch_bounds__(DWAVES * 64, D == 128 && NT == 2 ? 1 : 2)
+__global__ __launch_bounds__(DWAVES * 64, 2)
 void attention_decode_kernel(AttnArgs p) {
   constexpr int ROWS = 16 * NT;
   constexpr int KP = D / 64;        // 64-dim groups: two MFMA steps each
@@ -468,14 +468,16 @@ hipError_t launch(const AttnArgs& p, hipStream_t stream) {
 }  // namespace
 
 int64_t attention_decode_workspace_bytes(int D) {
-  return (int64_t)ATTN_WORKGROUPS * 2 * (D == 64 ? sizeof(Partial<64, 2>) : sizeof(Partial<128, 2>));
+  return (int64_t)ATTN_WORKGROUPS * 2 * (D == 64 ? sizeof(Partial<64, 2>) : sizeof(Partial<128, 1>));
 }
 
 hipError_t launch_attention_decode(const AttnArgs& p, int D, hipStream_t stream) {
-  // two tiles of rows a wave once a sequence brings more than one on average
-  const bool two = p.seq.T * p.group > 16 * (int64_t)p.seq.S;
-  if (D == 64) return two ? launch<64, 2>(p, stream) : launch<64, 1>(p, stream);
-  return two ? launch<128, 2>(p, stream) : launch<128, 1>(p, stream);
+  // D 64: two tiles of rows a wave once a sequence brings more than one on average
+  // (60 sequences of 8000 tokens, 24 rows a head: 57 us, with one tile 85). D 128
+  // leaves no registers for that: one wave a SIMD, half as fast as reading the
+  // cache twice (8 sequences of 2000 tokens, 32 rows a head: 33 us against 19).
+  if (D == 128) return launch<128, 1>(p, stream);
+  return p.seq.T * p.group > 16 * (int64_t)p.seq.S ? launch<64, 2>(p, stream) : launch<64, 1>(p, stream);
 }
 
 int64_t attention_workspace_bytes(int D) {
