@@ -7,29 +7,16 @@
 // their block's power of two.
 //
 // Cache-bound: 2 D bytes a token and key head, read once for all the query
-// heads that share it. What the layout does about it:
-//   * the cache is cut into units of 64 tokens. A wave loads a unit's 128 D
-//     bytes with 16-byte loads straight into MFMA operand registers: a key
-//     operand lane holds 16 consecutive dims of a token, a value operand lane
-//     16 consecutive tokens of a dim (the cache keeps values that way). Token
-//     16 g + 4 c + r of the unit is row 4 g + r of score tile c, so the lane
-//     that holds four scores of each tile holds 16 consecutive tokens, and
-//     those are its share of the second product's operand: probabilities never
-//     leave the lane.
-//   * query rows are the MFMA's columns, NT tiles of 16: the query heads of
-//     one key head and their tokens.
-//   * the keys widen to bf16 (exact) and meet bf16 queries. The block's key
-//     scale multiplies the scores. The values widen to fp16 without their
-//     scale (every E4M3 value is one); the probabilities carry it instead:
-//     with w'_t = 2^(s_t + e_t - max(s + e)), s in units of log2 and e_t the
-//     value exponent, w' <= 1 rounds to fp16 (2^-11 relative, half of what
-//     bf16 would lose) and sum w = sum w' 2^-e, kept in float32.
-//   * all (sequence, row tile, key head) pairs' units form one line that is cut
-//     into equal pieces, one per workgroup, whatever the sequences' lengths.
-//     A piece covers the end of one pair, whole pairs, and the start of
-//     another; whole pairs are finished at once, the rest go to the workspace as
-//     (max, sum, unnormalised output) and a second small launch joins them.
-#include "attention_common.h"
+// heads that share it (attention_rows.h). All (sequence, row tile, key head)
+// pairs' units of 64 tokens form one line that is cut into equal pieces, one per
+// workgroup, whatever the sequences' lengths. A piece covers the end of one pair,
+// whole pairs, and the start of another; whole pairs are finished at once, the
+// rest go to the workspace as (max, sum, unnormalised output) and a second small
+// launch joins them.
+//
+// Measured, 64 heads of 128 over 8: 64 sequences of 127 to 8191 tokens 111 us,
+// 4.75 TB/s; one of 131072 56 us, 4.77 TB/s (a large copy reaches 5.1).
+#include "attention_rows.h"
 
 namespace iqp {
 namespace {
@@ -171,19 +158,8 @@ struct Partial {
 };
 
 template <int D, int NT>
-__global__ __launch_bounds__(DWAVES * 64, 2)
-void attention_decode_kernel(AttnArgs p) {
+__device__ __forceinline__ void decode(const AttnArgs& p, typename FewRows<D, NT, DWAVES>::Lds& lds) {
   constexpr int ROWS = 16 * NT;
-  constexpr int KP = D / 64;        // 64-dim groups: two MFMA steps each
-  constexpr int DT = D / 16;        // output tiles
-  __shared__ __attribute__((aligned(16))) float lds_o[DWAVES][ROWS][D + 4];
-  __shared__ float lds_m[DWAVES][ROWS], lds_l[DWAVES][ROWS];
-
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 15, g = lane >> 4;
-  const int kg = col >> 2;          // 16-token group of the lane's key rows
-
   Line<ROWS> line(p);
   if (line.total == 0) return;
   const int64_t per = piece_of(line.total);
@@ -196,205 +172,20 @@ void attention_decode_kernel(AttnArgs p) {
     line.advance(at);
     const Seq& q = line.q;
     const int64_t base = line.base;
-    const int s = q.r.s;
-    const int64_t q_begin = q.r.begin, q_n = q.r.end - q.r.begin, q_len = q.r.len;
     const int64_t pair = quotient(at - base, q.units);            // row tile and key head of the sequence
     const int64_t off = (at - base) - pair * q.units;
     const int64_t count = q.units - off < stop - at ? q.units - off : stop - at;
     const int64_t tile = quotient(pair, p.Hk);
     const int head = (int)(pair - tile * p.Hk);
-    const int64_t row0 = tile * ROWS, rows = q_n * p.group;
-
-    // the queries, and which tokens each column sees: [see_lo, see_hi)
-    v8bf fq[NT][2 * KP];
-    int64_t see_lo[NT], see_hi[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int64_t r = row0 + 16 * t + col;
-      const int64_t rc = r < rows ? r : rows - 1;
-      const int64_t i = rc / p.group;
-      const uint16_t* src = p.q + (q_begin + i) * p.ldq + ((int64_t)head * p.group + (rc - i * p.group)) * D + 16 * g;
-#pragma unroll
-      for (int k = 0; k < KP; ++k) {
-        fq[t][2 * k] = *reinterpret_cast<const v8bf*>(src + 64 * k);
-        fq[t][2 * k + 1] = *reinterpret_cast<const v8bf*>(src + 64 * k + 8);
-      }
-      const int64_t pos = q_len - q_n + i;
-      see_hi[t] = pos + 1;
-      see_lo[t] = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
-    }
-    // every column sees the tokens of [all_lo, all_hi)
-    const int64_t i_first = row0 / p.group, i_last = (row0 + ROWS - 1 < rows ? row0 + ROWS - 1 : rows - 1) / p.group;
-    const int64_t all_hi = q_len - q_n + i_first + 1;
-    const int64_t all_lo = p.window > 0 ? q_len - q_n + i_last + 1 - p.window : 0;
-    const int64_t tile_lo = p.window > 0 ? all_hi - p.window : 0;   // no column sees a token before this
-
-    float m[NT], l[NT];
-    v4f o[NT][DT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      m[t] = LOWEST;
-      l[t] = 0.f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[t][d] = v4f{0.f, 0.f, 0.f, 0.f};
-    }
-
-    const int32_t* table = p.seq.table + (int64_t)s * p.seq.ld_table;
-    const int lb = p.seq.log_block;
-    for (int64_t u = wave; u < count; u += DWAVES) {
-      const int64_t t0 = (q.unit0 + off + u) * UNIT;
-      // the block of the lane's key rows and the block of its value tokens
-      const int64_t bk = (t0 + 16 * kg) >> lb, bv = (t0 + 16 * g) >> lb;
-      int64_t pk = bk < p.seq.max_blocks ? table[bk] : -1;
-      int64_t pv = bv < p.seq.max_blocks ? table[bv] : -1;
-      const bool held = pv >= 0 && pv < p.seq.n_blocks && t0 + 16 * g < q_len;
-      pk = pk >= 0 && pk < p.seq.n_blocks ? pk : 0;
-      pv = pv >= 0 && pv < p.seq.n_blocks ? pv : 0;
-      const int inside = (1 << lb) - 1;
-      const uint8_t* kb = p.k_cache + ((pk * p.Hk + head) << lb) * D;
-      const uint8_t* vb = p.v_cache + ((pv * p.Hk + head) << lb) * D + ((t0 + 16 * g) & inside);
-      v4u kr[4][KP], vr[DT];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint8_t* src = kb + ((t0 + 16 * kg + 4 * c + (col & 3)) & inside) * D + 16 * g;
-#pragma unroll
-        for (int k = 0; k < KP; ++k) kr[c][k] = *reinterpret_cast<const v4u*>(src + 64 * k);
-      }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) vr[d] = *reinterpret_cast<const v4u*>(vb + ((int64_t)(16 * d + col) << lb));
-      const int ke = (int)p.k_scales[pv * p.Hk + head] - 127, ve = (int)p.v_scales[pv * p.Hk + head] - 127;
-      const float kmul = p.scale_log2 * pow2(min(max(ke, -126), 127));
-      const float ve_f = (float)ve, vinv = pow2(min(max(-ve, -126), 127));
-
-      // scores: tile c, row 4 g + r is token 16 g + 4 c + r
-      v4f sc[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int k = 0; k < KP; ++k) {
-          const v8bf k0 = widen_bf16(kr[c][k][0], kr[c][k][1]), k1 = widen_bf16(kr[c][k][2], kr[c][k][3]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, fq[t][2 * k], sc[t][c], 0, 0, 0);
-            sc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, fq[t][2 * k + 1], sc[t][c], 0, 0, 0);
-          }
-        }
-      const bool edge = t0 < all_lo || t0 + UNIT > all_hi || t0 + UNIT > q_len;
-      // a block that is not held, or an edge: some token of the unit is out
-      if (edge || __ballot(!held) != 0) {
-        const int64_t tb = t0 + 16 * g;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int64_t tok = tb + 4 * c + r;
-              const bool in = held && tok >= see_lo[t] && tok < see_hi[t];
-              sc[t][c][r] = in ? sc[t][c][r] * kmul + ve_f : -INFINITY;
-            }
-        // whatever lies behind the sequence, before every row's window or in a
-        // block that is not held must not reach the product: 0 * NaN
-        const int64_t vhi = held ? q_len - tb : 0, vlo = tile_lo - tb;
-        const int hi = vhi > 16 ? 16 : (int)vhi, lo = vlo > 16 ? 16 : (int)vlo;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) vr[d] = clear_outside(vr[d], lo, hi);
-      } else {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sc[t][c][r] = sc[t][c][r] * kmul + ve_f;
-      }
-      v8h fp[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float mx = sc[t][0][0];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) mx = fmaxf(mx, sc[t][c][r]);
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m[t], mx);
-        const float alpha = __builtin_amdgcn_exp2f(m[t] - mn);
-        m[t] = mn;
-        float sum = 0.f;
-        float w[16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float x = __builtin_amdgcn_exp2f(sc[t][c][r] - mn);
-            w[4 * c + r] = x;
-            sum += x;
-          }
-        l[t] = l[t] * alpha + sum * vinv;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) o[t][d][r] *= alpha;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          fp[t][c] = v8h{(_Float16)w[8 * c], (_Float16)w[8 * c + 1], (_Float16)w[8 * c + 2], (_Float16)w[8 * c + 3],
-                         (_Float16)w[8 * c + 4], (_Float16)w[8 * c + 5], (_Float16)w[8 * c + 6], (_Float16)w[8 * c + 7]};
-      }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const v8h v0 = widen_f16(vr[d][0], vr[d][1]), v1 = widen_f16(vr[d][2], vr[d][3]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, fp[t][0], o[t][d], 0, 0, 0);
-          o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, fp[t][1], o[t][d], 0, 0, 0);
-        }
-      }
-    }
-
-    // join the four waves: each puts its rows, relative to its own maximum,
-    // into LDS
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float sum = l[t];
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      if (g == 0) {
-        lds_m[wave][16 * t + col] = m[t];
-        lds_l[wave][16 * t + col] = sum;
-      }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(&lds_o[wave][16 * t + col][16 * d + 4 * g]) = o[t][d];
-    }
-    __syncthreads();
+    const int64_t row0 = tile * ROWS;
     const bool whole = off == 0 && count == q.units;
-    Partial<D, NT>* part = nullptr;
-    if (!whole) {
-      // slot 0: a pair begun by another workgroup; slot 1: one begun here
-      part = reinterpret_cast<Partial<D, NT>*>(p.workspace) + 2 * (int64_t)blockIdx.x + (off == 0 ? 1 : 0);
-    }
-    for (int i = tid; i < ROWS * (D / 4); i += DWAVES * 64) {
-      const int r = i / (D / 4), d = 4 * (i % (D / 4));
-      if (row0 + r >= rows) break;
-      float mx = lds_m[0][r];
-#pragma unroll
-      for (int w = 1; w < DWAVES; ++w) mx = fmaxf(mx, lds_m[w][r]);
-      float sum = 0.f;
-      v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < DWAVES; ++w) {
-        const float a = __builtin_amdgcn_exp2f(lds_m[w][r] - mx);
-        sum += lds_l[w][r] * a;
-        const v4f x = *reinterpret_cast<const v4f*>(&lds_o[w][r][d]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] += x[j] * a;
-      }
+    // slot 0: a pair begun by another workgroup; slot 1: one begun here
+    Partial<D, NT>* const part = reinterpret_cast<Partial<D, NT>*>(p.workspace) + 2 * (int64_t)blockIdx.x + (off == 0 ? 1 : 0);
+    FewRows<D, NT, DWAVES>::run(p, q.r, row0, head, q.unit0 + off, count, lds,
+                                [&](int r, int d, float mx, float sum, v4f acc) __attribute__((always_inline)) {
       if (whole) {
         const float inv = inverse_sum(sum);
-        uint16_t* dst = p.out + row_offset(q_begin, row0 + r, head, p.group, D, p.ldo) + d;
+        uint16_t* dst = p.out + row_offset(q.r.begin, row0 + r, head, p.group, D, p.ldo) + d;
         *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
       } else {
         *reinterpret_cast<v4f*>(&part->o[r][d]) = acc;
@@ -403,10 +194,17 @@ void attention_decode_kernel(AttnArgs p) {
           part->l[r] = sum;
         }
       }
-    }
+    });
     __syncthreads();
     at += count;
   }
+}
+
+template <int D, int NT>
+__global__ __launch_bounds__(DWAVES * 64, 2)
+void attention_decode_kernel(AttnArgs p) {
+  __shared__ __attribute__((aligned(16))) typename FewRows<D, NT, DWAVES>::Lds lds;
+  decode<D, NT>(p, lds);
 }
 
 // Joins the pairs whose units went to more than one workgroup. Workgroup (x, z)
@@ -458,7 +256,9 @@ hipError_t launch(const AttnArgs& p, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const int64_t pairs = (((p.seq.T * p.group) >> (NT == 1 ? 4 : 5)) + p.seq.S) * p.Hk;   // at most
   if (pairs <= ATTN_WORKGROUPS / 4)
-    // each may be in many pieces (8 heads of 131072 tokens: 64 each): a workgroup a row
+    // each may be in many pieces (8 heads of 131072 tokens: 64 each): a workgroup a
+    // row (that one 50 us, by decode workgroup 57; 512 pairs of up to 8192 tokens 112
+    // by decode workgroup, by pair 128)
     hipLaunchKernelGGL((attention_join_kernel<D, NT, true>), dim3((unsigned)pairs, 16 * NT), dim3(JOIN_THREADS), 0, stream, p);
   else
     hipLaunchKernelGGL((attention_join_kernel<D, NT, false>), dim3(ATTN_WORKGROUPS, 2), dim3(JOIN_THREADS), 0, stream, p);

@@ -20,6 +20,8 @@
 //     scales and whether they are held are scalars. Key scales multiply the
 //     scores, value exponents go into the probabilities' exponents (see
 //     attention_decode.hip);
+//   * a tile of few rows (a single token beside prompts, the rest of a prompt) is
+//     computed as the decode kernel computes it;
 //   * 16-byte chunks in LDS are permuted by row (c ^ row % 16 in rows of 256
 //     bytes, c ^ (row / 2) % 8 in rows of 128), so that the 16
 //     lanes of a read cycle meet distinct banks.
@@ -33,7 +35,7 @@
 // 190 us of it; a large bf16 product of the library reaches 1.39).
 #include <type_traits>
 
-#include "attention_common.h"
+#include "attention_rows.h"
 
 namespace iqp {
 namespace {
@@ -42,6 +44,10 @@ using namespace attn;
 
 constexpr int PWAVES = 4;
 constexpr int PROWS = 32 * PWAVES;     // rows of a workgroup
+// A tile of no more rows than this goes to FewRows, whose waves share out the tokens
+// and not the rows (24 sequences of 1 to 30 tokens, 8 heads over 1, after up to 3900:
+// 69 us; with 64 instead 106)
+constexpr int FEW_ROWS = 32;
 constexpr float SLACK = 8.f;
 constexpr int SPLIT_GROUPS = 512;      // most workgroups of a split launch (partial results kept)
 
@@ -136,6 +142,34 @@ struct Prefill {
     Work w;
     if (!find_work(p, rest / splits, w)) return;
 
+    const int64_t u_lo = w.lo / U, u_hi = w.hi > w.lo ? (w.hi + U - 1) / U : u_lo;
+    if (w.rows - w.row0 <= FEW_ROWS) {
+      using Few = FewRows<D, 1, SETS * PWAVES>;
+      static_assert(sizeof(typename Few::Lds) <= LDS_BYTES, "in the units' place");
+      PartialTile<D>& part = reinterpret_cast<PartialTile<D>*>(p.workspace)[blockIdx.x];
+      const SeqRows seq = {w.s, (int)w.begin, (int)(w.begin + w.n), (int)w.len};
+      const int64_t u0 = u_lo + (u_hi - u_lo) * z / splits, u1 = u_lo + (u_hi - u_lo) * (z + 1) / splits;
+      for (int64_t r0 = w.row0; r0 < w.rows; r0 += Few::ROWS) {
+        Few::run(p, seq, r0, head, u0, u1 - u0, *reinterpret_cast<typename Few::Lds*>(lds_all),
+                 [&](int r, int d, float mx, float sum, v4f acc) __attribute__((always_inline)) {
+          if (splits == 1) {
+            const float inv = inverse_sum(sum);
+            uint16_t* const dst = p.out + row_offset(w.begin, r0 + r, head, p.group, D, p.ldo) + d;
+            *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+          } else {
+            const int i = (int)(r0 - w.row0) + r;
+            *reinterpret_cast<v4f*>(&part.o[i][d]) = acc;
+            if (d == 0) {
+              part.m[i] = mx;
+              part.l[i] = sum;
+            }
+          }
+        });
+        __syncthreads();
+      }
+      return;
+    }
+
     const int64_t row = w.row0 + 32 * wave + col;
     const int64_t rc = row < w.rows ? row : w.rows - 1;
     const int64_t src = row_offset(w.begin, rc, head, p.group, D, p.ldq);
@@ -143,7 +177,6 @@ struct Prefill {
 #pragma unroll
     for (int k = 0; k < KS; ++k) fq[k] = *reinterpret_cast<const v8bf*>(p.q + src + 16 * k + 8 * half);
     // tokens relative to the unit range's first, 32 bits wide
-    const int64_t u_lo = w.lo / U, u_hi = w.hi > w.lo ? (w.hi + U - 1) / U : u_lo;
     const int64_t cuts = (int64_t)SETS * splits, cut = (int64_t)SETS * z + set;
     const int64_t u0 = u_lo + (u_hi - u_lo) * cut / cuts, u1 = u_lo + (u_hi - u_lo) * (cut + 1) / cuts;
     const int64_t base = u0 * U;

@@ -278,15 +278,21 @@ struct AttnArgs {
   int64_t max_rows;         // set by the launcher: sequences of more rows (tokens * group) are the
                             // prompt kernel's, the others the decode kernel's
 };
-// workgroups of the decode kernel: two for each of a full chip's 256 CUs
+// workgroups of the decode kernel: two for each of a full chip's 256 CUs (64
+// sequences of up to 8192 tokens: 112 us; with 256 workgroups 126, 768 123, 1024 116)
 constexpr int ATTN_WORKGROUPS = 512;
-// Sequences of more than ATTN_DECODE_ROWS rows are the prompt kernel's, in a
-// batch that has more than that on average; else all are the decode kernel's.
+// A batch of no more rows (tokens times query heads of a key head) than this on
+// average is the decode kernel's (32 sequences of 6000 tokens, 64 heads over 8, us,
+// decode / prompt kernel: 64 rows 185 / 207, 128 rows 326 / 207). Of another one,
+// sequences of more rows are the prompt kernel's.
 constexpr int ATTN_DECODE_ROWS = 64;
-// Where a row sees no more tokens than this (the table, or the window), the prompt
-// kernel takes such a batch's short sequences too: their few units cost less than
-// two more launches that mostly find nothing (9 us where they find nothing at all).
-constexpr int ATTN_SHORT_REACH = 1024;
+// The sequences of few rows in such a batch: where a row sees no more tokens than
+// this (the table, or the window), the prompt kernel takes them too, beside the
+// others; else they are the decode kernel's, behind it (two prompts of 500 tokens
+// beside single tokens, us, one / two kernels: 32 sequences of 2000 39 / 57, of 4000
+// 71 / 81, of 7500 138 / 133; 8 of 16000 166 / 83; 24 sequences of 1 to 30 new tokens
+// after up to 3900: 69 / 95).
+constexpr int ATTN_SHORT_REACH = 8192;
 int64_t attention_decode_workspace_bytes(int D);
 int64_t attention_prefill_workspace_bytes(int D);
 hipError_t launch_attention_decode(const AttnArgs& args, int D, hipStream_t stream);

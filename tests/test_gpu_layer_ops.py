@@ -297,8 +297,8 @@ def test_append_leaves_out_what_is_not_held(gpu_lib):
 
 # ---------------------------------------------------------------- attention
 
-def attend(lib, g, lens, new, hq, h, d, block, window=0, scale=None, table=None, nan_codes=False, tail=0):
-    auto, cu, n = make_batch(g, lens, new, block, width_extra=1)
+def attend(lib, g, lens, new, hq, h, d, block, window=0, scale=None, table=None, nan_codes=False, tail=0, extra=1):
+    auto, cu, n = make_batch(g, lens, new, block, width_extra=extra)
     table = auto if table is None else table(auto, n)
     ref = random_cache(g, n, h, block, d, nan_codes=nan_codes)
     if nan_codes:
@@ -351,10 +351,12 @@ def test_attention_rows(gpu_lib, lens, new, hq, h, d, block, window):
 @pytest.mark.parametrize("lens,new", [([1500, 40, 1100], [200, 1, 90]), ([1300, 1200], [150, 130]), ([1030, 1, 5], [1, 1, 0]),
                                       ([1100, 1080, 1], [70, 66, 1])])
 @pytest.mark.parametrize("hq,h,d,block", [(4, 2, 128, 64), (8, 1, 64, 32)])
-def test_attention_prompts_over_a_long_table(gpu_lib, lens, new, hq, h, d, block):
-    """Batches whose sequences go to two kernels, or to one of them alone."""
-    print("attend long table", lens, new, hq, h, d, block, flush=True)
-    attend(gpu_lib, gen(18, len(lens), lens[0], new[0], hq), lens, new, hq, h, d, block, 0, tail=1)
+@pytest.mark.parametrize("width", [1, 9000])
+def test_attention_prompts_over_a_long_table(gpu_lib, lens, new, hq, h, d, block, width):
+    """Batches whose sequences go to two kernels (a wide table), or to one of them alone."""
+    print("attend long table", lens, new, hq, h, d, block, width, flush=True)
+    attend(gpu_lib, gen(18, len(lens), lens[0], new[0], hq), lens, new, hq, h, d, block, 0, tail=1, extra=-(-width // block),
+           nan_codes=width > 1)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -364,6 +366,23 @@ def test_attention_prompts_that_fill_the_chip(gpu_lib, d):
     g = gen(23, d)
     lens = [int(x) for x in g.integers(66, 200, 18)]
     attend(gpu_lib, g, lens, [min(n, 66 + i) for i, n in enumerate(lens)], 32, 32, d, 32, tail=1, nan_codes=True)
+
+
+@pytest.mark.parametrize("width", [1, 9000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_short_tiles_beside_prompts(gpu_lib, d, width):
+    """Tiles of 1 to 33 rows, also the last of a prompt, in batches whose tiles are
+    split over the tokens and in ones that are not; a hole in one of them."""
+    print("attend short tiles", d, width, flush=True)
+    def hole(t, n):
+        t = t.clone()
+        t[2, 1] = -1
+        return t
+    attend(gpu_lib, gen(24, d, width), [900, 333, 700, 65, 1, 130], [129, 1, 16, 2, 1, 130], 1, 1, d, 64, tail=1, nan_codes=True, table=hole,
+           extra=-(-width // 64))
+    lens = [900, 333, 700, 65, 1, 130, 600, 600, 20, 640, 70, 200]
+    attend(gpu_lib, gen(25, d, width), lens, [69, 1, 4, 2, 1, 130, 8, 9, 3, 70, 70, 65], 16, 4, d, 16, nan_codes=True, table=hole, window=250,
+           extra=-(-width // 16))
 
 
 @pytest.mark.parametrize("window", [100, 700])
