@@ -287,7 +287,8 @@ int64_t attention_workspace_bytes(int D) {
 
 hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream) {
   AttnArgs p = args;
-  if (p.seq.T * p.group <= ATTN_DECODE_ROWS * (int64_t)p.seq.S) {
+  const int64_t rows = p.seq.T * p.group;
+  if (rows <= ATTN_DECODE_ROWS * (int64_t)p.seq.S && (reach(p) > ATTN_DIRECT_REACH || rows > ATTN_DIRECT_ROWS * (int64_t)p.seq.S)) {
     p.max_rows = (int64_t)1 << 62;
     return launch_attention_decode(p, D, stream);
   }

@@ -282,10 +282,16 @@ struct AttnArgs {
 // sequences of up to 8192 tokens: 112 us; with 256 workgroups 126, 768 123, 1024 116)
 constexpr int ATTN_WORKGROUPS = 512;
 // A batch of no more rows (tokens times query heads of a key head) than this on
-// average is the decode kernel's (32 sequences of 6000 tokens, 64 heads over 8, us,
+// average is the decode kernel's, but see below (32 sequences of 6000 tokens, 64 heads over 8, us,
 // decode / prompt kernel: 64 rows 185 / 207, 128 rows 326 / 207). Of another one,
 // sequences of more rows are the prompt kernel's.
 constexpr int ATTN_DECODE_ROWS = 64;
+// Where a row sees no more tokens than this, batches of few rows are the prompt
+// kernel's too: a workgroup a sequence and head, no second launch (single tokens, us,
+// direct / decode kernel: 10 sequences of 35 tokens 5.8 / 8.5, 30 of up to 900, 64
+// heads over 8, 12.8 / 18.2, of up to 2000 20.8 / 25.3; 64 of up to 4000 84 / 69, as
+// the lengths differ; 8 sequences of 2000 with 64 rows a head 28 / 25).
+constexpr int ATTN_DIRECT_REACH = 2048, ATTN_DIRECT_ROWS = 32;
 // The sequences of few rows in such a batch: where a row sees no more tokens than
 // this (the table, or the window), the prompt kernel takes them too, beside the
 // others; else they are the decode kernel's, behind it (two prompts of 500 tokens

@@ -335,8 +335,9 @@ def attend(lib, g, lens, new, hq, h, d, block, window=0, scale=None, table=None,
 @pytest.mark.parametrize("window", [0, 50])
 def test_attention_single_tokens(gpu_lib, hq, h, d, block, window):
     print("attend", hq, h, d, block, window, flush=True)
-    attend(gpu_lib, gen(10, hq, d, block, window), [1, 2, 63, 64, 65, 130, 517, 16], [1] * 8, hq, h, d, block, window,
-           nan_codes=True)
+    for width in (1, 2100):                                  # a table that keeps them in one launch, and one that does not
+        attend(gpu_lib, gen(10, hq, d, block, window), [1, 2, 63, 64, 65, 130, 517, 16], [1] * 8, hq, h, d, block, window,
+               nan_codes=True, extra=-(-width // block))
 
 
 @pytest.mark.parametrize("lens,new", [([70, 33, 5], [2, 3, 5]), ([200, 17, 0, 1, 129], [4, 0, 0, 1, 100]),
@@ -345,7 +346,9 @@ def test_attention_single_tokens(gpu_lib, hq, h, d, block, window):
 @pytest.mark.parametrize("window", [0, 40])
 def test_attention_rows(gpu_lib, lens, new, hq, h, d, block, window):
     print("attend rows", lens, new, hq, h, d, block, window, flush=True)
-    attend(gpu_lib, gen(11, len(lens), lens[0], hq, d, window), lens, new, hq, h, d, block, window, nan_codes=True, tail=3)
+    for width in (1, 2100):
+        attend(gpu_lib, gen(11, len(lens), lens[0], hq, d, window), lens, new, hq, h, d, block, window, nan_codes=True, tail=3,
+               extra=-(-width // block))
 
 
 @pytest.mark.parametrize("lens,new", [([1500, 40, 1100], [200, 1, 90]), ([1300, 1200], [150, 130]), ([1030, 1, 5], [1, 1, 0]),
@@ -401,6 +404,7 @@ def test_attention_many_sequences(gpu_lib):
     lens = [int(x) for x in g.integers(1, 90, 150)]
     new = [int(x) for x in g.integers(0, 2, 150)]
     attend(gpu_lib, g, lens, new, 4, 2, 64, 16, tail=2)
+    attend(gpu_lib, g, lens, new, 4, 2, 64, 16, tail=2, extra=130)
     lens = [int(x) for x in g.integers(20, 60, 70)]
     attend(gpu_lib, g, lens, [int(x) for x in g.integers(0, 20, 70)], 8, 2, 128, 16, window=30)
 
@@ -419,11 +423,13 @@ def test_attention_rows_that_see_nothing(gpu_lib):
         t[1, 1] = n + 5                     # a hole in the middle
         t[2, 0] = -1                        # the first rows of it see nothing
         return t
-    attend(gpu_lib, gen(14), [40, 100, 60, 0, 3], [3, 2, 60, 2, 6], 4, 2, 128, 32, table=holes, nan_codes=True)
-    attend(gpu_lib, gen(15), [40, 100, 60, 0, 3], [3, 2, 60, 2, 6], 4, 2, 64, 16, table=holes, nan_codes=True, window=20)
+    for extra in (1, 140):
+        attend(gpu_lib, gen(14), [40, 100, 60, 0, 3], [3, 2, 60, 2, 6], 4, 2, 128, 32, table=holes, nan_codes=True, extra=extra)
+        attend(gpu_lib, gen(15), [40, 100, 60, 0, 3], [3, 2, 60, 2, 6], 4, 2, 64, 16, table=holes, nan_codes=True, window=20, extra=extra)
+        attend(gpu_lib, gen(26), [40, 100, 60, 0, 3], [3, 2, 1, 2, 6], 4, 2, 64, 16, table=holes, nan_codes=True, extra=extra)
 
 
-@pytest.mark.parametrize("lens,new", [([200], [1]), ([200, 180], [120, 100]), ([1300, 1200], [100, 120])])
+@pytest.mark.parametrize("lens,new", [([200], [1]), ([200, 200], [1, 1]), ([200, 180], [120, 100]), ([1300, 1200], [100, 120])])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_value_scales_far_apart(gpu_lib, lens, new, d):
     """Neighbouring blocks whose value and key exponents differ by many powers
@@ -432,7 +438,7 @@ def test_attention_value_scales_far_apart(gpu_lib, lens, new, d):
     print("attend scales", lens, new, d, flush=True)
     g = gen(16, d)
     h, block = 2, 32
-    table, cu, n = make_batch(g, lens, new, block)
+    table, cu, n = make_batch(g, lens, new, block, width_extra=70 if lens == [200] else 0)
     ref = random_cache(g, n, h, block, d)
     for s in range(len(lens)):
         for i in range(-(-lens[s] // block)):
