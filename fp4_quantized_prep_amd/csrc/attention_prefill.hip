@@ -22,9 +22,8 @@
 //     attention_decode.hip);
 //   * a tile of few rows (a single token beside prompts, the rest of a prompt) is
 //     computed as the decode kernel computes it;
-//   * 16-byte chunks in LDS are permuted by row (c ^ row % 16 in rows of 256
-//     bytes, c ^ (row / 2) % 8 in rows of 128), so that the 16
-//     lanes of a read cycle meet distinct banks.
+//   * 16-byte chunks in LDS are permuted by row, so that the lanes of a cycle
+//     meet distinct banks.
 // Workgroups are numbered with the key head fastest, so that with 8 heads an
 // XCD's L2 holds one head's cache, longest row tiles first. Where there are few,
 // SETS = 2 gives a workgroup eight waves, of which four take the first half of
@@ -115,11 +114,12 @@ struct Prefill {
   static constexpr int K_BYTES = U * D * 2, V_BYTES = D * U * 2;
   static constexpr int SET_BYTES = 2 * (K_BYTES + V_BYTES), LDS_BYTES = SETS * SET_BYTES;
 
-  // permutation of a key row's 16-byte chunks: rows of 256 bytes cover all
-  // banks, rows of 128 half of them
-  static __device__ __forceinline__ int key_swizzle(int tok) { return D == 128 ? tok & 15 : (tok >> 1) & 7; }
-  // and of a value row's (128 bytes: half of the banks)
-  static __device__ __forceinline__ int value_swizzle(int dim) { return (dim >> 1) & 7; }
+  // Where 16-byte chunk c of a key row, of a value row lies in it. A read takes one
+  // chunk of 16 rows, which then lie in distinct banks of 64; a store every second
+  // chunk of one row (256 bytes) or of two (128), distinct among 32.
+  static __device__ __forceinline__ int narrow_chunk(int row, int c) { return c ^ ((row >> 1) & 7) ^ (row & 1); }
+  static __device__ __forceinline__ int key_chunk(int tok, int c) { return D == 128 ? c ^ (c >> 3) ^ (tok & 15) : narrow_chunk(tok, c); }
+  static __device__ __forceinline__ int value_chunk(int dim, int c) { return narrow_chunk(dim, c); }
 
   struct Codes {
     v4u k[LOADS], v[LOADS];
@@ -238,8 +238,8 @@ struct Prefill {
       return c;
     };
     const int key_to = tok * (2 * D), value_to = K_BYTES + dim * (2 * U);
-    const int key_to0 = key_to + 16 * ((2 * piece) ^ key_swizzle(tok)), key_to1 = key_to + 16 * ((2 * piece + 1) ^ key_swizzle(tok));
-    const int value_to0 = value_to + 16 * ((2 * gr) ^ value_swizzle(dim)), value_to1 = value_to + 16 * ((2 * gr + 1) ^ value_swizzle(dim));
+    const int key_to0 = key_to + 16 * key_chunk(tok, 2 * piece), key_to1 = key_to + 16 * key_chunk(tok, 2 * piece + 1);
+    const int value_to0 = value_to + 16 * value_chunk(dim, 2 * gr), value_to1 = value_to + 16 * value_chunk(dim, 2 * gr + 1);
     // values behind the sequence, before the window or not held must not reach
     // the product (0 * NaN)
     auto clear_codes = [&](int u, Codes& c, int blk) __attribute__((always_inline)) {
@@ -274,9 +274,9 @@ struct Prefill {
     const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
     int koff[KS], voff[GR];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) koff[k] = krow * (2 * D) + 16 * ((2 * k + half) ^ key_swizzle(krow));
+    for (int k = 0; k < KS; ++k) koff[k] = krow * (2 * D) + 16 * key_chunk(krow, 2 * k + half);
 #pragma unroll
-    for (int i = 0; i < GR; ++i) voff[i] = K_BYTES + col * (2 * U) + 16 * ((2 * i + half) ^ value_swizzle(col));
+    for (int i = 0; i < GR; ++i) voff[i] = K_BYTES + col * (2 * U) + 16 * value_chunk(col, 2 * i + half);
     // a unit's granules in scalar registers (so no floating-point values);
     // granule 2 a + (r >> 3) holds score register r of tile a
     struct Scales {
