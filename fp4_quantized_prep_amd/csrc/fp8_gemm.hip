@@ -4,6 +4,17 @@
 //   out[m, n] = sum_j 2^(ea(m, j) + ew(n / 128, j)) sum_{k in block j} A[m, k] W[n, k]
 // summed in float32 by the matrix cores, which apply the scales themselves,
 // and rounded to bf16 once.
+//
+// Up to 64 tokens the product is bound by the read of the weights (stream
+// kernel): 32x7168x8192 13.2 to 14.5 us, 4.1 to 4.5 TB/s of a large copy's 5.1;
+// 1x1536x7168 4.9 us, of which launch and first loads are half. Above (tile
+// kernel) by the loop around the matrix cores: a K block takes a workgroup 1.28 to
+// 1.48 us for its 0.87 us of MFMAs (256x256 tile: 4632x8192x1536 70 us, 1.65 PFLOP/s;
+// 4632x8192x7168 266 us, 2.04, as three rounds of tiles for 2.4; a large product of
+// the library reaches 2.66), 0.4 us for 0.11 (128x64: 777x2115x7168 23.3 us, 1.0
+// PFLOP/s). What did not help that loop: more LDS stages, tiles in another order
+// (fewer L2 misses, same time), workgroups that stay and copy the next tile's
+// first blocks before they store (72.7 us for 71).
 #include <type_traits>
 
 #include "iq_common.h"
@@ -521,9 +532,12 @@ int fp8_gemm_splits(int64_t M, int64_t N, int64_t K) {
 }
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& p, hipStream_t stream) {
-  // up to 64 tokens the product is a read of the weights; 16 or 32 rows of them a
-  // workgroup, by which of the two gives the CUs enough workgroups (measured at
-  // 16 tokens, 32 / 16 rows: N 7168, K 8192 13.6 / 15.6 us; N 1536, K 7168 5.8 / 5.1)
+  // Up to 64 tokens the product is a read of the weights (64x1500x7168, us: stream
+  // kernel 10.1, 64x64 tiles 19.2; 64x7168x8192 20.3, 26.9; 64x4000x1536 5.5, 6.7); 16 or
+  // 32 rows of them a workgroup, by which of the two gives the CUs enough
+  // workgroups (32 / 16 rows: 16x7168x8192 13.6 / 15.3, 32x7168x8192 15.6 / 20.0,
+  // 64x7168x8192 20.3 / 28.3, 40x8192x1536 6.5 / 8.7; 16x1536x7168 7.2 / 5.6,
+  // 32x2000x7168 8.6 / 7.0, 64x4000x1536 6.2 / 5.5).
   if (p.M <= 16) return p.N >= 6144 ? launch_stream<2, 1, 8, 3>(p, stream) : launch_stream<1, 1, 4, 4>(p, stream);
   if (p.M <= 32) return p.N >= 6144 ? launch_stream<2, 2, 8, 2>(p, stream) : launch_stream<1, 2, 4, 3>(p, stream);
   if (p.M <= 64) return p.N >= 6144 ? launch_stream<2, 4, 4, 3>(p, stream) : launch_stream<1, 4, 4, 3>(p, stream);

@@ -19,7 +19,13 @@
 //
 // HBM-bound (2 bytes in and 1 out a value). The workgroup holds its new rows in
 // registers (16 bytes a lane) from the amax to the conversion, so they are read
-// once; the values are turned in LDS.
+// once; the values are turned in LDS, and a piece of 16 tokens that is partly new
+// is merged with its old codes and stored whole.
+//
+// Measured: three prompts of 900 to 4632 tokens after up to 700, 8 heads of 128: 22.4 us
+// for writing and reading back, 4.5 TB/s (a large copy reaches 5.1); a token each
+// for 64 sequences: 7.0 us, four dependent loads (lengths, block table, rows and
+// scales, old codes) and a launch.
 #include "fp8_block.h"
 #include "layer_common.h"
 

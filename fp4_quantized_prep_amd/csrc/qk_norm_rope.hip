@@ -16,6 +16,9 @@
 // and each lane keeps its partner's weights beside its own), which costs four
 // cross-lane moves a head. A wave takes PASSES groups of heads of one token,
 // loads first, with the token's table row and the weights read once.
+//
+// Measured: 4632 tokens, 64 query and 8 key heads of 128: 36.2 us, 4.75 TB/s (a large
+// copy reaches 5.1); 16 tokens: 3.0 us.
 #include <type_traits>
 
 #include "layer_common.h"
@@ -160,7 +163,9 @@ hipError_t launch(const QkNormRopeArgs& p, hipStream_t stream) {
   constexpr int HEADS = 64 / (D / 8);
   const int total = p.Hq + p.Hk;
   // one pass a wave while that leaves fewer than 32 waves a CU, two above; past
-  // the caches what would not stay in them for its reader
+  // the caches what would not stay in them for its reader (4632 tokens, 64 + 8 heads of
+  // 128, inputs that no cache holds: one pass 44.6 us, two 40.4, past the caches 36.4;
+  // 1000 tokens, held: one 10.8, two 10.1, past the caches 10.4)
   const int64_t waves1 = p.M * ((total + HEADS - 1) / HEADS), waves2 = p.M * ((total + 2 * HEADS - 1) / (2 * HEADS));
   const bool two = waves1 >= (int64_t)cu_count() * 32;
   const bool past = p.M * total * D * 2 > ((int64_t)32 << 20);
