@@ -30,6 +30,16 @@
  *      16-byte loads (built once per table); indexer_q_gemm_rope_fp4_lanes
  *      is call 2 reading it.
  *
+ * and the operators of the attention layer around it, with 8-bit operands:
+ *
+ *   7. fp8_gemm_1x128_128x128   the layer's other projections: the operands of
+ *      calls 1 and 5, bf16 out.
+ *   8. qk_norm_rope   RMS norm of every query and key head and RoPE, in one pass.
+ *   9. kv_cache_append_fp8, kv_cache_read_fp8   a paged key/value cache in E4M3
+ *      with a UE8M0 scale per block of tokens and head: written, read back.
+ *  10. attention_fp8_kv   causal attention over that cache, for prompts, their
+ *      continuations and single tokens in one ragged batch.
+ *
  * Conventions shared by every entry point:
  *
  *   - Every data pointer is a caller-owned DEVICE pointer on the current HIP
