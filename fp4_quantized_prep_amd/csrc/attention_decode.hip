@@ -287,13 +287,15 @@ int64_t attention_workspace_bytes(int D) {
 
 hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream) {
   AttnArgs p = args;
-  const int64_t rows = p.seq.T * p.group;
-  if (rows <= ATTN_DECODE_ROWS * (int64_t)p.seq.S && (reach(p) > ATTN_DIRECT_REACH || rows > ATTN_DIRECT_ROWS * (int64_t)p.seq.S)) {
+  const int64_t rows = p.seq.T * p.group, S = p.seq.S;
+  const bool many = S * p.Hk >= ATTN_MANY_PAIRS || S >= ATTN_MANY;
+  const bool direct = rows <= ATTN_DIRECT_ROWS * S && reach(p) <= ATTN_DIRECT_REACH * (many ? 2 : 1);
+  if (rows <= ATTN_DECODE_ROWS * S && !direct) {
     p.max_rows = (int64_t)1 << 62;
     return launch_attention_decode(p, D, stream);
   }
   // (a single sequence needs one kernel, whatever its number of rows turns out to be)
-  const bool alone = p.seq.S == 1 || reach(p) <= ATTN_SHORT_REACH;
+  const bool alone = S == 1 || reach(p) <= ATTN_SHORT_REACH;
   p.max_rows = alone ? 0 : ATTN_DECODE_ROWS;
   const hipError_t e = launch_attention_prefill(p, D, stream);
   if (e != hipSuccess || alone) return e;

@@ -290,8 +290,12 @@ constexpr int ATTN_DECODE_ROWS = 64;
 // kernel's too: a workgroup a sequence and head, no second launch (single tokens, us,
 // direct / decode kernel: 10 sequences of 35 tokens 5.8 / 8.5, 30 of up to 900, 64
 // heads over 8, 12.8 / 18.2, of up to 2000 20.8 / 25.3; 64 of up to 4000 84 / 69, as
-// the lengths differ; 8 sequences of 2000 with 64 rows a head 28 / 25).
-constexpr int ATTN_DIRECT_REACH = 2048, ATTN_DIRECT_ROWS = 32;
+// the lengths differ; 8 sequences of 2000 with 64 rows a head 28 / 25); twice as many
+// tokens where ATTN_MANY_PAIRS sequences times heads even out by themselves or
+// ATTN_MANY sequences make the decode kernel's walk over all lengths long (100 to 4000
+// tokens: 128 sequences, 8 heads 120 / 128, 200 176 / 196; 500, one head of 64, 37 / 49,
+// 1000 57 / 92; but of 2000 to 8000, 128 sequences, 8 heads, 273 / 254).
+constexpr int ATTN_DIRECT_REACH = 2048, ATTN_DIRECT_ROWS = 32, ATTN_MANY_PAIRS = 1024, ATTN_MANY = 256;
 // The sequences of few rows in such a batch: where a row sees no more tokens than
 // this (the table, or the window), the prompt kernel takes them too, beside the
 // others; else they are the decode kernel's, behind it (two prompts of 500 tokens

@@ -270,6 +270,23 @@ def test_append_token_by_token(gpu_lib):
         same_cache(dev, ref)
 
 
+@pytest.mark.parametrize("S", [64, 65, 129, 300, 4200])
+def test_append_to_many_sequences(gpu_lib, S):
+    """Sequences found among more than a wave has lanes, some without rows."""
+    print("append many", S, flush=True)
+    g = gen(27, S)
+    h, d, block = 1, 64, 16
+    lens = [int(x) for x in g.integers(0, 40, S)]
+    new = [min(n, int(x)) for n, x in zip(lens, g.integers(0, 3, S))]
+    table, cu, n = make_batch(g, lens, new, block)
+    ref = random_cache(g, n, h, block, d)
+    k, v = bf16(g, cu[-1], h, d), bf16(g, cu[-1], h, d)
+    dev = to_gpu(gpu_lib, ref)
+    gpu_lib.kv_cache_append_fp8(k.cuda(), v.cuda(), dev, table.cuda(), ints(lens), ints(cu))
+    R.append(ref, k, v, table, lens, cu)
+    same_cache(dev, ref)
+
+
 def test_append_leaves_out_what_is_not_held(gpu_lib):
     """Table entries outside the cache, positions past the table and below
     zero: their rows are left out, and nothing else is touched."""
@@ -405,6 +422,10 @@ def test_attention_many_sequences(gpu_lib):
     new = [int(x) for x in g.integers(0, 2, 150)]
     attend(gpu_lib, g, lens, new, 4, 2, 64, 16, tail=2)
     attend(gpu_lib, g, lens, new, 4, 2, 64, 16, tail=2, extra=130)
+    lens = [int(x) for x in g.integers(1, 40, 300)]
+    new = [int(x) for x in g.integers(0, 2, 300)]
+    attend(gpu_lib, g, lens, new, 2, 1, 64, 16, tail=1, nan_codes=True, extra=200)   # one launch
+    attend(gpu_lib, g, lens, new, 2, 1, 64, 16, tail=1, extra=300)                   # the decode kernel
     lens = [int(x) for x in g.integers(20, 60, 70)]
     attend(gpu_lib, g, lens, [int(x) for x in g.integers(0, 20, 70)], 8, 2, 128, 16, window=30)
 
