@@ -86,7 +86,7 @@ struct Line {
   int chunk = 0, in_chunk = 0;
   int64_t total = 0;       // units of the whole line
   int64_t base = 0;        // units before sequence q
-  Seq q;
+  Seq q = {};              // (none: no tiles, no work)
 
   __device__ __forceinline__ explicit Line(const AttnArgs& p_) : p(p_) {
     rows64 = lane_sequence(p.seq, 0);    // kept: most batches have no more
@@ -97,12 +97,19 @@ struct Line {
       total += t;
     }
   }
-  // to the sequence that holds unit at (< total); once
+  // To the sequence that holds unit at (< total); once. (Should the lengths change
+  // under the kernel, which no caller may do, the walks still end: q.work is 0.)
   __device__ __forceinline__ void seek(int64_t at) {
     uint64_t past = __ballot(sum > at);
     while (past == 0) {
       base += __shfl((long long)sum, 63);
       chunk += 64;
+      if (chunk >= p.seq.S) {
+        in_chunk = 63;
+        q.r.s = p.seq.S;
+        q.work = 0;
+        return;
+      }
       rows64 = lane_sequence(p.seq, chunk);
       int64_t t;
       sum = scan(get_seq<ROWS>(p, rows64).work, t);
@@ -112,7 +119,8 @@ struct Line {
     q = get_seq<ROWS>(p, sequence_of_lane(rows64, in_chunk));
     base += __shfl((long long)sum, in_chunk) - q.work;
   }
-  // to the sequence that owns row tile slot `item` (as find_sequence finds it); once
+  // to the sequence that owns row tile slot `item` (as find_sequence finds it; none
+  // before the first); once
   __device__ __forceinline__ void seek_item(int64_t item) {
     constexpr int SHIFT = ROWS == 16 ? 4 : 5;
     int64_t before = 0;
@@ -131,7 +139,7 @@ struct Line {
   }
   // on to the sequence that holds unit at (< total) from one at or before it
   __device__ __forceinline__ void advance(int64_t at) {
-    while (at >= base + q.work) {
+    while (at >= base + q.work && q.r.s < p.seq.S) {
       base += q.work;
       if (++in_chunk == 64) {
         in_chunk = 0;
@@ -171,6 +179,7 @@ __device__ __forceinline__ void decode(const AttnArgs& p, typename FewRows<D, NT
   while (at < stop) {
     line.advance(at);
     const Seq& q = line.q;
+    if (q.work == 0) return;
     const int64_t base = line.base;
     const int64_t pair = quotient(at - base, q.units);            // row tile and key head of the sequence
     const int64_t off = (at - base) - pair * q.units;
@@ -225,12 +234,13 @@ void attention_join_kernel(AttnArgs p) {
     const int64_t item = blockIdx.x / (unsigned)p.Hk;
     line.seek_item(item);
     const int64_t tile = item - item_key(q.r, p.group, NT == 1 ? 4 : 5, 1);
-    if (tile >= q.tiles) return;
+    if (tile < 0 || tile >= q.tiles) return;                 // (below 0: offsets that decrease)
     pair = tile * p.Hk + blockIdx.x % (unsigned)p.Hk;
   } else {
     const int64_t last = (blockIdx.x + (int64_t)1) * per - 1;   // the workgroup's last unit
     if (last >= line.total) return;
     line.seek(last);
+    if (q.work == 0) return;
     pair = quotient(last - line.base, q.units);
   }
   const int64_t u0 = line.base + pair * q.units, w0 = quotient(u0, per), w1 = quotient(u0 + q.units - 1, per);

@@ -74,7 +74,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& p, int64_t item, Work&
   if (w.n <= 0 || w.rows <= p.max_rows) return false;
   const int64_t tiles = (w.rows + PROWS - 1) / PROWS;
   const int64_t tile = item - item_key(q, p.group, 7, 1);
-  if (tile >= tiles) return false;
+  if (tile < 0 || tile >= tiles) return false;
   w.row0 = (tiles - 1 - tile) * PROWS;     // the longest first
   const int64_t last = w.row0 + PROWS < w.rows ? w.row0 + PROWS - 1 : w.rows - 1;
   const int64_t held = (int64_t)p.seq.max_blocks << p.seq.log_block;

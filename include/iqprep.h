@@ -660,8 +660,9 @@ int qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int64_t
  * A batch of S sequences and T rows: rows cu_rows[s] .. cu_rows[s+1] - 1 are
  * the last tokens of sequence s, which has seq_lens[s] tokens with them (row
  * cu_rows[s] + i is position seq_lens[s] - (cu_rows[s+1] - cu_rows[s]) + i).
- *   cu_rows      int32 [S + 1], non-decreasing from 0; values outside [0, T]
- *                are clamped into it.
+ *   cu_rows      int32 [S + 1], non-decreasing; values outside [0, T] are
+ *                clamped into it. Rows before cu_rows[0] and from cu_rows[S]
+ *                on belong to no sequence: they are not read, nor written.
  *   seq_lens     int32 [S].
  *   block_table  int32 [S, max_blocks], row stride ld_table: position p of
  *                sequence s is token p % block_size of block
@@ -731,6 +732,9 @@ int kv_cache_read_fp8(const void* k_cache, const void* v_cache, const uint8_t* k
  *   workspace  attention_fp8_kv_workspace_bytes(D) bytes of device memory,
  *              256-byte aligned; its contents do not matter before and mean
  *              nothing after. Calls that share one must not overlap.
+ * The same call gives the same bits. The order of its sums depends on T, S, Hq,
+ * Hk, D, the table's width and the window, so a row's last bit may differ
+ * between batches.
  */
 int64_t attention_fp8_kv_workspace_bytes(int32_t D);
 int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t Hk, int32_t D,

@@ -473,6 +473,31 @@ def test_attention_value_scales_far_apart(gpu_lib, lens, new, d):
     assert bool((off <= tol).all()), float((off / tol.clamp_min(1e-300)).nan_to_num(1e9).max())
 
 
+@pytest.mark.parametrize("lens,new", [([40, 70, 300], [1, 1, 1]), ([300, 70], [40, 1]), ([200, 300], [130, 200])])
+@pytest.mark.parametrize("width", [1, 2100, 9000])
+def test_rows_before_the_first_sequence(gpu_lib, lens, new, width):
+    """Row offsets that do not begin at 0: the rows before belong to nobody."""
+    print("rows before", lens, new, width, flush=True)
+    g = gen(28, lens[0], width)
+    h, d, block, skip = 2, 64, 16, 37
+    table, cu, n = make_batch(g, lens, new, block, width_extra=-(-width // block))
+    cu = [c + skip for c in cu]
+    ref = random_cache(g, n, h, block, d)
+    k, v, q = bf16(g, cu[-1] + 1, h, d), bf16(g, cu[-1] + 1, h, d), bf16(g, cu[-1] + 1, 8, d)
+    dev = to_gpu(gpu_lib, ref)
+    gpu_lib.kv_cache_append_fp8(k.cuda(), v.cuda(), dev, table.cuda(), ints(lens), ints(cu))
+    R.append(ref, k, v, table, lens, cu)
+    same_cache(dev, ref)
+    want, tol = R.attention(q, ref, table, lens, cu, d ** -0.5, 0)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    got = gpu_lib.attention_fp8_kv(q.cuda(), dev, table.cuda(), ints(lens), ints(cu), out=out).cpu().double()
+    assert bool((got[:skip] == 7.0).all()) and bool((got[cu[-1]:] == 7.0).all())
+    assert bool(((got - want).abs() <= tol)[skip:cu[-1]].all())
+    back = torch.full((2, cu[-1] + 1, h, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.kv_cache_read_fp8(dev, table.cuda(), ints(lens), ints(cu), cu[-1] + 1, k_out=back[0], v_out=back[1])
+    assert bool((back[:, :skip] == 7.0).all()) and bool((back[:, cu[-1]:] == 7.0).all()) and not bool((back[:, skip:cu[-1]] == 7.0).all())
+
+
 def test_attention_scale_and_deterministic(gpu_lib):
     args, out = attend(gpu_lib, gen(17), [700, 300, 90], [1, 1, 1], 16, 2, 128, 64, scale=0.3)
     again = [gpu_lib.attention_fp8_kv(*args, scale=0.3) for _ in range(3)]
