@@ -12,9 +12,12 @@
 // 1.48 us for its 0.87 us of MFMAs (256x256 tile: 4632x8192x1536 70 us, 1.65 PFLOP/s;
 // 4632x8192x7168 266 us, 2.04, as three rounds of tiles for 2.4; a large product of
 // the library reaches 2.66), 0.4 us for 0.11 (128x64: 777x2115x7168 23.3 us, 1.0
-// PFLOP/s). What did not help that loop: more LDS stages, tiles in another order
-// (fewer L2 misses, same time), workgroups that stay and copy the next tile's
-// first blocks before they store (72.7 us for 71).
+// PFLOP/s). LDS takes as long as the MFMAs (0.88 us a 256x256 block at 128 bytes a
+// cycle, the copies in and the waves' reads), the copies alone more (1.7 us at
+// 2048x8192x7168, the whole 1.9). What did not help that loop: more LDS stages, tiles
+// in another order (fewer L2 misses, same time), K blocks in another order for
+// each workgroup, workgroups that stay and copy the next tile's first blocks
+// before they store (72.7 us for 71).
 #include <type_traits>
 
 #include "iq_common.h"
