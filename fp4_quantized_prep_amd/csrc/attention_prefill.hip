@@ -352,7 +352,7 @@ struct Prefill {
       for (int i = 0; i < GR; ++i) {
         const v16f& x = sc[i >> 1];
         const int r = 8 * (i & 1);
-        const float gm = max3(max3(x[r], x[r + 1], x[r + 2]), max3(x[r + 3], x[r + 4], x[r + 5]), fmaxf(x[r + 6], x[r + 7]));
+        const float gm = max3(max3(x[r], x[r + 1], x[r + 2]), max3(x[r + 3], x[r + 4], x[r + 5]), max3(x[r + 6], x[r + 7], x[r + 7]));
         mx = fmaxf(mx, __builtin_fmaf(gm, kmul_of(g, i), exponent_of(g, i)));
       }
       mx = max_halves(mx);
