@@ -542,12 +542,18 @@ hipError_t launch(const AttnArgs& p, hipStream_t stream) {
   // workgroup or two: two sets of waves in each (us with two sets / one / split:
   // 1000 rows of 32 heads over 4, D 128, 26.4 / - / 36.4; 1500 rows over 8 heads
   // 37 / 43 / 57; 1250 rows, D 64, 28 / 33 / 43). More: one set (4632 rows of
-  // 64 heads 382, with two sets 428).
+  // 64 heads 382, with two sets 428). From 257 on also where rows see too little to
+  // be shared out (us with one / two sets, single tokens, 8 heads: 41 sequences of 39
+  // tokens 5.6 / 9.1, 40 of up to 900 17.2 / 20.7; 12 prompts of 200 12.2 / 17.0; 6 of 400
+  // after up to 500 21.2 / 23.7), unless FewRows has two tiles a workgroup (30
+  // sequences of up to 900 tokens, 32 rows a head 26.8 / 21.4).
   const int64_t longest = reach(p) / (4 * UNIT);
   int64_t splits = pairs > 128 ? 1 : SPLIT_GROUPS / pairs;
   if (splits > longest) splits = longest;
   if (splits < 1) splits = 1;
-  const bool two = splits == 1 && pairs <= 512;
+  const int64_t rows = p.seq.T * p.group, S = p.seq.S;
+  const bool share = reach(p) >= 1024 || (rows > 16 * S && rows <= FEW_ROWS * S);
+  const bool two = splits == 1 && pairs <= (share ? 512 : 256);
   if (pairs * splits > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (two)
     hipLaunchKernelGGL((attention_prefill_kernel<D, 2>), dim3((unsigned)(pairs * splits)), dim3(2 * PWAVES * 64), 0, stream, p, (int)splits);
