@@ -145,8 +145,9 @@ struct FewRows {
             }
         // whatever lies behind the sequence, before every row's window or in a
         // block that is not held must not reach the product: 0 * NaN
+        // (both ends limited on both sides: a window may pass 2^31 tokens)
         const int64_t vhi = held ? q_len - tb : 0, vlo = tile_lo - tb;
-        const int hi = vhi > 16 ? 16 : (int)vhi, lo = vlo > 16 ? 16 : (int)vlo;
+        const int hi = vhi > 16 ? 16 : (vhi < 0 ? 0 : (int)vhi), lo = vlo > 16 ? 16 : (vlo < 0 ? 0 : (int)vlo);
 #pragma unroll
         for (int d = 0; d < DT; ++d) vr[d] = clear_outside(vr[d], lo, hi);
       } else {
