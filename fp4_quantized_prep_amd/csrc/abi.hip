@@ -531,12 +531,18 @@ int check_seq_batch(int64_t T, int32_t S, const int32_t* block_table, int64_t ld
   return IQP_OK;
 }
 
+// Sizes that the FP8 product takes: a workgroup keeps a weight tile's scale bytes
+// in one register (4 per lane), so at most 256 K blocks.
+bool gemm_sizes_supported(int64_t M, int64_t N, int64_t K) {
+  return M > 0 && M <= 0x7FFFFFFF && N > 0 && N <= 0x7FFFFFFF && K > 0 && K % 128 == 0 && K / 128 <= 256;
+}
+
 }  // namespace
 
 extern "C" {
 
 int64_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return M > 0 && N > 0 && K > 0 && iqp::fp8_gemm_splits(M, N, K) > 1 ? iqp::GEMM_WORKSPACE_BYTES : 0;
+  return gemm_sizes_supported(M, N, K) && iqp::fp8_gemm_splits(M, N, K) > 1 ? iqp::GEMM_WORKSPACE_BYTES : 0;
 }
 
 int fp8_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m, int64_t as_stride_w,
@@ -551,9 +557,8 @@ int fp8_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, 
   if (check_scale_strides(M, nw, as_stride_m, as_stride_w) != IQP_OK || ld_ws < K / 128) return IQP_ERR_INVALID;
   if (!aligned(a, 16) || lda % 16 || !aligned(w, 16) || ldw % 16 || !aligned(a_scales, 4) || !aligned(out, 2))
     return IQP_ERR_UNSUPPORTED;
-  // a workgroup keeps a weight tile's scale bytes in one register (4 per lane)
-  // and addresses its tiles of up to 256 rows with 32-bit offsets
-  if (K / 128 > 256 || M > 0x7FFFFFFF || N > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  if (!gemm_sizes_supported(M, N, K)) return IQP_ERR_UNSUPPORTED;
+  // tiles of up to 256 rows are addressed with 32-bit offsets
   if (lda > ((int64_t)1 << 22) || ldw > ((int64_t)1 << 22)) return IQP_ERR_UNSUPPORTED;
   if (as_stride_m >= ((int64_t)1 << 19) || as_stride_w >= ((int64_t)1 << 27) / nw) return IQP_ERR_UNSUPPORTED;
   const bool split = workspace && iqp::fp8_gemm_splits(M, N, K) > 1;

@@ -611,7 +611,8 @@ int iqp_device_clock_rates(int64_t* wall_clock_hz, int64_t* peak_shader_clock_hz
  *              memory, 256-byte aligned: with it a product of few output tiles
  *              and many K blocks is split over K (two launches). Its contents do
  *              not matter before and mean nothing after; calls that share one
- *              must not overlap. Where that size is 0 it is not used.
+ *              must not overlap. Where that size is 0 it is not used (also for
+ *              sizes that the product refuses).
  * M == 0 or N == 0: no-op. The sum must fit float32, as there. The order in
  * which K blocks are added depends on M, N, K and the workspace's presence only.
  */
