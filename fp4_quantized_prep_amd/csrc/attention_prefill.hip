@@ -87,11 +87,12 @@ __device__ __forceinline__ bool find_work(const AttnArgs& p, int64_t item, Work&
 // bits 0 .. n - 1, none below 0, all from 32 on
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : (1u << (n < 0 ? 0 : n)) - 1u; }
 
-// fmaxf of three in one instruction (the compiler would quiet each operand first)
+// The largest of three in one instruction, v_maximum3_f32 (for fmaxf the compiler would
+// quiet each operand first). Not inline asm: operands are MFMA results, and the
+// compiler counts the wait states behind an MFMA only to instructions of its own.
+// A NaN is kept; it makes its row NaN in any case.
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // largest of a lane's value and its partner's (lane ^ 32)
