@@ -17,6 +17,9 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int UNIT = 64;             // tokens the kernels take at a time
 constexpr float LOWEST = -1e30f;     // below every score: the running maximum before the first token
+// Weights are computed times a power of two, so that the largest that may occur is
+// 2^FP16_TOP: fp16 then holds those far below it as well as it can.
+constexpr float FP16_TOP = 15.f;
 
 // eight E4M3 codes as bf16 / fp16: exact, without their block's scale
 __device__ __forceinline__ v8bf widen_bf16(uint32_t a, uint32_t b) {

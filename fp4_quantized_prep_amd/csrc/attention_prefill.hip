@@ -358,7 +358,9 @@ struct Prefill {
       }
       mx = max_halves(mx);
       // m follows the maximum only where it rose by more than SLACK (log2):
-      // weights then stay below 2^SLACK, and what is summed is seldom rescaled
+      // what is summed is then seldom rescaled, and weights, computed times
+      // 2^(FP16_TOP - SLACK), stay below 2^FP16_TOP. Those that fp16 holds as
+      // subnormals, below 2^-21 of the largest, are off by at most 2^-32 of it
       if (__ballot(mx > m + SLACK) != 0) {
         const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
         m = mn;
@@ -375,7 +377,7 @@ struct Prefill {
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         km[i] = kmul_of(g, i);
-        cm[i] = exponent_of(g, i) - m;
+        cm[i] = exponent_of(g, i) - (m - (FP16_TOP - SLACK));
       }
       auto weights = [&](int i, int j) __attribute__((always_inline)) {   // scores j, j + 1 of granule i
         const v16f& x = sc[i >> 1];

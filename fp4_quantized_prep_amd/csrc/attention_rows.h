@@ -15,9 +15,11 @@
 //   * The keys widen to bf16 (exact) and meet bf16 queries. The block's key
 //     scale multiplies the scores. The values widen to fp16 without their
 //     scale (every E4M3 value is one); the probabilities carry it instead:
-//     with w'_t = 2^(s_t + e_t - max(s + e)), s in units of log2 and e_t the
-//     value exponent, w' <= 1 rounds to fp16 (2^-11 relative, half of what
-//     bf16 would lose) and sum w = sum w' 2^-e, kept in float32.
+//     with w'_t = 2^(15 + s_t + e_t - max(s + e)), s in units of log2 and e_t the
+//     value exponent, w' <= 2^15 rounds to fp16 (2^-11 relative, an eighth of what
+//     bf16 would lose; below 2^-29 of the largest, where fp16 is subnormal,
+//     2^-40 of the largest) and sum w = sum w' 2^-e, kept in float32. The power
+//     of two leaves with the division.
 //   * The waves' results, each relative to its own maximum, meet in LDS.
 #pragma once
 
@@ -172,12 +174,13 @@ struct FewRows {
         const float alpha = __builtin_amdgcn_exp2f(m[t] - mn);
         m[t] = mn;
         float sum = 0.f;
+        const float top = mn - FP16_TOP;
         float w[16];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float x = __builtin_amdgcn_exp2f(sc[t][c][r] - mn);
+            const float x = __builtin_amdgcn_exp2f(sc[t][c][r] - top);
             w[4 * c + r] = x;
             sum += x;
           }

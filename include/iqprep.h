@@ -720,11 +720,16 @@ int kv_cache_read_fp8(const void* k_cache, const void* v_cache, const uint8_t* k
  * tokens t <= p (and t > p - window where window > 0) of key head h / (Hq / Hk):
  *   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q . k_t)
  * with k_t, v_t the values the cache stands for; zeros where there is no such
- * token. Scores, maxima and sums are float32; the weights w_t are rounded to
- * fp16 for the second product, relative to the row's largest w_t 2^e_t (e_t the
- * value exponent of t's block). The value exponents that a row sees may lie up to
- * 100 apart (always so where no value written exceeds 2^86): beyond that the
- * smaller ones' weights are lost from the sum.
+ * token. Scores, maxima and sums are float32. For the second product the weights
+ * are rounded to fp16 relative to the row's largest w_t 2^e_t (e_t the value
+ * exponent of t's block): each is off by at most 2^-11 of itself, and those below
+ * 2^-21 of the largest by at most 2^-32 of the largest. The latter moves the output
+ * of a row that sees n tokens by at most n 2^-31 times the largest value of the
+ * block of the largest w_t 2^e_t (an eighth of bf16's own half step at a million
+ * tokens of like sizes). The value exponents that a row sees may lie up to 100
+ * apart (always so where no value written exceeds 2^86), and must not lie below
+ * -80 (what kv_cache_append_fp8 writes does not lie below -22): beyond that weights
+ * are lost from the sum.
  *
  *   q, out     bf16 [T, Hq*D], row strides ldq, ldo (elements); 16-byte
  *              aligned, strides multiples of 8; out must not overlap q. Rows
