@@ -170,17 +170,20 @@ struct FewRows {
           for (int r = 0; r < 4; ++r) mx = fmaxf(mx, sc[t][c][r]);
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m[t], mx);
+        // m: the largest score so far less FP16_TOP, or the score itself where that
+        // difference would not be exact enough: weights stay within fp16
+        float top = mx - FP16_TOP;
+        top = mx - top > FP16_TOP ? mx : top;
+        const float mn = fmaxf(m[t], top);
         const float alpha = __builtin_amdgcn_exp2f(m[t] - mn);
         m[t] = mn;
         float sum = 0.f;
-        const float top = mn - FP16_TOP;
         float w[16];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float x = __builtin_amdgcn_exp2f(sc[t][c][r] - top);
+            const float x = __builtin_amdgcn_exp2f(sc[t][c][r] - mn);
             w[4 * c + r] = x;
             sum += x;
           }
