@@ -115,7 +115,7 @@ struct Prefill {
   static constexpr int DT = D / 32;             // output tiles
   static constexpr int K_BYTES = U * D * 2, V_BYTES = D * U * 2;
   static constexpr int SET_BYTES = 2 * (K_BYTES + V_BYTES), LDS_BYTES = SETS * SET_BYTES;
-  static constexpr int VOTE_BYTES = 4 * SETS * PWAVES;   // LDS's last: whether a wave met a large score
+  static constexpr int FLAG_BYTES = 4 * SETS * PROWS;   // LDS's last: whether a row met a large score
 
   // Where 16-byte chunk c of a key row, of a value row lies in it. A read takes one
   // chunk of 16 rows, which then lie in distinct banks of 64; a store every second
@@ -134,24 +134,35 @@ struct Prefill {
                   // load, so that nothing waits for the codes loaded behind them
   };
 
-  // The tile's rows as the decode kernel computes them, 16 at a time
+  // whether each row of the tile met a large score, in each set of waves
+  static __device__ __forceinline__ int* large_flags(uint8_t* lds_all) { return reinterpret_cast<int*>(lds_all + LDS_BYTES - FLAG_BYTES); }
+  static __device__ __forceinline__ bool is_large(const int* flags, int row) {
+    return (SETS == 1 ? flags[row] : flags[row] | flags[PROWS + row]) != 0;
+  }
+
+  // The tile's rows, or those that are large alone, as the decode kernel computes them
+  template <bool LARGE_ONLY>
   static __device__ __forceinline__ void few_rows(const AttnArgs& p, int splits, uint8_t* lds_all, const Work& w, int head, int z,
                                                   int64_t u_lo, int64_t u_hi) {
     using Few = FewRows<D, 1, SETS * PWAVES>;
-    static_assert(sizeof(typename Few::Lds) <= LDS_BYTES - VOTE_BYTES, "in the units' place");
+    static_assert(sizeof(typename Few::Lds) <= LDS_BYTES - FLAG_BYTES, "in the units' place");
     PartialTile<D>& part = reinterpret_cast<PartialTile<D>*>(p.workspace)[blockIdx.x];
     const SeqRows seq = {w.s, (int)w.begin, (int)(w.begin + w.n), (int)w.len};
     const int64_t u0 = u_lo + (u_hi - u_lo) * z / splits, u1 = u_lo + (u_hi - u_lo) * (z + 1) / splits;
     const int64_t end = w.row0 + PROWS < w.rows ? w.row0 + PROWS : w.rows;
+    const int* const flags = large_flags(lds_all);
     for (int64_t r0 = w.row0; r0 < end; r0 += Few::ROWS) {
+      const int at = (int)(r0 - w.row0);
+      if (LARGE_ONLY && __ballot(is_large(flags, at + (threadIdx.x & (Few::ROWS - 1)))) == 0) continue;
       Few::run(p, seq, r0, head, u0, u1 - u0, *reinterpret_cast<typename Few::Lds*>(lds_all),
                [&](int r, int d, float mx, float sum, v4f acc) __attribute__((always_inline)) {
+        if (LARGE_ONLY && !is_large(flags, at + r)) return;
         if (splits == 1) {
           const float inv = inverse_sum(sum);
           uint16_t* const dst = p.out + row_offset(w.begin, r0 + r, head, p.group, D, p.ldo) + d;
           *reinterpret_cast<v2u*>(dst) = v2u{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
         } else {
-          const int i = (int)(r0 - w.row0) + r;
+          const int i = at + r;
           *reinterpret_cast<v4f*>(&part.o[i][d]) = acc;
           if (d == 0) {
             part.m[i] = mx;
@@ -163,8 +174,8 @@ struct Prefill {
     }
   }
 
-  // The tile's rows on 32x32 MFMAs. False, and nothing written, where some score was
-  // too large for that (below); uniform over the workgroup.
+  // The tile's rows on 32x32 MFMAs. Whether some of them, not written then, have scores
+  // too large for that (below): LDS holds which ones.
   static __device__ __forceinline__ bool many_rows(const AttnArgs& p, int splits, uint8_t* lds_all, const Work& w, int head, int z,
                                                    int64_t u_lo, int64_t u_hi) {
     const int tid = threadIdx.x % (64 * PWAVES), lane = tid & 63, half = lane >> 5, col = lane & 31;
@@ -265,7 +276,7 @@ struct Prefill {
     };
 
     float m = LOWEST, l = 0.f;
-    bool large = false;               // uniform over the wave
+    bool large = false;
     v16f o[DT];
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -367,8 +378,8 @@ struct Prefill {
         const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - mn);
         // A weight's exponent takes score, factor and maximum in one rounding, but the
         // maximum was rounded before: off by half its step, which from LARGE on could put
-        // all of a row's weights beyond fp16, at either end
-        large |= __ballot(mx > m + SLACK && fabsf(mx) >= LARGE) != 0;
+        // all of the row's weights beyond fp16, at either end
+        large |= mx > m + SLACK && fabsf(mx) >= LARGE;
         m = mn;
         l *= alpha;
 #pragma unroll
@@ -456,23 +467,23 @@ struct Prefill {
       if (u < turns) unit(u, std::integral_constant<int, 0>{});
     }
 
-    // Large scores anywhere in the tile: false, for FewRows, which subtracts the maximum from
-    // scores that are rounded as it was. (Rounding the scores so here, in a branch of each
-    // unit, costs the mixed batch 3 %, this vote 12 prompts of 200 tokens 2 %: 13.6 -> 13.9 us.)
-    int* const votes = reinterpret_cast<int*>(lds_all + LDS_BYTES - VOTE_BYTES);
+    // A row with large scores is left to FewRows, which subtracts the maximum from scores
+    // that are rounded as it was. (Rounding the scores so here, in a branch of each unit,
+    // costs the mixed batch 3 %, these flags 12 prompts of 200 tokens 2 %: 13.6 -> 13.9 us.)
+    bool any_large = false;
     if (turns > 0) {
-      if (lane == 0) votes[PWAVES * set + wave] = large;
+      int* const flags = large_flags(lds_all);
+      if (half == 0) flags[PROWS * set + 32 * wave + col] = large && m < INFINITY;   // (infinite: NaN either way)
       __syncthreads();
+      int any = 0;
 #pragma unroll
-      for (int i = 0; i < SETS * PWAVES; ++i) large |= votes[i] != 0;
-      if (__builtin_expect(__builtin_amdgcn_readfirstlane(large) != 0, 0)) {
-        __syncthreads();   // before LDS is used again
-        return false;
-      }
+      for (int i = 0; i < SETS * PROWS; i += 64) any |= flags[i + lane];
+      any_large = __ballot(any != 0) != 0;
+      large = is_large(flags, 32 * wave + col);
     }
 
     if constexpr (SETS > 1) {
-      static_assert(64 * PWAVES * (64 * DT + 8) <= LDS_BYTES - VOTE_BYTES, "beside the votes");
+      static_assert(64 * PWAVES * (64 * DT + 8) <= LDS_BYTES - FLAG_BYTES, "beside the flags");
       // the sets' results, lane for lane: the second's go through LDS
       constexpr int THREADS = 64 * PWAVES;
       v4f* const to = reinterpret_cast<v4f*>(lds_all) + tid;
@@ -486,7 +497,7 @@ struct Prefill {
           for (int a = 0; a < 4; ++a) to[(4 * t + a) * THREADS] = v4f{o[t][4 * a], o[t][4 * a + 1], o[t][4 * a + 2], o[t][4 * a + 3]};
       }
       __syncthreads();
-      if (set > 0) return true;
+      if (set > 0) return any_large;
       const float m1 = stats[0], mn = fmaxf(m, m1), a0 = __builtin_amdgcn_exp2f(m - mn), a1 = __builtin_amdgcn_exp2f(m1 - mn);
       m = mn;
       l = l * a0 + stats[THREADS] * a1;
@@ -500,7 +511,7 @@ struct Prefill {
         }
     }
     l = sum_halves(l);
-    if (row >= w.rows) return true;
+    if (row >= w.rows || large) return any_large;
     if (splits == 1) {
       const float inv = inverse_sum(l);
       uint16_t* const dst = p.out + row_offset(w.begin, row, head, p.group, D, p.ldo) + 4 * half;
@@ -524,7 +535,7 @@ struct Prefill {
           *reinterpret_cast<v4f*>(&part.o[r0][32 * t + 8 * a + 4 * half]) =
               v4f{o[t][4 * a], o[t][4 * a + 1], o[t][4 * a + 2], o[t][4 * a + 3]};
     }
-    return true;
+    return any_large;
   }
 
   static __device__ __forceinline__ void run(const AttnArgs& p, int splits, uint8_t* lds_all) {
@@ -536,10 +547,13 @@ struct Prefill {
 
     const int64_t u_lo = w.lo / U, u_hi = w.hi > w.lo ? (w.hi + U - 1) / U : u_lo;
     if (w.rows - w.row0 <= FEW_ROWS) {
-      few_rows(p, splits, lds_all, w, head, z, u_lo, u_hi);
+      few_rows<false>(p, splits, lds_all, w, head, z, u_lo, u_hi);
       return;
     }
-    if (!many_rows(p, splits, lds_all, w, head, z, u_lo, u_hi)) few_rows(p, splits, lds_all, w, head, z, u_lo, u_hi);
+    if (__builtin_expect(many_rows(p, splits, lds_all, w, head, z, u_lo, u_hi), 0)) {
+      __syncthreads();   // the sets' results are read
+      few_rows<true>(p, splits, lds_all, w, head, z, u_lo, u_hi);
+    }
   }
 };
 
