@@ -16,7 +16,7 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int UNIT = 64;             // tokens the kernels take at a time
-constexpr float LOWEST = -1e30f;     // below every score: the running maximum before the first token
+constexpr float LOWEST = -3.402823466e38f;   // no score lies below: the running maximum before the first token
 // Weights are computed times a power of two, so that the largest that may occur is
 // 2^FP16_TOP: fp16 then holds those far below it as well as it can.
 constexpr float FP16_TOP = 15.f;

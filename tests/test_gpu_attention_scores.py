@@ -50,3 +50,12 @@ def one_token_each(lib, lens, new, d, width, size, steps, other):
     # four significant bits a value, off by a few 2^-24 before it is rounded to bf16
     bad = (got != want).any(-1)
     assert not bool(bad.any()), (int(bad.sum()), got[bad][0, :4].tolist(), want[bad][0, :4].tolist())
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new", [([200], [1]), ([200, 90], [2, 3]), ([200, 160], [190, 60]), ([200] * 5, [200] * 5)])
+def test_scores_far_below_zero(gpu_lib, lens, new, d, width):
+    """Rows all of whose scores lie below -10^30: still the token that outweighs the others."""
+    print("attend scores below zero", lens, new, d, width, flush=True)
+    one_token_each(gpu_lib, lens, new, d, width, -2.0 ** 100, {0: 352.0, 3: 176.0, 20: 88.0, 70: 44.0, 150: 9.0}, 448.0)
