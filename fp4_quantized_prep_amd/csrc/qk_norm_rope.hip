@@ -112,6 +112,15 @@ void qk_norm_rope_kernel(QkNormRopeArgs p) {
     wk_p = *reinterpret_cast<const v4u*>(p.k_weight + 8 * partner_l);
   }
 
+  auto put = [&](int h, v4u out) __attribute__((always_inline)) {
+    v4u* dst = reinterpret_cast<v4u*>(h < p.Hq ? p.q_out + token * p.ldqo + (int64_t)h * D + 8 * l
+                                               : p.k_out + token * p.ldko + (int64_t)(h - p.Hq) * D + 8 * l);
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(out, dst);
+    else
+      *dst = out;
+  };
+  uint64_t infinite[PASSES] = {};          // lanes of heads whose sum of squares is infinite
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int h = head0 + HEADS * i;
@@ -125,6 +134,7 @@ void qk_norm_rope_kernel(QkNormRopeArgs p) {
       sum += b * b;
     }
     sum = lanes_sum<LANES>(sum);
+    if constexpr (INTERLEAVED) infinite[i] = __ballot(sum == INFINITY);
     const float r = 1.f / sqrtf(sum * (1.f / D) + p.eps);
     const v4u w = is_q ? wq : wk;
     float y[8];
@@ -147,13 +157,22 @@ void qk_norm_rope_kernel(QkNormRopeArgs p) {
         out[j] = pack_bf16(y[2 * j] * c[2 * j] + lo * s[2 * j], y[2 * j + 1] * c[2 * j + 1] + hi * s[2 * j + 1]);
       }
     }
-    if (h < total) {
-      v4u* dst = reinterpret_cast<v4u*>(is_q ? p.q_out + token * p.ldqo + (int64_t)h * D + 8 * l
-                                             : p.k_out + token * p.ldko + (int64_t)(h - p.Hq) * D + 8 * l);
-      if constexpr (STREAM)
-        __builtin_nontemporal_store(out, dst);
-      else
-        *dst = out;
+    if (h < total) put(h, out);
+  }
+  // Behind the rotated dims an interleaved pair's other value came in times sin 0: NaN
+  // where that one is infinite. Those heads' dims again, unrotated: x / infinity. (A
+  // half-split pair is there a value and itself.)
+  if constexpr (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      if (infinite[i] == 0) continue;
+      const int h = head0 + HEADS * i;
+      const v4u w = h < p.Hq ? wq : wk;
+      v4u out;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        out[j] = pack_bf16(bf16_lo(x[i][j]) * 0.f * bf16_lo(w[j]), bf16_hi(x[i][j]) * 0.f * bf16_hi(w[j]));
+      if (h < total && !turned && (infinite[i] >> lane & 1) != 0) put(h, out);
     }
   }
 }

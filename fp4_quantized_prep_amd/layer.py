@@ -53,7 +53,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6
 
     q, k: bf16 [M, H * head_dim] or [M, H, head_dim], rows contiguous, any row
     strides that are multiples of 8 (column ranges of a fused projection's rows); q_weight,
-    k_weight: bf16 [head_dim]; positions: int64 [M]; cos_sin: float32 [max_pos,
+    k_weight: bf16 [head_dim], finite; positions: int64 [M]; cos_sin: float32 [max_pos,
     rope_dim], the table of :func:`rope_cos_sin_table`, rope_dim a multiple of
     16 up to head_dim. rope_layout: pairs (i, i + rope_dim/2) "half_split", or
     (2i, 2i+1) "interleaved". head_dim: 64, 128 or 256. Returns ``(q_out,

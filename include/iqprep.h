@@ -638,7 +638,7 @@ int fp8_gemm_1x128_128x128(const void* a, int64_t lda,
  *              16-byte aligned, strides multiples of 8.
  *   q_out, k_out   likewise, strides ldqo, ldko; may be q and k themselves (same
  *              strides), otherwise must not overlap them.
- *   q_weight, k_weight   bf16 [D], 16-byte aligned.
+ *   q_weight, k_weight   bf16 [D], 16-byte aligned, finite.
  *   D          64, 128 or 256; rope_dim a multiple of 16, 16 to D; eps >= 0.
  *   positions, cos_sin, max_pos   as in indexer_q_gemm_rope_fp4 (table of
  *              rope_dim columns; positions outside it are clamped).
