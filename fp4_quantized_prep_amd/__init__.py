@@ -7,7 +7,8 @@ memory and streams, nothing else.
 
 If the library has not been built, importing this package raises ImportError
 (build it with ``python fp4_quantized_prep_amd/build.py``); there is no
-fallback implementation.
+fallback implementation. The attention layer's operators go through
+``_binding.so`` besides, and raise ImportError when called without it.
 """
 import contextlib
 import ctypes
@@ -58,9 +59,9 @@ IQP_ERR_HIP = 3
 
 
 def _load():
-    for path in (LIB_PATH, os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")):
-        if not os.path.exists(path):
-            raise ImportError(f"{path} is missing: build it with `python fp4_quantized_prep_amd/build.py`")
+    if not os.path.exists(LIB_PATH):
+        raise ImportError(
+            f"{LIB_PATH} is missing: build it with `python fp4_quantized_prep_amd/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     c_i64, c_i32, c_p, c_dbl = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_double
     lib.fp8_quant_1x128_ue8m0.argtypes = [c_p, c_i64, c_i64, c_i64, c_p, c_i64, c_p, c_i64, c_i64, c_p]

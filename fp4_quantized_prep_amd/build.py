@@ -46,7 +46,8 @@ def compile_flags() -> list:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile and link the library; returns its path. Raises on failure."""
+    """Compile and link the library and the binding; returns the library's path.
+    Raises on failure, and then leaves the built files as they were."""
     sources = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     if not sources:
         raise RuntimeError(f"no HIP sources under {CSRC}")
@@ -67,38 +68,39 @@ def build(verbose: bool = False) -> str:
     jobs = max(1, min(8, len(os.sched_getaffinity(0))))
     with concurrent.futures.ThreadPoolExecutor(jobs) as pool:
         objs = list(pool.map(compile_one, sources))
-    tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
+    lib = os.path.join(obj_dir, LIB_NAME)     # under its own name, which the binding records
+    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", lib] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB_PATH)
-    build_binding(verbose)
+    binding = build_binding(obj_dir, verbose)
+    os.replace(lib, LIB_PATH)
+    os.replace(binding, BINDING_PATH)
     return LIB_PATH
 
 
-def build_binding(verbose: bool = False) -> str:
-    """Compile csrc/binding.cpp against torch and libiqprep.so; host code only."""
+def build_binding(lib_dir: str, verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp against torch and lib_dir's libiqprep.so, into
+    lib_dir; host code only."""
     import sysconfig
 
     import torch
     import torch.utils.cpp_extension as ext
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING_PATH + ".tmp"
+    path = os.path.join(lib_dir, os.path.basename(BINDING_PATH))
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
            "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += [f"-I{INCLUDE}"] + [f"-isystem{d}" for d in ext.include_paths() + ["/opt/rocm/include", sysconfig.get_paths()["include"]]]
-    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{torch_lib}", "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_hip",
-            f"-L{PKG_DIR}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", path, f"-L{torch_lib}", "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_hip",
+            f"-L{lib_dir}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"the binding's build failed:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, BINDING_PATH)
-    return BINDING_PATH
+    return path
 
 
 if __name__ == "__main__":

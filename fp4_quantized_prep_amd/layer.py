@@ -6,14 +6,32 @@ import typing
 
 import torch
 
-from . import _binding, _check, _lib
+from . import _check, _lib
 
 __all__ = [
     "fp8_gemm_1x128_128x128", "fp8_gemm_workspace_bytes", "qk_norm_rope", "Fp8KvCache", "fp8_kv_cache", "kv_cache_append_fp8", "kv_cache_read_fp8",
     "attention_fp8_kv", "attention_fp8_kv_workspace_bytes", "attention_fp8_kv_workspace",
 ]
 
-_binding.set_error(_check)
+
+class _NoBinding:
+    """Stands for _binding.so where that does not load: the rest of the package
+    needs the C library alone."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError("the attention layer's operators need fp4_quantized_prep_amd/_binding.so, which is missing or does not "
+                          f"load ({self.why}): build it with `python fp4_quantized_prep_amd/build.py`")
+
+
+try:
+    from . import _binding
+except ImportError as e:
+    _binding = _NoBinding(str(e))
+else:
+    _binding.set_error(_check)
 
 
 def _on(stream, tensor, fn, *args):
