@@ -115,6 +115,8 @@ def _load():
                                            c_p, c_i64, c_p, c_i64, c_p]
     lib.fp8_gemm_workspace_bytes.argtypes = [c_i64, c_i64, c_i64]
     lib.fp8_gemm_workspace_bytes.restype = c_i64
+    lib.iqp_debug_fp8_gemm_kernel.argtypes = [c_i64, c_i64, c_i64, c_i32]
+    lib.iqp_debug_fp8_gemm_kernel.restype = ctypes.c_char_p
     lib.qk_norm_rope.argtypes = [c_p, c_i64, c_p, c_i64, c_i64, c_i32, c_i32, c_i32, c_i32, c_p, c_p, c_f32, c_p, c_p,
                                  c_i64, c_p, c_i64, c_p, c_i64, c_i32, c_p]
     batch_args = [c_p, c_i64, c_i32, c_p, c_p, c_i32]

@@ -545,6 +545,11 @@ int64_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return gemm_sizes_supported(M, N, K) && iqp::fp8_gemm_splits(M, N, K) > 1 ? iqp::GEMM_WORKSPACE_BYTES : 0;
 }
 
+const char* iqp_debug_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int32_t with_workspace) {
+  if (!gemm_sizes_supported(M, N, K)) return "";
+  return iqp::fp8_gemm_kernel_name(iqp::fp8_gemm_kernel(M, N, K, with_workspace ? iqp::fp8_gemm_splits(M, N, K) : 1));
+}
+
 int fp8_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m, int64_t as_stride_w,
                            const void* w, int64_t ldw, const uint8_t* w_scales, int64_t ld_ws, int64_t M, int64_t N,
                            int64_t K, void* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {

@@ -511,11 +511,11 @@ hipError_t launch_split(const Fp8GemmArgs& p, hipStream_t stream) {
 // 8192, K 640 .. 7168; us a block for up to 256 workgroups, for up to 512:
 //   64x64 0.32, 0.52;  128x64 0.42, 0.69;  128x128 four stages 0.56, 1.13;
 //   128x128 two stages 0.75, 0.9;  256x256 1.3, 2.6 (an area 16 times the first's)
-double tile_us(const Fp8GemmArgs& p, int TN, int TM, double fixed, double block, double more, int group) {
-  const int64_t tiles = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
+double tile_us(int64_t M, int64_t N, int64_t nkb, int TN, int TM, double fixed, double block, double more, int group) {
+  const int64_t tiles = ((M + TM - 1) / TM) * ((N + TN - 1) / TN);
   const int64_t rounds = (tiles + 255) / 256;
   const int64_t turns = (rounds + group - 1) / group;      // `group` workgroups share a CU
-  return turns * fixed + p.nkb * (turns * block + (rounds - turns) * more);
+  return turns * fixed + nkb * (turns * block + (rounds - turns) * more);
 }
 
 }  // namespace
@@ -534,30 +534,71 @@ int fp8_gemm_splits(int64_t M, int64_t N, int64_t K) {
   return z >= 2 && nkb - nkb / z >= 16 ? (int)z : 1;
 }
 
-hipError_t launch_fp8_gemm(const Fp8GemmArgs& p, hipStream_t stream) {
+GemmKernel fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int splits) {
   // Up to 64 tokens the product is a read of the weights (64x1500x7168, us: stream
   // kernel 10.1, 64x64 tiles 19.2; 64x7168x8192 20.3, 26.9; 64x4000x1536 5.5, 6.7); 16 or
   // 32 rows of them a workgroup, by which of the two gives the CUs enough
   // workgroups (32 / 16 rows: 16x7168x8192 13.6 / 15.3, 32x7168x8192 15.6 / 20.0,
   // 64x7168x8192 20.3 / 28.3, 40x8192x1536 6.5 / 8.7; 16x1536x7168 7.2 / 5.6,
   // 32x2000x7168 8.6 / 7.0, 64x4000x1536 6.2 / 5.5).
-  if (p.M <= 16) return p.N >= 6144 ? launch_stream<2, 1, 8, 3>(p, stream) : launch_stream<1, 1, 4, 4>(p, stream);
-  if (p.M <= 32) return p.N >= 6144 ? launch_stream<2, 2, 8, 2>(p, stream) : launch_stream<1, 2, 4, 3>(p, stream);
-  if (p.M <= 64) return p.N >= 6144 ? launch_stream<2, 4, 4, 3>(p, stream) : launch_stream<1, 4, 4, 3>(p, stream);
-  if (p.splits > 1) return launch_split(p, stream);
-  const double t64 = tile_us(p, 64, 64, 1.5, 0.31, 0.23, 2), t128x64 = tile_us(p, 128, 64, 2.0, 0.41, 0.3, 2),
-               t128 = tile_us(p, 128, 128, 3.0, 0.54, 0.54, 1), t128x2 = tile_us(p, 128, 128, 3.0, 0.73, 0.18, 2),
-               t256 = tile_us(p, 256, 256, 5.0, 1.28, 1.28, 1);
-  double best = t64;
-  if (t128x64 < best) best = t128x64;
-  if (t128 < best) best = t128;
-  if (t128x2 < best) best = t128x2;
-  if (t256 < best) best = t256;
-  if (best == t64) return launch_tile<64, 64, 2, 2, 4>(p, stream);
-  if (best == t128x64) return launch_tile<128, 64, 2, 2, 3>(p, stream);
-  if (best == t128) return launch_tile<128, 128, 2, 2, 4>(p, stream);
-  if (best == t128x2) return launch_tile<128, 128, 2, 2, 2>(p, stream);
-  return launch_tile<256, 256, 2, 4, 2>(p, stream);
+  if (M <= 64) {
+    const bool wide = N >= 6144;
+    if (M <= 16) return wide ? GEMM_STREAM_32x16 : GEMM_STREAM_16x16;
+    if (M <= 32) return wide ? GEMM_STREAM_32x32 : GEMM_STREAM_16x32;
+    return wide ? GEMM_STREAM_32x64 : GEMM_STREAM_16x64;
+  }
+  if (splits > 1) return GEMM_SPLIT_64x64;
+  const int64_t nkb = K / 128;
+  const struct {
+    GemmKernel kernel;
+    double us;
+  } tiles[] = {
+      {GEMM_TILE_64x64, tile_us(M, N, nkb, 64, 64, 1.5, 0.31, 0.23, 2)},
+      {GEMM_TILE_128x64, tile_us(M, N, nkb, 128, 64, 2.0, 0.41, 0.3, 2)},
+      {GEMM_TILE_128x128, tile_us(M, N, nkb, 128, 128, 3.0, 0.54, 0.54, 1)},
+      {GEMM_TILE_128x128_TWO, tile_us(M, N, nkb, 128, 128, 3.0, 0.73, 0.18, 2)},
+      {GEMM_TILE_256x256, tile_us(M, N, nkb, 256, 256, 5.0, 1.28, 1.28, 1)},
+  };
+  int best = 0;
+  for (int i = 1; i < 5; ++i)
+    if (tiles[i].us < tiles[best].us) best = i;
+  return tiles[best].kernel;
+}
+
+const char* fp8_gemm_kernel_name(GemmKernel kernel) {
+  switch (kernel) {
+    case GEMM_STREAM_16x16: return "stream 16x16";
+    case GEMM_STREAM_32x16: return "stream 32x16";
+    case GEMM_STREAM_16x32: return "stream 16x32";
+    case GEMM_STREAM_32x32: return "stream 32x32";
+    case GEMM_STREAM_16x64: return "stream 16x64";
+    case GEMM_STREAM_32x64: return "stream 32x64";
+    case GEMM_SPLIT_64x64: return "split 64x64";
+    case GEMM_TILE_64x64: return "tile 64x64";
+    case GEMM_TILE_128x64: return "tile 128x64";
+    case GEMM_TILE_128x128: return "tile 128x128";
+    case GEMM_TILE_128x128_TWO: return "tile 128x128, two stages";
+    case GEMM_TILE_256x256: return "tile 256x256";
+  }
+  return "";
+}
+
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& p, hipStream_t stream) {
+  switch (fp8_gemm_kernel(p.M, p.N, (int64_t)p.nkb * 128, p.splits)) {
+    case GEMM_STREAM_16x16: return launch_stream<1, 1, 4, 4>(p, stream);
+    case GEMM_STREAM_32x16: return launch_stream<2, 1, 8, 3>(p, stream);
+    case GEMM_STREAM_16x32: return launch_stream<1, 2, 4, 3>(p, stream);
+    case GEMM_STREAM_32x32: return launch_stream<2, 2, 8, 2>(p, stream);
+    case GEMM_STREAM_16x64: return launch_stream<1, 4, 4, 3>(p, stream);
+    case GEMM_STREAM_32x64: return launch_stream<2, 4, 4, 3>(p, stream);
+    case GEMM_SPLIT_64x64: return launch_split(p, stream);
+    case GEMM_TILE_64x64: return launch_tile<64, 64, 2, 2, 4>(p, stream);
+    case GEMM_TILE_128x64: return launch_tile<128, 64, 2, 2, 3>(p, stream);
+    case GEMM_TILE_128x128: return launch_tile<128, 128, 2, 2, 4>(p, stream);
+    case GEMM_TILE_128x128_TWO: return launch_tile<128, 128, 2, 2, 2>(p, stream);
+    case GEMM_TILE_256x256: return launch_tile<256, 256, 2, 4, 2>(p, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace iqp

@@ -212,6 +212,24 @@ struct Fp8GemmArgs {
 constexpr int GEMM_SPLIT_GROUPS = 256;
 constexpr int64_t GEMM_WORKSPACE_BYTES = (int64_t)GEMM_SPLIT_GROUPS * 64 * 64 * 4;
 int fp8_gemm_splits(int64_t M, int64_t N, int64_t K);
+// The product's kernels: weight rows x tokens of a workgroup.
+enum GemmKernel {
+  GEMM_STREAM_16x16,
+  GEMM_STREAM_32x16,
+  GEMM_STREAM_16x32,
+  GEMM_STREAM_32x32,
+  GEMM_STREAM_16x64,
+  GEMM_STREAM_32x64,
+  GEMM_SPLIT_64x64,
+  GEMM_TILE_64x64,
+  GEMM_TILE_128x64,
+  GEMM_TILE_128x128,        // four LDS stages
+  GEMM_TILE_128x128_TWO,    // two, so that two workgroups share a CU
+  GEMM_TILE_256x256,
+};
+// the one that a product takes, in `splits` pieces of its K blocks
+GemmKernel fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int splits);
+const char* fp8_gemm_kernel_name(GemmKernel kernel);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& args, hipStream_t stream);
 
 struct QkNormRopeArgs {

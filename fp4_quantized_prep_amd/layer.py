@@ -9,7 +9,7 @@ import torch
 from . import _check, _lib
 
 __all__ = [
-    "fp8_gemm_1x128_128x128", "fp8_gemm_workspace_bytes", "qk_norm_rope", "Fp8KvCache", "fp8_kv_cache", "kv_cache_append_fp8", "kv_cache_read_fp8",
+    "fp8_gemm_1x128_128x128", "fp8_gemm_workspace_bytes", "debug_fp8_gemm_kernel", "qk_norm_rope", "Fp8KvCache", "fp8_kv_cache", "kv_cache_append_fp8", "kv_cache_read_fp8",
     "attention_fp8_kv", "attention_fp8_kv_workspace_bytes", "attention_fp8_kv_workspace",
 ]
 
@@ -46,6 +46,12 @@ def _on(stream, tensor, fn, *args):
 def fp8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
     """Bytes of the workspace that :func:`fp8_gemm_1x128_128x128` can use (0: none)."""
     return int(_lib.fp8_gemm_workspace_bytes(M, N, K))
+
+
+def debug_fp8_gemm_kernel(M: int, N: int, K: int, workspace: bool = True) -> str:
+    """Name of the kernel that :func:`fp8_gemm_1x128_128x128` takes for these
+    sizes ("" where it refuses them), for tests that mean to reach each."""
+    return _lib.iqp_debug_fp8_gemm_kernel(M, N, K, int(workspace)).decode()
 
 
 def fp8_gemm_1x128_128x128(a, a_scales, w, w_scales, out=None, workspace=None, stream=None):

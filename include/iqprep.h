@@ -624,6 +624,15 @@ int fp8_gemm_1x128_128x128(const void* a, int64_t lda,
                            void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * iqp_debug_fp8_gemm_kernel — the name of the kernel that
+ * fp8_gemm_1x128_128x128 takes for these sizes, with a workspace or without
+ * ("stream 32x16", "tile 256x256": weight rows x tokens of a workgroup), "" for
+ * sizes that it refuses. Static storage; touches no device. For tests that mean
+ * to reach each of them.
+ */
+const char* iqp_debug_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int32_t with_workspace);
+
+/*
  * qk_norm_rope — RMS norm of every query and key head, times its weights,
  * then RoPE, in one pass.
  *
