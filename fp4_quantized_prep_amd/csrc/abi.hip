@@ -694,7 +694,8 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
                      const int32_t* seq_lens, const int32_t* cu_rows, int32_t S, float scale, int32_t window, void* out,
                      int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
   iqp::AttnArgs p{};
-  if (Hq < 0 || window < 0 || !(scale > 0.f) || scale > 3e38f) return IQP_ERR_INVALID;
+  // (a scale beyond these would leave float32 together with log2(e) or a key scale)
+  if (Hq < 0 || window < 0 || !(scale >= 0x1p-64f && scale <= 0x1p64f)) return IQP_ERR_INVALID;
   int st = check_seq_batch(T, S, block_table, ld_table, max_blocks, seq_lens, cu_rows, n_blocks, block_size, Hk, D, p.seq);
   if (st != IQP_OK || T == 0 || S == 0) return st;
   if (!q || !k_cache || !v_cache || !k_scales || !v_scales || !out || !workspace) return IQP_ERR_INVALID;

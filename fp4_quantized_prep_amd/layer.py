@@ -157,7 +157,7 @@ def attention_fp8_kv(q, cache, block_table, seq_lens, cu_rows, scale: float = No
     them; block_table entries outside [0, n_blocks) hold nothing. A query that
     sees nothing gives zeros; rows behind ``cu_rows[S]`` are left as they were.
     ``out`` must not overlap q.
-    scale: 1 / sqrt(head_dim) by default. workspace: a tensor from
+    scale: 1 / sqrt(head_dim) by default, else 2^-64 to 2^64. workspace: a tensor from
     :func:`attention_fp8_kv_workspace` (allocated here when None); calls that
     share one must not overlap. Returns ``out`` in q's shape.
     """

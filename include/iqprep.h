@@ -743,7 +743,9 @@ int kv_cache_read_fp8(const void* k_cache, const void* v_cache, const uint8_t* k
  *   q, out     bf16 [T, Hq*D], row strides ldq, ldo (elements); 16-byte
  *              aligned, strides multiples of 8; out must not overlap q. Rows
  *              behind cu_rows[S] are left as they were.
- *   Hq         a multiple of Hk (else IQP_ERR_INVALID); scale > 0.
+ *   Hq         a multiple of Hk (else IQP_ERR_INVALID).
+ *   scale      2^-64 to 2^64 (else IQP_ERR_INVALID); times the power of two of a
+ *              key scale it must lie between 2^-100 and 2^126.
  *   workspace  attention_fp8_kv_workspace_bytes(D) bytes of device memory,
  *              256-byte aligned; its contents do not matter before and mean
  *              nothing after. Calls that share one must not overlap.
