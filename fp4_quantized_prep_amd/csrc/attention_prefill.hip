@@ -2,9 +2,9 @@
 // over the FP8 key/value cache: the formula of attention_decode.hip.
 //
 // Bound by the matrix cores and the vector instructions of the softmax
-// together: 4 D operations a visible (row, token) pair on the former, about five
-// instructions on the latter, which take as long at D 128 and twice as long at
-// D 64. A workgroup's four waves take 128 rows (query heads of one key head by
+// together: 4 D operations a visible (row, token) pair on the former, seven to eight
+// instructions on the latter (four to five of them the softmax, the others widening and
+// addresses), which take as long at D 128 and twice as long at D 64. A workgroup's four waves take 128 rows (query heads of one key head by
 // tokens, 32 a wave) and walk the visible tokens in units of 64:
 //   * a unit's codes are loaded once (16 bytes a lane) two units ahead, widened
 //     once (keys to bf16, values to fp16, both exact) and put in LDS beside the
@@ -21,7 +21,7 @@
 //     scores, value exponents go into the probabilities' exponents (see
 //     attention_decode.hip);
 //   * a tile of few rows (a single token beside prompts, the rest of a prompt) is
-//     computed as the decode kernel computes it;
+//     computed as the decode kernel computes it, and so are rows of very large scores;
 //   * 16-byte chunks in LDS are permuted by row, so that the lanes of a cycle
 //     meet distinct banks.
 // Workgroups are numbered with the key head fastest, so that with 8 heads an

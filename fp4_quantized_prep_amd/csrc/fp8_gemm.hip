@@ -511,6 +511,8 @@ hipError_t launch_split(const Fp8GemmArgs& p, hipStream_t stream) {
 // 8192, K 640 .. 7168; us a block for up to 256 workgroups, for up to 512:
 //   64x64 0.32, 0.52;  128x64 0.42, 0.69;  128x128 four stages 0.56, 1.13;
 //   128x128 two stages 0.75, 0.9;  256x256 1.3, 2.6 (an area 16 times the first's)
+// It ranks tiles and is no forecast: 61 us for 4632x8192x1536, which takes 69 to 76,
+// and it has no term for bytes.
 double tile_us(int64_t M, int64_t N, int64_t nkb, int TN, int TM, double fixed, double block, double more, int group) {
   const int64_t tiles = ((M + TM - 1) / TM) * ((N + TN - 1) / TN);
   const int64_t rounds = (tiles + 255) / 256;
@@ -540,7 +542,9 @@ GemmKernel fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int splits) {
   // 32 rows of them a workgroup, by which of the two gives the CUs enough
   // workgroups (32 / 16 rows: 16x7168x8192 13.6 / 15.3, 32x7168x8192 15.6 / 20.0,
   // 64x7168x8192 20.3 / 28.3, 40x8192x1536 6.5 / 8.7; 16x1536x7168 7.2 / 5.6,
-  // 32x2000x7168 8.6 / 7.0, 64x4000x1536 6.2 / 5.5).
+  // 32x2000x7168 8.6 / 7.0, 64x4000x1536 6.2 / 5.5). Above, it would read the weights
+  // once for every 64 tokens (7168x8192, us, tiles / stream kernel by 64 tokens: 65
+  // tokens 22.9 / 27.9, 128 22.7 / 32.3, 256 32.9 / 66.4; 64 in one read 17.0).
   if (M <= 64) {
     const bool wide = N >= 6144;
     if (M <= 16) return wide ? GEMM_STREAM_32x16 : GEMM_STREAM_16x16;

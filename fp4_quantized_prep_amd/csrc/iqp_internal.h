@@ -302,7 +302,12 @@ constexpr int ATTN_WORKGROUPS = 512;
 // A batch of no more rows (tokens times query heads of a key head) than this on
 // average is the decode kernel's, but see below (32 sequences of 6000 tokens, 64 heads over 8, us,
 // decode / prompt kernel: 64 rows 185 / 207, 128 rows 326 / 207). Of another one,
-// sequences of more rows are the prompt kernel's.
+// sequences of more rows are the prompt kernel's. These sides are of sequences alike:
+// the host knows the average alone, so that a prompt's chunk beside many single tokens
+// over long tables may be the decode kernel's too, which reads the cache for every 16
+// rows of it (64 heads over 8, us together / single tokens alone / chunk alone: 448 new
+// tokens beside 63 single ones, 8192 held, 678 / 207 / 167; 512 beside 128, 887 / 400 /
+// 166; 1000 beside 64, where the average is above and both kernels run, 534 / 205 / 331).
 constexpr int ATTN_DECODE_ROWS = 64;
 // Where a row sees no more tokens than this, batches of few rows are the prompt
 // kernel's too: a workgroup a sequence and head, no second launch (single tokens, us,

@@ -128,7 +128,8 @@ def kv_cache_read_fp8(cache, block_table, seq_lens, cu_rows, rows: int, k_out=No
     """Reads keys and values back as bf16: row ``cu_rows[s] + i`` of ``rows`` is
     position ``seq_lens[s] - (cu_rows[s+1] - cu_rows[s]) + i`` of sequence s
     (whole sequences: cu_rows the running sum of seq_lens). Rows that no held
-    token belongs to are left as they were. Returns ``(k, v)``, [rows,
+    token belongs to are left as they were in ``k_out`` and ``v_out``; in tensors
+    allocated here they hold no particular values. Returns ``(k, v)``, [rows,
     n_kv_heads, head_dim].
     """
     args = (*cache, block_table, seq_lens, cu_rows, rows, k_out, v_out)
@@ -155,8 +156,9 @@ def attention_fp8_kv(q, cache, block_table, seq_lens, cu_rows, scale: float = No
     them, all of which the cache holds (append first). A query at position p
     sees the positions up to p, with ``window`` > 0 only the last ``window`` of
     them; block_table entries outside [0, n_blocks) hold nothing. A query that
-    sees nothing gives zeros; rows behind ``cu_rows[S]`` are left as they were.
-    ``out`` must not overlap q.
+    sees nothing gives zeros. Rows that belong to no sequence (before ``cu_rows[0]``,
+    behind ``cu_rows[S]``) are left as they were in ``out``; in a tensor allocated
+    here they hold no particular values. ``out`` must not overlap q.
     scale: 1 / sqrt(head_dim) by default, else 2^-64 to 2^64. workspace: a tensor from
     :func:`attention_fp8_kv_workspace` (allocated here when None); calls that
     share one must not overlap. Returns ``out`` in q's shape.

@@ -742,7 +742,13 @@ int kv_cache_read_fp8(const void* k_cache, const void* v_cache, const uint8_t* k
  *
  *   q, out     bf16 [T, Hq*D], row strides ldq, ldo (elements); 16-byte
  *              aligned, strides multiples of 8; out must not overlap q. Rows
- *              behind cu_rows[S] are left as they were.
+ *              behind cu_rows[S] are left as they were. A row of q that holds a NaN
+ *              or an infinity makes no other row's output NaN.
+ *   k_cache, v_cache   held tokens' codes other than NaN (kv_cache_append_fp8 writes
+ *              none for finite values): a NaN among the values of a token reaches
+ *              rows computed beside those that see it, also ones before it. What
+ *              lies in blocks that are not held, behind a sequence and before every
+ *              window does not matter.
  *   Hq         a multiple of Hk (else IQP_ERR_INVALID).
  *   scale      2^-64 to 2^64 (else IQP_ERR_INVALID); times the power of two of a
  *              key scale it must lie between 2^-100 and 2^126.
@@ -750,8 +756,9 @@ int kv_cache_read_fp8(const void* k_cache, const void* v_cache, const uint8_t* k
  *              256-byte aligned; its contents do not matter before and mean
  *              nothing after. Calls that share one must not overlap.
  * The same call gives the same bits. The order of its sums depends on T, S, Hq,
- * Hk, D, the table's width and the window, so a row's last bit may differ
- * between batches.
+ * Hk, D, the table's width and the window, and a row's weights are rounded relative
+ * to a maximum that rows computed beside it share in raising, so a row's last bit
+ * may differ between batches.
  */
 int64_t attention_fp8_kv_workspace_bytes(int32_t D);
 int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
