@@ -257,7 +257,8 @@ __device__ __forceinline__ void gemm_tile(const Fp8GemmArgs& p, uint8_t* lds) {
   }
 
   if constexpr (SPLIT) {
-    // the sums, in the accumulators' order, for fp8_gemm_join_kernel
+    // the sums, in the accumulators' order, for fp8_gemm_join_kernel (copies past the
+    // last block may be on their way to LDS: a wave's end waits for them)
     float* const to = p.sums + (tile * p.splits + z) * (TN * TM) + wave * (AN * AM * 1024) + 4 * lane;
 #pragma unroll
     for (int t = 0; t < AN; ++t)
