@@ -130,6 +130,20 @@ def _load():
         getattr(lib, name).restype = ctypes.c_int
     lib.attention_fp8_kv_workspace_bytes.argtypes = [c_i32]
     lib.attention_fp8_kv_workspace_bytes.restype = c_i64
+    lib.moe_route.argtypes = [c_p, c_i64, c_i32, c_p, c_i64, c_i32, c_i32, c_i32, c_i32, c_f32, c_p, c_p, c_p]
+    lib.group_rows.argtypes = [c_p, c_i64, c_i32, c_p, c_p, c_p, c_p, c_i64, c_p]
+    grouped_args = [c_p, c_i64, c_p, c_i64, c_i64, c_i64, c_p, c_i64, c_i64, c_p, c_i64, c_i64, c_p, c_p, c_i64, c_i32, c_i32,
+                    c_i64, c_i64]
+    lib.fp8_grouped_gemm_1x128_128x128.argtypes = grouped_args + [c_p, c_i64, c_p]
+    lib.fp8_grouped_swiglu_1x128.argtypes = grouped_args + [c_p, c_i64, c_p, c_i64, c_i64, c_p]
+    lib.moe_combine.argtypes = [c_p, c_i64, c_i64, c_p, c_p, c_i64, c_i32, c_i64, c_p, c_i64, c_p, c_i64, c_p]
+    lib.lora_add.argtypes = [c_p, c_i64, c_i64, c_i64, c_p, c_p, c_p, c_i32, c_p, c_p, c_i32, c_i64, c_p, c_i64, c_p, c_i64, c_p]
+    for name in ("moe_route", "group_rows", "fp8_grouped_gemm_1x128_128x128", "fp8_grouped_swiglu_1x128", "moe_combine", "lora_add"):
+        getattr(lib, name).restype = ctypes.c_int
+    lib.group_rows_workspace_bytes.argtypes = [c_i64, c_i32]
+    lib.group_rows_workspace_bytes.restype = c_i64
+    lib.lora_add_workspace_bytes.argtypes = [c_i64, c_i32, c_i32, c_i64]
+    lib.lora_add_workspace_bytes.restype = c_i64
     return lib
 
 

@@ -724,3 +724,224 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
 }
 
 }  // extern "C"
+
+namespace {
+
+// Checks of the grouped products, shared by both; fills p. R == 0 or N == 0 leaves
+// nothing to do (p.groups.R is then 0).
+int check_grouped(const void* a, int64_t lda, const int32_t* a_scales, int64_t sm, int64_t sw, int64_t M, const void* w,
+                  int64_t ldwg, int64_t ldw, const uint8_t* w_scales, int64_t ld_wsg, int64_t ld_ws,
+                  const int32_t* offsets, const int32_t* rows, int64_t R, int32_t G, int32_t top_k, int64_t N, int64_t K,
+                  iqp::Fp8GroupedArgs& p) {
+  if (M < 0 || R < 0 || G < 0 || top_k < 0 || N < 0 || K < 0) return IQP_ERR_INVALID;
+  if (R == 0 || N == 0) return IQP_OK;
+  if (!a || !a_scales || !w || !w_scales || !offsets || (top_k && !rows)) return IQP_ERR_INVALID;
+  if (G == 0 || K == 0 || lda < K || ldw < K) return IQP_ERR_INVALID;
+  if (M > R || (top_k ? R % top_k || M != R / top_k : M != R)) return IQP_ERR_INVALID;
+  if (K % 128) return IQP_ERR_UNSUPPORTED;
+  const int64_t kb = K / 128, nw = (kb + 3) / 4;
+  if (check_scale_strides(M, nw, sm, sw) != IQP_OK || ld_ws < kb) return IQP_ERR_INVALID;
+  if (!aligned(a, 16) || lda % 16 || !aligned(w, 16) || ldw % 16 || ldwg % 16 || !aligned(a_scales, 4) ||
+      !aligned(offsets, 4) || !aligned(rows, 4))
+    return IQP_ERR_UNSUPPORTED;
+  if (G > iqp::MAX_GROUPS || R > 0x7FFFFFFF || N > 0x7FFFFFFF || kb > 256) return IQP_ERR_UNSUPPORTED;
+  // 256 weight rows are addressed with 32-bit offsets, and so is all of a
+  constexpr int64_t REACH = (int64_t)1 << 31;
+  if (ldw > ((int64_t)1 << 22) || lda >= REACH || sm >= REACH || sw >= REACH) return IQP_ERR_UNSUPPORTED;
+  if ((M - 1) * lda + K >= REACH || 4 * ((M - 1) * sm + (nw - 1) * sw + 1) >= REACH) return IQP_ERR_UNSUPPORTED;
+  // groups may share weights (a stride of 0), and lie apart by less than 2^62 bytes in all
+  const int64_t far = (int64_t)1 << 52;
+  if (ldwg < 0 || ld_wsg < 0) return IQP_ERR_INVALID;
+  if (ldwg > far || ld_wsg > far || ld_ws > ((int64_t)1 << 31)) return IQP_ERR_UNSUPPORTED;
+  p.groups = {offsets, rows, R, G};
+  p.a = static_cast<const uint8_t*>(a);
+  p.lda = lda;
+  p.a_scales = a_scales;
+  p.as_sm = sm;
+  p.as_sw = sw;
+  p.M = M;
+  p.top = top_k;
+  p.w = static_cast<const uint8_t*>(w);
+  p.ldwg = ldwg;
+  p.ldw = ldw;
+  p.w_scales = w_scales;
+  p.ld_wsg = ld_wsg;
+  p.ld_ws = ld_ws;
+  p.N = N;
+  p.nkb = (int32_t)kb;
+  return IQP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_route(const void* logits, int64_t ld, int32_t logits_bf16, const float* bias, int64_t M, int32_t E, int32_t top_k,
+              int32_t scoring, int32_t renormalize, float scale, float* weights, int32_t* experts, void* stream) {
+  if (M < 0 || E < 0 || top_k < 0 || scoring < IQP_SCORE_SOFTMAX || scoring > IQP_SCORE_SQRT_SOFTPLUS) return IQP_ERR_INVALID;
+  if (M == 0) return IQP_OK;
+  if (!logits || !weights || !experts) return IQP_ERR_INVALID;
+  if (E == 0 || top_k == 0 || top_k > E || ld < E) return IQP_ERR_INVALID;
+  if (E > iqp::MAX_GROUPS || top_k > 64) return IQP_ERR_UNSUPPORTED;
+  if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(experts, 4))
+    return IQP_ERR_UNSUPPORTED;
+  if (M > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  const int st = device_status();
+  if (st != IQP_OK) return st;
+  iqp::MoeRouteArgs p{};
+  p.logits = logits;
+  p.ld = ld;
+  p.half = logits_bf16 != 0;
+  p.bias = bias;
+  p.M = M;
+  p.E = E;
+  p.top = top_k;
+  p.scoring = scoring;
+  p.renormalize = renormalize != 0;
+  p.scale = scale;
+  p.weights = weights;
+  p.experts = experts;
+  return from_hip(iqp::launch_moe_route(p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t group_rows_workspace_bytes(int64_t R, int32_t G) {
+  if (R <= 0 || R > 0x7FFFFFFF || G <= 0 || G > iqp::MAX_GROUPS) return 0;
+  const int64_t chunk = iqp::group_rows_chunk(R), chunks = (R + chunk - 1) / chunk;
+  return chunks > 1 ? chunks * G * 4 : 0;
+}
+
+int group_rows(const int32_t* index, int64_t R, int32_t G, int32_t* offsets, int32_t* rows, int32_t* slots, void* workspace,
+               int64_t workspace_bytes, void* stream) {
+  if (R < 0 || G < 0 || workspace_bytes < 0) return IQP_ERR_INVALID;
+  if (G == 0 || !offsets || (R > 0 && (!index || !rows || !slots))) return IQP_ERR_INVALID;
+  if (G > iqp::MAX_GROUPS || R > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  const int64_t need = group_rows_workspace_bytes(R, G);
+  if (need && (!workspace || workspace_bytes < need)) return IQP_ERR_INVALID;
+  if (!aligned(index, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4) || (need && !aligned(workspace, 4)))
+    return IQP_ERR_UNSUPPORTED;
+  const int st = device_status();
+  if (st != IQP_OK) return st;
+  iqp::GroupRowsArgs p{};
+  p.index = index;
+  p.R = R;
+  p.G = G;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.slots = slots;
+  p.counts = static_cast<int32_t*>(workspace);
+  return from_hip(iqp::launch_group_rows(p, static_cast<hipStream_t>(stream)));
+}
+
+int fp8_grouped_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m,
+                                   int64_t as_stride_w, int64_t M, const void* w, int64_t ldwg, int64_t ldw,
+                                   const uint8_t* w_scales, int64_t ld_wsg, int64_t ld_ws, const int32_t* offsets,
+                                   const int32_t* rows, int64_t R, int32_t G, int32_t top_k, int64_t N, int64_t K, void* out,
+                                   int64_t ldo, void* stream) {
+  iqp::Fp8GroupedArgs p{};
+  int st = check_grouped(a, lda, a_scales, as_stride_m, as_stride_w, M, w, ldwg, ldw, w_scales, ld_wsg, ld_ws, offsets, rows,
+                         R, G, top_k, N, K, p);
+  if (st != IQP_OK || R == 0 || N == 0) return st;
+  if (!out || ldo < N) return IQP_ERR_INVALID;
+  if (!aligned(out, 2)) return IQP_ERR_UNSUPPORTED;
+  st = device_status();
+  if (st != IQP_OK) return st;
+  p.out = static_cast<uint16_t*>(out);
+  p.ldo = ldo;
+  p.wide_out = aligned(out, 16) && ldo % 8 == 0;
+  return from_hip(iqp::launch_fp8_grouped(p, static_cast<hipStream_t>(stream)));
+}
+
+int fp8_grouped_swiglu_1x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m, int64_t as_stride_w,
+                             int64_t M, const void* w, int64_t ldwg, int64_t ldw, const uint8_t* w_scales, int64_t ld_wsg,
+                             int64_t ld_ws, const int32_t* offsets, const int32_t* rows, int64_t R, int32_t G, int32_t top_k,
+                             int64_t I, int64_t K, void* q, int64_t ldq, int32_t* q_scales, int64_t qs_stride_m,
+                             int64_t qs_stride_w, void* stream) {
+  if (I < 0) return IQP_ERR_INVALID;
+  if (I > 0x3FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  iqp::Fp8GroupedArgs p{};
+  int st = check_grouped(a, lda, a_scales, as_stride_m, as_stride_w, M, w, ldwg, ldw, w_scales, ld_wsg, ld_ws, offsets, rows,
+                         R, G, top_k, 2 * I, K, p);
+  if (st != IQP_OK || R == 0 || I == 0) return st;
+  if (!q || !q_scales || ldq < I) return IQP_ERR_INVALID;
+  if (I % 128) return IQP_ERR_UNSUPPORTED;
+  if (check_scale_strides(R, (I / 128 + 3) / 4, qs_stride_m, qs_stride_w) != IQP_OK) return IQP_ERR_INVALID;
+  if (!aligned(q, 16) || ldq % 16 || !aligned(q_scales, 4)) return IQP_ERR_UNSUPPORTED;
+  st = device_status();
+  if (st != IQP_OK) return st;
+  p.q = static_cast<uint8_t*>(q);
+  p.ldq = ldq;
+  p.q_scales = q_scales;
+  p.qs_sm = qs_stride_m;
+  p.qs_sw = qs_stride_w;
+  return from_hip(iqp::launch_fp8_grouped(p, static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, const float* weights, int64_t M, int32_t top_k,
+                int64_t d, const void* shared, int64_t ld_shared, void* out, int64_t ldo, void* stream) {
+  if (R < 0 || M < 0 || top_k < 0 || d < 0) return IQP_ERR_INVALID;
+  if (M == 0 || d == 0) return IQP_OK;
+  if ((!y && R > 0) || !slots || !weights || !out || top_k == 0) return IQP_ERR_INVALID;
+  if (ldy < d || ldo < d || (shared && ld_shared < d)) return IQP_ERR_INVALID;
+  if (d % 8 || !aligned(y, 16) || ldy % 8 || !aligned(out, 16) || ldo % 8 || !aligned(slots, 4) || !aligned(weights, 4) ||
+      (shared && (!aligned(shared, 16) || ld_shared % 8)))
+    return IQP_ERR_UNSUPPORTED;
+  if (R > 0x7FFFFFFF || M > 0x7FFFFFFF || d > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  const int st = device_status();
+  if (st != IQP_OK) return st;
+  iqp::MoeCombineArgs p{};
+  p.y = static_cast<const uint16_t*>(y);
+  p.ldy = ldy;
+  p.R = R;
+  p.slots = slots;
+  p.weights = weights;
+  p.top = top_k;
+  p.shared = static_cast<const uint16_t*>(shared);
+  p.lds = ld_shared;
+  p.M = M;
+  p.d = d;
+  p.out = static_cast<uint16_t*>(out);
+  p.ldo = ldo;
+  return from_hip(iqp::launch_moe_combine(p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t lora_add_workspace_bytes(int64_t M, int32_t G, int32_t rank, int64_t K) {
+  if (M <= 0 || M > 0x7FFFFFFF || G <= 0 || G > iqp::MAX_GROUPS || rank < 8 || rank > 128 || K <= 0) return 0;
+  return iqp::lora_splits(M, G, K) * M * iqp::lora_pitch(rank) * 4;
+}
+
+int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, const void* b, const float* scales, int32_t rank,
+             const int32_t* offsets, const int32_t* rows, int32_t G, int64_t N, void* out, int64_t ldo, void* workspace,
+             int64_t workspace_bytes, void* stream) {
+  if (M < 0 || K < 0 || rank < 0 || G < 0 || N < 0 || workspace_bytes < 0) return IQP_ERR_INVALID;
+  if (M == 0 || N == 0 || G == 0) return IQP_OK;
+  if (!x || !a || !b || !offsets || !rows || !out || !workspace) return IQP_ERR_INVALID;
+  if (K == 0 || rank == 0 || ldx < K || ldo < N) return IQP_ERR_INVALID;
+  if (rank % 8 || rank > 128 || K % 8) return IQP_ERR_UNSUPPORTED;
+  if (!aligned(x, 16) || ldx % 8 || !aligned(a, 16) || !aligned(b, 16) || !aligned(scales, 4) || !aligned(offsets, 4) ||
+      !aligned(rows, 4) || !aligned(out, 2))
+    return IQP_ERR_UNSUPPORTED;
+  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || K > 0x7FFFFFFF || G > iqp::MAX_GROUPS) return IQP_ERR_UNSUPPORTED;
+  if (workspace_bytes < lora_add_workspace_bytes(M, G, rank, K)) return IQP_ERR_INVALID;
+  if (!aligned(workspace, 256)) return IQP_ERR_UNSUPPORTED;
+  const int st = device_status();
+  if (st != IQP_OK) return st;
+  iqp::LoraArgs p{};
+  p.groups = {offsets, rows, M, G};
+  p.x = static_cast<const uint16_t*>(x);
+  p.ldx = ldx;
+  p.M = M;
+  p.K = K;
+  p.a = static_cast<const uint16_t*>(a);
+  p.b = static_cast<const uint16_t*>(b);
+  p.scales = scales;
+  p.rank = rank;
+  p.out = static_cast<uint16_t*>(out);
+  p.ldo = ldo;
+  p.N = N;
+  p.wide_out = aligned(out, 16) && ldo % 8 == 0;
+  p.h = static_cast<float*>(workspace);
+  p.splits = iqp::lora_splits(M, G, K);
+  return from_hip(iqp::launch_lora_add(p, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -16,6 +16,7 @@
 #include <optional>
 #include <string>
 #include <tuple>
+#include <utility>
 
 #include "iqprep.h"
 
@@ -259,6 +260,224 @@ Tensor attention(const Tensor& q, const Tensor& kc, const Tensor& vc, const Tens
   return out;
 }
 
+// A tensor that has to be contiguous, of these sizes
+const Tensor& exact(const Tensor& t, const char* name, at::ScalarType dtype, c10::Device dev, at::IntArrayRef sizes) {
+  require(t, name, dtype, dev, (int64_t)sizes.size());
+  if (t.sizes() != sizes) {
+    std::string want = "(";
+    for (size_t i = 0; i < sizes.size(); ++i) want += (i ? ", " : "") + str(sizes[i]);
+    value_error(std::string(name) + " must be of shape " + want + "), got " + shape_of(t));
+  }
+  if (!t.is_contiguous()) value_error(std::string(name) + " must be contiguous");
+  return t;
+}
+
+std::tuple<Tensor, Tensor> route(const Tensor& logits, int64_t top_k, const OptTensor& bias, int64_t scoring, bool renormalize,
+                                 double scale, const OptTensor& weights_, const OptTensor& experts_) {
+  const c10::Device dev = gpu_of(logits, "logits");
+  const bool half = logits.scalar_type() == at::kBFloat16;
+  require(logits, "logits", half ? at::kBFloat16 : at::kFloat, dev, 2);
+  const int64_t M = logits.size(0), E = logits.size(1);
+  if (top_k < 1 || top_k > E) value_error("top_k must be 1 to " + str(E) + ", got " + str(top_k));
+  if (E > 0x7FFFFFFF) value_error("logits has too many columns");
+  if (M && E > 1 && logits.stride(1) != 1) value_error("logits needs contiguous rows");
+  if (bias) exact(*bias, "bias", at::kFloat, dev, {E});
+  Tensor weights = weights_ ? *weights_ : empty({M, top_k}, at::kFloat, dev);
+  Tensor experts = experts_ ? *experts_ : empty({M, top_k}, at::kInt, dev);
+  exact(weights, "weights", at::kFloat, dev, {M, top_k});
+  exact(experts, "experts", at::kInt, dev, {M, top_k});
+  run(moe_route, "moe_route", dev, logits.const_data_ptr(), M > 1 ? logits.stride(0) : E, (int32_t)half,
+      bias ? (const float*)bias->const_data_ptr() : nullptr, M, (int32_t)E, (int32_t)top_k, (int32_t)scoring, (int32_t)renormalize,
+      (float)scale, (float*)weights.mutable_data_ptr(), (int32_t*)experts.mutable_data_ptr());
+  return {weights, experts};
+}
+
+std::tuple<Tensor, Tensor, Tensor> group(const Tensor& index, int64_t G, const OptTensor& offsets_, const OptTensor& rows_,
+                                         const OptTensor& slots_, const OptTensor& workspace_) {
+  const c10::Device dev = gpu_of(index, "index");
+  if (index.dim() != 1 && index.dim() != 2) value_error("index must be [M] or [M, k], got shape " + shape_of(index));
+  exact(index, "index", at::kInt, dev, index.sizes());
+  if (G < 1 || G > 1024) value_error("n_groups must be 1 to 1024, got " + str(G));
+  const int64_t R = index.numel();
+  Tensor offsets = offsets_ ? *offsets_ : empty({G + 1}, at::kInt, dev);
+  Tensor rows = rows_ ? *rows_ : empty({R}, at::kInt, dev);
+  Tensor slots = slots_ ? *slots_ : empty(index.sizes(), at::kInt, dev);
+  exact(offsets, "offsets", at::kInt, dev, {G + 1});
+  exact(rows, "rows", at::kInt, dev, {R});
+  exact(slots, "slots", at::kInt, dev, index.sizes());
+  const int64_t need = group_rows_workspace_bytes(R, (int32_t)G);
+  Tensor ws;
+  if (workspace_) {
+    ws = *workspace_;
+    require(ws, "workspace", at::kByte, dev, 1);
+    if (!ws.is_contiguous()) value_error("workspace must be contiguous");
+  } else if (need) {
+    ws = empty({need}, at::kByte, dev);
+  }
+  run(group_rows, "group_rows", dev, (const int32_t*)index.const_data_ptr(), R, (int32_t)G, (int32_t*)offsets.mutable_data_ptr(),
+      (int32_t*)rows.mutable_data_ptr(), (int32_t*)slots.mutable_data_ptr(), ws.defined() ? ws.mutable_data_ptr() : nullptr,
+      ws.defined() ? (int64_t)ws.numel() : (int64_t)0);
+  return {offsets, rows, slots};
+}
+
+// What group_rows gave, as its readers need it
+struct Groups {
+  const int32_t *offsets, *rows;
+  int64_t R, top;      // places; entries of a token
+  int32_t G;
+};
+
+Groups groups_of(const Tensor& offsets, const Tensor& rows, const Tensor& slots, c10::Device dev) {
+  require(offsets, "groups.offsets", at::kInt, dev, 1);
+  require(rows, "groups.rows", at::kInt, dev, 1);
+  if (!slots.defined()) throw py::type_error("groups.slots must be a torch.Tensor");
+  if (slots.dim() != 1 && slots.dim() != 2) value_error("groups.slots must be [M] or [M, k], got shape " + shape_of(slots));
+  require(slots, "groups.slots", at::kInt, dev, slots.dim());
+  if (!offsets.is_contiguous() || !rows.is_contiguous() || !slots.is_contiguous()) value_error("the groups' tensors must be contiguous");
+  const int64_t G = offsets.size(0) - 1, R = rows.size(0);
+  if (G < 1 || G > 1024) value_error("groups.offsets must hold 2 to 1025 entries, got " + str(G + 1));
+  if (slots.numel() != R) value_error("groups.rows and groups.slots must hold as many entries, got " + str(R) + " and " + str(slots.numel()));
+  return {(const int32_t*)offsets.const_data_ptr(), (const int32_t*)rows.const_data_ptr(), R, slots.dim() == 2 ? slots.size(1) : 1, (int32_t)G};
+}
+
+// Scale words [rows, words]: their strides as the C calls take them
+std::pair<int64_t, int64_t> word_strides(const Tensor& t) {
+  const int64_t M = t.size(0), nw = t.size(1);
+  int64_t sm = t.stride(0), sw = t.stride(1);
+  if (M == 1) sm = sw == 1 ? nw : 1;
+  if (nw == 1) {
+    if (sm == 1) sw = M;
+    else sw = 1;
+  }
+  return {sm, sw};
+}
+
+// The operands that both grouped products take
+struct Grouped {
+  c10::Device dev;
+  Groups g;
+  int64_t M, K, N, lda, sm, sw, ldwg, ldw, ld_wsg, ld_ws;
+  int32_t top;
+};
+
+Grouped grouped_of(const Tensor& a, const Tensor& a_scales, const Tensor& w, const Tensor& w_scales, const Tensor& offsets,
+                   const Tensor& rows, const Tensor& slots, bool gather) {
+  const c10::Device dev = gpu_of(a, "a");
+  require_codes(a, "a", dev, 2);
+  require(a_scales, "a_scales", at::kInt, dev, 2);
+  require_codes(w, "w", dev, 3);
+  require(w_scales, "w_scales", at::kByte, dev, 3);
+  const Groups g = groups_of(offsets, rows, slots, dev);
+  const int64_t M = a.size(0), K = a.size(1), N = w.size(1), kb = K / 128, nw = (kb + 3) / 4;
+  const int64_t want = gather ? (g.top ? g.R / g.top : 0) : g.R;
+  if (M != want)
+    value_error(std::string("a must have ") + str(want) + (gather ? " rows, one a token" : " rows, one a place") + ", got " + str(M));
+  if (w.size(0) != g.G || w.size(2) != K) value_error("w must be [" + str(g.G) + ", N, " + str(K) + "], got " + shape_of(w));
+  if (a_scales.size(0) != M || a_scales.size(1) != nw)
+    value_error("a_scales must be [" + str(M) + ", " + str(nw) + "] (one packed word per 512 columns), got " + shape_of(a_scales));
+  if (w_scales.size(0) != g.G || w_scales.size(1) != (N + 127) / 128 || w_scales.size(2) != kb)
+    value_error("w_scales must be [" + str(g.G) + ", " + str((N + 127) / 128) + ", " + str(kb) + "], got " + shape_of(w_scales));
+  if (M && N && (a.stride(1) != 1 || w.stride(2) != 1 || (kb > 1 && w_scales.stride(2) != 1)))
+    value_error("a, w and w_scales need contiguous rows");
+  const auto [sm, sw] = word_strides(a_scales);
+  // the stride of a single row or group means nothing: torch gives any
+  const int64_t ldw = N > 1 ? w.stride(1) : K, ld_ws = w_scales.size(1) > 1 ? w_scales.stride(1) : kb;
+  return {dev, g, M, K, N, M > 1 ? a.stride(0) : K, sm, sw, g.G > 1 ? w.stride(0) : N * ldw, ldw,
+          g.G > 1 ? w_scales.stride(0) : w_scales.size(1) * ld_ws, ld_ws, gather ? (int32_t)g.top : 0};
+}
+
+Tensor grouped_gemm(const Tensor& a, const Tensor& a_scales, const Tensor& w, const Tensor& w_scales, const Tensor& offsets,
+                    const Tensor& rows, const Tensor& slots, bool gather, const OptTensor& out_) {
+  const Grouped p = grouped_of(a, a_scales, w, w_scales, offsets, rows, slots, gather);
+  const int64_t R = p.g.R;
+  Tensor out = out_ ? *out_ : empty({R, p.N}, at::kBFloat16, p.dev);
+  require(out, "out", at::kBFloat16, p.dev, 2);
+  if (out.size(0) != R || out.size(1) != p.N) value_error("out must be [" + str(R) + ", " + str(p.N) + "], got " + shape_of(out));
+  if (R && p.N > 1 && out.stride(1) != 1) value_error("out needs contiguous rows");
+  run(fp8_grouped_gemm_1x128_128x128, "fp8_grouped_gemm_1x128_128x128", p.dev, a.const_data_ptr(), p.lda,
+      (const int32_t*)a_scales.const_data_ptr(), p.sm, p.sw, p.M, w.const_data_ptr(), p.ldwg, p.ldw,
+      (const uint8_t*)w_scales.const_data_ptr(), p.ld_wsg, p.ld_ws, p.g.offsets, p.g.rows, R, p.g.G, p.top, p.N, p.K,
+      out.mutable_data_ptr(), R > 1 ? out.stride(0) : (p.N + 7) / 8 * 8);
+  return out;
+}
+
+std::tuple<Tensor, Tensor> grouped_swiglu(const Tensor& a, const Tensor& a_scales, const Tensor& w, const Tensor& w_scales,
+                                          const Tensor& offsets, const Tensor& rows, const Tensor& slots, bool gather,
+                                          const OptTensor& q_, const OptTensor& q_scales_) {
+  const Grouped p = grouped_of(a, a_scales, w, w_scales, offsets, rows, slots, gather);
+  if (p.N % 2) value_error("w must have gate rows and as many up rows, got " + str(p.N));
+  const int64_t R = p.g.R, I = p.N / 2, nw = (I / 128 + 3) / 4;
+  Tensor q = q_ ? *q_ : empty({R, I}, at::kByte, p.dev);
+  Tensor words = q_scales_ ? *q_scales_ : empty({R, nw}, at::kInt, p.dev);
+  require_codes(q, "q", p.dev, 2);
+  require(words, "q_scales", at::kInt, p.dev, 2);
+  if (q.size(0) != R || q.size(1) != I) value_error("q must be [" + str(R) + ", " + str(I) + "], got " + shape_of(q));
+  if (words.size(0) != R || words.size(1) != nw) value_error("q_scales must be [" + str(R) + ", " + str(nw) + "], got " + shape_of(words));
+  if (R && I > 1 && q.stride(1) != 1) value_error("q needs contiguous rows");
+  const auto [sm, sw] = word_strides(words);
+  run(fp8_grouped_swiglu_1x128, "fp8_grouped_swiglu_1x128", p.dev, a.const_data_ptr(), p.lda,
+      (const int32_t*)a_scales.const_data_ptr(), p.sm, p.sw, p.M, w.const_data_ptr(), p.ldwg, p.ldw,
+      (const uint8_t*)w_scales.const_data_ptr(), p.ld_wsg, p.ld_ws, p.g.offsets, p.g.rows, R, p.g.G, p.top, I, p.K,
+      q.mutable_data_ptr(), R > 1 ? q.stride(0) : I, (int32_t*)words.mutable_data_ptr(), sm, sw);
+  return {q, words};
+}
+
+// bf16 [rows, cols] with contiguous rows; its row stride
+int64_t matrix(const Tensor& t, const char* name, c10::Device dev, int64_t rows, int64_t cols) {
+  require(t, name, at::kBFloat16, dev, 2);
+  if (t.size(0) != rows || t.size(1) != cols)
+    value_error(std::string(name) + " must be [" + str(rows) + ", " + str(cols) + "], got " + shape_of(t));
+  if (rows && cols > 1 && t.stride(1) != 1) value_error(std::string(name) + " needs contiguous rows");
+  return rows > 1 ? t.stride(0) : (cols + 7) / 8 * 8;
+}
+
+Tensor combine(const Tensor& y, const Tensor& offsets, const Tensor& rows, const Tensor& slots, const Tensor& weights,
+               const OptTensor& shared, const OptTensor& out_) {
+  const c10::Device dev = gpu_of(y, "y");
+  const Groups g = groups_of(offsets, rows, slots, dev);
+  require(y, "y", at::kBFloat16, dev, 2);
+  const int64_t R = g.R, d = y.size(1), M = slots.size(0), top = g.top;
+  const int64_t ldy = matrix(y, "y", dev, R, d);
+  require(weights, "weights", at::kFloat, dev, slots.dim());
+  exact(weights, "weights", at::kFloat, dev, slots.sizes());
+  const int64_t lds = shared ? matrix(*shared, "shared", dev, M, d) : 0;
+  Tensor out = out_ ? *out_ : empty({M, d}, at::kBFloat16, dev);
+  const int64_t ldo = matrix(out, "out", dev, M, d);
+  run(moe_combine, "moe_combine", dev, y.const_data_ptr(), ldy, R, (const int32_t*)slots.const_data_ptr(),
+      (const float*)weights.const_data_ptr(), M, (int32_t)top, d, shared ? shared->const_data_ptr() : nullptr, lds,
+      out.mutable_data_ptr(), ldo);
+  return out;
+}
+
+Tensor lora(const Tensor& out, const Tensor& x, const Tensor& a, const Tensor& b, const Tensor& offsets, const Tensor& rows,
+            const Tensor& slots, const OptTensor& scales, const OptTensor& workspace_) {
+  const c10::Device dev = gpu_of(x, "x");
+  const Groups g = groups_of(offsets, rows, slots, dev);
+  require(x, "x", at::kBFloat16, dev, 2);
+  require(out, "out", at::kBFloat16, dev, 2);
+  const int64_t M = x.size(0), K = x.size(1), N = out.size(1);
+  if (g.top != 1 || g.R != M) value_error("the groups must hold one adapter for each of the " + str(M) + " tokens");
+  require(a, "lora_a", at::kBFloat16, dev, 3);
+  const int64_t rank = a.size(1);
+  exact(a, "lora_a", at::kBFloat16, dev, {g.G, rank, K});
+  exact(b, "lora_b", at::kBFloat16, dev, {g.G, N, rank});
+  if (scales) exact(*scales, "scales", at::kFloat, dev, {g.G});
+  const int64_t ldx = matrix(x, "x", dev, M, K), ldo = matrix(out, "out", dev, M, N);
+  if (rank > 0x7FFFFFFF) value_error("lora_a has too many rows");
+  Tensor ws;
+  if (workspace_) {
+    ws = *workspace_;
+    require(ws, "workspace", at::kByte, dev, 1);
+    if (!ws.is_contiguous()) value_error("workspace must be contiguous");
+  } else if (const int64_t need = lora_add_workspace_bytes(M, g.G, (int32_t)rank, K)) {
+    ws = empty({need}, at::kByte, dev);
+  }
+  run(lora_add, "lora_add", dev, x.const_data_ptr(), ldx, M, K, a.const_data_ptr(), b.const_data_ptr(),
+      scales ? (const float*)scales->const_data_ptr() : nullptr, (int32_t)rank, g.offsets, g.rows, g.G, N, (void*)out.mutable_data_ptr(), ldo,
+      ws.defined() ? ws.mutable_data_ptr() : nullptr, ws.defined() ? (int64_t)ws.numel() : (int64_t)0);
+  return out;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_binding, m) {
@@ -271,4 +490,10 @@ PYBIND11_MODULE(_binding, m) {
   m.def("kv_append", &kv_append);
   m.def("kv_read", &kv_read);
   m.def("attention", &attention);
+  m.def("route", &route);
+  m.def("group", &group);
+  m.def("grouped_gemm", &grouped_gemm);
+  m.def("grouped_swiglu", &grouped_swiglu);
+  m.def("combine", &combine);
+  m.def("lora", &lora);
 }

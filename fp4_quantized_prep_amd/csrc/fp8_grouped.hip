@@ -1,0 +1,525 @@
+// Block-scaled FP8 products of rows sorted by group, each group with weights of
+// its own (the experts of a mixture). For place i, in group g,
+//   y[i, n] = sum_j 2^(ea(src, j) + ew(g, n / 128, j)) sum_{k in block j} A[src, k] W[g, n, k]
+// with src = i, or the token that place i came from; summed in float32 by the
+// matrix cores, which apply the scales. Then either
+//   out = bf16(y), or, the weights' rows being I gates and I ups,
+//   h[i, c] = y_c / (1 + exp(-y_c)) y_(I + c), quantised in 1x128 blocks as
+//   fp8_quant_1x128_ue8m0 does, from the float32 values.
+#include <type_traits>
+
+#include "iq_common.h"
+#include "layer_common.h"
+#include "row_groups.h"
+
+namespace iqp {
+namespace {
+
+enum Epilogue { TO_BF16, SWIGLU };
+
+constexpr int SLAB = 1024;   // bytes of one wave-wide copy to LDS
+constexpr int TN = 256;      // weight rows of a workgroup (SWIGLU: 128 gates and their 128 ups)
+constexpr int NW = 8;        // its waves
+
+constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
+// An offset beyond every buffer: operands reach less than 2^31 bytes. Joined to
+// others by "or", so that two of them stay one.
+constexpr uint32_t PAST = 0x80000000u;
+
+// row of a that place t.begin + r reads, PAST where there is none
+__device__ __forceinline__ uint32_t source_row(const Fp8GroupedArgs& p, const groups::Tile& t, int r) {
+  if (r >= t.rows) return PAST;
+  int src = t.begin + r;
+  if (p.top) {
+    src = p.groups.rows[src];
+    if (src < 0) return PAST;
+    src = (int)((unsigned)src / (unsigned)p.top);
+  }
+  return src < p.M ? (uint32_t)src : PAST;
+}
+
+// what the bodies read of a group's weights
+struct Weights {
+  rsrc_t rows[2];            // TO_BF16: 256 rows from n0 on, twice; SWIGLU: 128 gates, 128 ups
+  const uint8_t* scales;     // of the group
+  int64_t n0;                // first row (SWIGLU: first channel)
+};
+
+template <Epilogue EPI>
+__device__ __forceinline__ Weights weights_of(const Fp8GroupedArgs& p, const groups::Tile& t) {
+  Weights w;
+  const uint8_t* const base = p.w + t.group * p.ldwg;
+  w.scales = p.w_scales + t.group * p.ld_wsg;
+  w.n0 = (int64_t)t.part * (EPI == SWIGLU ? TN / 2 : TN);
+  if constexpr (EPI == SWIGLU) {
+    const uint64_t bytes = (uint64_t)(TN / 2 - 1) * p.ldw + (uint64_t)KB * p.nkb;
+    w.rows[0] = make_rsrc(base + w.n0 * p.ldw, bytes);
+    w.rows[1] = make_rsrc(base + (p.N / 2 + w.n0) * p.ldw, bytes);
+  } else {
+    const int64_t rows = p.N - w.n0 < TN ? p.N - w.n0 : TN;
+    w.rows[0] = w.rows[1] = make_rsrc(base + w.n0 * p.ldw, (uint64_t)(rows - 1) * p.ldw + (uint64_t)KB * p.nkb);
+  }
+  return w;
+}
+
+// the scale bytes of 128-row tile `tile` of the group's weights, 4 K blocks a lane
+__device__ __forceinline__ uint32_t scale_lanes(const Fp8GroupedArgs& p, const Weights& w, int64_t tile, int lane) {
+  const int64_t last = (p.N + 127) / 128 - 1;
+  const uint8_t* const s = w.scales + (tile < last ? tile : last) * p.ld_ws;
+  uint32_t v = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) v |= (uint32_t)s[4 * lane + b < p.nkb ? 4 * lane + b : 0] << (8 * b);
+  return v;
+}
+
+__device__ __forceinline__ int scale_of(uint32_t lanes, int j) {
+  return (int)((uint32_t)__builtin_amdgcn_readlane((int)lanes, (j >> 2) & 63) >> (8 * (j & 3)));
+}
+
+__device__ __forceinline__ float swiglu(float gate, float up) {
+  return gate / (1.f + __expf(-gate)) * up;
+}
+
+// The exponent of a block from its largest magnitude (float32 bits): the least
+// e >= -22 with 448 2^e >= amax. amax = (1 + f 2^-23) 2^(E - 127), 448 = 1.75 2^8.
+__device__ __forceinline__ int exponent_of(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 135 + ((b & 0x7FFFFF) > 0x600000 ? 1 : 0);
+  return e > -22 ? e : -22;
+}
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float mul) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * mul, b * mul, 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c * mul, d * mul, r, true);
+  return (uint32_t)r;
+}
+
+// scale byte of channels n0 .. n0 + 127 of a place; the last one's word is filled up with zeros
+__device__ __forceinline__ void store_scale(const Fp8GroupedArgs& p, int64_t place, int64_t n0, int e) {
+  const int block = (int)(n0 / 128), blocks = (int)(p.N / 256);
+  uint8_t* const word = reinterpret_cast<uint8_t*>(p.q_scales + place * p.qs_sm + (int64_t)(block >> 2) * p.qs_sw);
+  word[block & 3] = (uint8_t)(e + 127);
+  if (block == blocks - 1)
+    for (int b = (block & 3) + 1; b < 4; ++b) word[b] = 0;
+}
+
+// Tile body: 256 weight rows x up to TM = 64 AM places, eight waves of 64 x 32 AM
+// (4 by 2; the places in tiles of 32 that alternate between the two). K block by
+// K block through NST LDS stages, 8 rows of 128 bytes a copy, the 16-byte chunks
+// of LDS row r permuted by (r / 2) % 8 so that the operand reads meet distinct
+// banks; weight row n of a 32-row tile sits in LDS row 8 ((n / 4) % 4) + 4 (n / 16)
+// + n % 4 of it, so that a lane's sixteen accumulators are sixteen consecutive n
+// of one place. Copies past the last block or row read zeros out of bounds,
+// which keeps the wait counts constant.
+template <int AM, int NST>
+constexpr int tile_bytes() { return NST * (TN * KB + 64 * AM * (KB + 4)); }
+
+template <Epilogue EPI, int AM, int NST>
+__device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups::Tile& t, uint8_t* lds) {
+  constexpr int TM = 64 * AM, AN = 2;
+  constexpr int W_BYTES = TN * KB, A_BYTES = TM * KB, S_BYTES = TM * 4;
+  constexpr int WC = W_BYTES / SLAB / NW, AC = A_BYTES / SLAB / NW, NCOPY = WC + AC + 1;
+  static_assert(WC == 4 && AC == AM, "whole slabs");
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave & 3, wm = wave >> 2;
+  uint8_t* const lw = lds;
+  uint8_t* const la = lw + NST * W_BYTES;
+  uint8_t* const ls = la + NST * A_BYTES;
+  const Weights w = weights_of<EPI>(p, t);
+  const int nkb = p.nkb;
+  const int64_t nw = (nkb + 3) / 4;
+  const rsrc_t ra = make_rsrc(p.a, (uint64_t)(p.M - 1) * p.lda + (uint64_t)KB * nkb);
+  const rsrc_t rs = make_rsrc(p.a_scales, 4 * (uint64_t)((p.M - 1) * p.as_sm + (nw - 1) * p.as_sw + 1));
+
+  // copies: slab i of this wave is LDS rows 8 (wave + NW i) + lane / 8
+  uint32_t vw[WC], va[AC], vs;
+#pragma unroll
+  for (int i = 0; i < WC; ++i) {
+    int r = 8 * (wave + NW * i) + (lane >> 3);
+    const int chunk = 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    if (EPI == SWIGLU) r &= TN / 2 - 1;
+    const int n = (r & ~31) + 4 * ((r >> 3) & 3) + 16 * ((r >> 2) & 1) + (r & 3);
+    vw[i] = (uint32_t)(n * (int)p.ldw + chunk);
+  }
+#pragma unroll
+  for (int i = 0; i < AC; ++i) {
+    const int r = 8 * (wave + NW * i) + (lane >> 3);
+    const uint32_t src = source_row(p, t, r);
+    va[i] = src == PAST ? PAST : src * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+  }
+  {
+    const uint32_t src = source_row(p, t, 64 * (wave % AM) + lane);
+    vs = src == PAST ? PAST : 4 * src * (uint32_t)p.as_sm;
+  }
+
+  // copy c (0 .. NCOPY - 1) of block j into stage st
+  auto copy = [&](int j, int st, int c) __attribute__((always_inline)) {
+    const uint32_t past = j < nkb ? 0 : PAST;
+    if (c < WC) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rows[c / (WC / 2)], (lds_void*)(lw + st * W_BYTES + SLAB * (wave + NW * c)), 16,
+                                               (vw[c] + KB * j) | past, 0, 0, 0);
+    } else if (c < WC + AC) {
+      const int k = c - WC;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(la + st * A_BYTES + SLAB * (wave + NW * k)), 16,
+                                               (va[k] + KB * j) | past, 0, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(ls + st * S_BYTES + 256 * (wave % AM)), 4,
+                                               (vs + 4 * (j >> 2) * (int)p.as_sw) | past, 0, 0, 0);
+    }
+  };
+
+  // the weight scales of the wave's two 32-row tiles
+  const uint32_t wsc0 = scale_lanes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : 64 * wn)) / 128, lane);
+  const uint32_t wsc1 = EPI == SWIGLU ? scale_lanes(p, w, (p.N / 2 + w.n0) / 128, lane) : wsc0;
+#pragma unroll
+  for (int i = 0; i < NST; ++i)
+#pragma unroll
+    for (int c = 0; c < NCOPY; ++c) copy(i, i, c);
+  __builtin_amdgcn_sched_barrier(0);
+
+  v16f acc[AN][AM];
+#pragma unroll
+  for (int i = 0; i < AN; ++i)
+#pragma unroll
+    for (int j = 0; j < AM; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // Half-steps of 64: while the MFMAs of one run, the operands of the next are
+  // read. One barrier a block, between its halves: by then every wave has read
+  // all of block j, whose stage is refilled, and block j + 1 has landed (only
+  // the NST - 2 blocks after it may be in flight).
+  constexpr int WAIT = waitcnt_vm((NST - 2) * NCOPY);
+  const int row = lane & 31, swz = (row >> 1) & 7;
+  v8i fw[2][AN], fa[2][AM];
+  uint32_t as_word[AM];
+  auto read_half = [&](int st, auto khc) __attribute__((always_inline)) {
+    constexpr int kh = decltype(khc)::value;
+    const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
+#pragma unroll
+    for (int u = 0; u < AM; ++u) {
+      const uint8_t* b = la + st * A_BYTES + KB * (32 * (2 * u + wm) + row);
+      fa[kh][u] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
+    }
+#pragma unroll
+    for (int i = 0; i < AN; ++i) {
+      const uint8_t* b = lw + st * W_BYTES + KB * ((EPI == SWIGLU ? 128 * i + 32 * wn : 64 * wn + 32 * i) + row);
+      fw[kh][i] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
+    }
+  };
+  auto read_scales = [&](int st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < AM; ++u) as_word[u] = *reinterpret_cast<const uint32_t*>(ls + st * S_BYTES + 4 * (32 * (2 * u + wm) + row));
+  };
+  using H0 = std::integral_constant<int, 0>;
+  using H1 = std::integral_constant<int, 1>;
+  {
+    constexpr int FIRST = waitcnt_vm((NST - 1) * NCOPY);
+    __builtin_amdgcn_s_waitcnt(FIRST);
+  }
+  block_barrier();
+  read_scales(0);
+  read_half(0, H0{});
+  int st = 0;
+  for (int j = 0; j < nkb; ++j) {
+    const int ws[2] = {scale_of(wsc0, j), scale_of(wsc1, j)};
+    int as[AM];
+#pragma unroll
+    for (int u = 0; u < AM; ++u) as[u] = (int)(as_word[u] >> (8 * (j & 3)));
+    read_half(st, H1{});
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < AN; ++i)
+#pragma unroll
+      for (int u = 0; u < AM; ++u)
+        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[0][i], fa[0][u], acc[i][u], 0, 0, 0, ws[i], 0, as[u]);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
+    __builtin_amdgcn_s_waitcnt(WAIT);
+    block_barrier();
+    const int st1 = st + 1 < NST ? st + 1 : 0;
+    read_scales(st1);
+    read_half(st1, H0{});
+    __builtin_amdgcn_sched_barrier(0);
+    // the copies one by one between the MFMAs: issued together they would hold
+    // the wave until the address unit has taken them all
+#pragma unroll
+    for (int i = 0; i < AN; ++i)
+#pragma unroll
+      for (int u = 0; u < AM; ++u) {
+        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[1][i], fa[1][u], acc[i][u], 0, 0, 0, ws[i], 0, as[u]);
+#pragma unroll
+        for (int c = NCOPY * (i * AM + u) / (AN * AM); c < NCOPY * (i * AM + u + 1) / (AN * AM); ++c) copy(j + NST, st, c);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    st = st1;
+  }
+
+  // in the ring's place: every wave has read its operands, and no copy is in flight
+  __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
+  __syncthreads();
+  if constexpr (EPI == SWIGLU) {
+    float* const amax = reinterpret_cast<float*>(lds);    // [wn][TM]
+#pragma unroll
+    for (int u = 0; u < AM; ++u) {
+      float m = 0.f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        acc[0][u][r] = swiglu(acc[0][u][r], acc[1][u][r]);
+        m = fmaxf(m, fabsf(acc[0][u][r]));
+      }
+      m = fmaxf(m, __shfl_xor(m, 32));
+      if (half == 0) amax[wn * TM + 32 * (2 * u + wm) + row] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < AM; ++u) {
+      const int r = 32 * (2 * u + wm) + row;
+      const float m = fmaxf(fmaxf(amax[r], amax[TM + r]), fmaxf(amax[2 * TM + r], amax[3 * TM + r]));
+      const int e = exponent_of(m);
+      const float mul = layer::pow2(-e);
+      if (r < t.rows) {
+        const int64_t place = t.begin + r;
+        uint32_t d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = codes4(acc[0][u][4 * i], acc[0][u][4 * i + 1], acc[0][u][4 * i + 2], acc[0][u][4 * i + 3], mul);
+        *reinterpret_cast<v4u*>(p.q + place * p.ldq + w.n0 + 32 * wn + 16 * half) = v4u{d[0], d[1], d[2], d[3]};
+        if (wn == 0 && half == 0) store_scale(p, place, w.n0, e);
+      }
+    }
+  } else {
+    // through the wave's part of LDS, 32 places at a time, so that a store covers
+    // whole stretches of a row
+    constexpr int PITCH = 64 * AN + 16, LANES = 4 * AN;   // bytes of a place's row; 16-byte pieces of it
+    uint8_t* const mine = lds + wave * 32 * PITCH;
+    const int64_t n0 = w.n0 + 64 * wn;
+    const int rows_n = p.N - n0 < 64 ? (int)(p.N - n0) : 64;
+#pragma unroll
+    for (int u = 0; u < AM; ++u) {
+      const int m = 32 * (2 * u + wm);
+      const int rows_m = t.rows - m < 32 ? t.rows - m : 32;
+#pragma unroll
+      for (int i = 0; i < AN; ++i) {
+        uint32_t d[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) d[r] = layer::pack_bf16(acc[i][u][2 * r], acc[i][u][2 * r + 1]);
+        uint8_t* const to = mine + row * PITCH + 64 * i + 32 * half;
+        *reinterpret_cast<v4u*>(to) = v4u{d[0], d[1], d[2], d[3]};
+        *reinterpret_cast<v4u*>(to + 16) = v4u{d[4], d[5], d[6], d[7]};
+      }
+      asm volatile("" ::: "memory");   // the wave's own writes, then its own reads: in order
+      uint16_t* const to = p.out + (int64_t)(t.begin + m) * p.ldo + n0;
+      if (p.wide_out && rows_n == 64) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 64 / LANES) {
+          const int r = i + lane / LANES, c = lane % LANES;
+          const v4u v = *reinterpret_cast<const v4u*>(mine + r * PITCH + 16 * c);
+          if (r < rows_m) *reinterpret_cast<v4u*>(to + r * p.ldo + 8 * c) = v;
+        }
+      } else {
+        for (int r = 0; r < rows_m; ++r)
+          if (lane < rows_n) to[r * p.ldo + lane] = *reinterpret_cast<const uint16_t*>(mine + r * PITCH + 2 * lane);
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+}
+
+// Stream body, for up to 16 MT places: the product is then a read of the
+// weights. Each wave owns 32 of the workgroup's 256 rows (SWIGLU: 16 gates and
+// their 16 ups) and walks all K blocks with an LDS ring of its own: no barrier
+// in the loop, only the wave's wait counts. 16x16x128 MFMA: weight rows as its
+// rows, places as its columns. Workgroups start the K blocks at different
+// places, as all rows lie at equal strides and would share memory channels.
+template <int MT>
+constexpr int stream_stage() { return (32 + 16 * MT) * KB + 256; }
+
+template <Epilogue EPI, int MT, int NST>
+__device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const groups::Tile& t, uint8_t* lds) {
+  constexpr int TOK = 16 * MT, STAGE = stream_stage<MT>();
+  constexpr int WC = 4, AC = TOK / 8, NCOPY = WC + AC + 1;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Weights w = weights_of<EPI>(p, t);
+  const int nkb = p.nkb;
+  const int rot = (int)((unsigned)(t.part * 5 + t.group * 3) % (unsigned)nkb);
+  const int64_t nw = (nkb + 3) / 4;
+  const rsrc_t ra = make_rsrc(p.a, (uint64_t)(p.M - 1) * p.lda + (uint64_t)KB * nkb);
+  const rsrc_t rs = make_rsrc(p.a_scales, 4 * (uint64_t)((p.M - 1) * p.as_sm + (nw - 1) * p.as_sw + 1));
+  // copy c moves rows 8 c + lane / 8, 16-byte chunk permuted by (row / 2) % 8
+  uint32_t vw[WC], va[AC];
+#pragma unroll
+  for (int c = 0; c < WC; ++c) {
+    const int r = 8 * c + (lane >> 3);
+    const int n = EPI == SWIGLU ? 16 * wave + (r & 15) : 32 * wave + r;
+    vw[c] = (uint32_t)(n * (int)p.ldw + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
+  }
+#pragma unroll
+  for (int c = 0; c < AC; ++c) {
+    const int r = 8 * c + (lane >> 3);
+    const uint32_t src = source_row(p, t, r);
+    va[c] = src == PAST ? PAST : src * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+  }
+  const uint32_t ssrc = lane < TOK ? source_row(p, t, lane) : PAST;
+  const uint32_t vs = ssrc == PAST ? PAST : 4 * ssrc * (uint32_t)p.as_sm;
+  uint8_t* const ring = lds + wave * NST * STAGE;
+
+  // the i-th block of the walk into stage st
+  auto block_of = [&](int i) __attribute__((always_inline)) { return i + rot < nkb ? i + rot : i + rot - nkb; };
+  auto copy = [&](int i, int st) __attribute__((always_inline)) {
+    const int j = block_of(i);
+    const uint32_t past = i < nkb ? 0 : PAST, u = KB * j;
+    uint8_t* const b = ring + st * STAGE;
+#pragma unroll
+    for (int c = 0; c < WC; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rows[c / 2], (lds_void*)(b + SLAB * c), 16, (vw[c] + u) | past, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < AC; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + 32 * KB + SLAB * c), 16, (va[c] + u) | past, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(b + (32 + TOK) * KB), 4, (vs + 4 * (j >> 2) * (int)p.as_sw) | past, 0, 0, 0);
+  };
+
+  const uint32_t wsc0 = scale_lanes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : 32 * wave)) / 128, lane);
+  const uint32_t wsc1 = EPI == SWIGLU ? scale_lanes(p, w, (p.N / 2 + w.n0) / 128, lane) : wsc0;
+#pragma unroll
+  for (int st = 0; st < NST; ++st) copy(st, st);
+  __builtin_amdgcn_sched_barrier(0);
+
+  v4f acc[2][MT];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = v4f{0.f, 0.f, 0.f, 0.f};
+  constexpr int WAIT = waitcnt_vm((NST - 1) * NCOPY);
+  const int swz = (col >> 1) & 7;
+  const int c0 = 16 * ((2 * g) ^ swz), c1 = 16 * ((2 * g + 1) ^ swz);
+  int st = 0;
+  for (int i = 0; i < nkb; ++i) {
+    __builtin_amdgcn_s_waitcnt(WAIT);
+    asm volatile("" ::: "memory");
+    const int j = block_of(i);
+    const uint8_t* const b = ring + st * STAGE;
+    const int ws[2] = {scale_of(wsc0, j), scale_of(wsc1, j)};
+    v8i fw[2], fa[MT];
+    int as[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      as[m] = (int)(*reinterpret_cast<const uint32_t*>(b + (32 + TOK) * KB + 4 * (16 * m + col)) >> (8 * (j & 3)));
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint8_t* x = b + KB * (16 * r + col);
+      fw[r] = make_v8i(*reinterpret_cast<const v4u*>(x + c0), *reinterpret_cast<const v4u*>(x + c1));
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint8_t* x = b + 32 * KB + KB * (16 * m + col);
+      fa[m] = make_v8i(*reinterpret_cast<const v4u*>(x + c0), *reinterpret_cast<const v4u*>(x + c1));
+    }
+    // the stage is read: refill it
+    __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    copy(i + NST, st);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        acc[r][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[r], fa[m], acc[r][m], 0, 0, 0, ws[r], 0, as[m]);
+    st = st + 1 < NST ? st + 1 : 0;
+  }
+
+  if constexpr (EPI == SWIGLU) {
+    __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
+    __syncthreads();
+    float* const amax = reinterpret_cast<float*>(lds);    // [wave][TOK], in the rings' place
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float x = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        acc[0][m][r] = swiglu(acc[0][m][r], acc[1][m][r]);
+        x = fmaxf(x, fabsf(acc[0][m][r]));
+      }
+      x = fmaxf(x, __shfl_xor(x, 16));
+      x = fmaxf(x, __shfl_xor(x, 32));
+      if (g == 0) amax[wave * TOK + 16 * m + col] = x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int r = 16 * m + col;
+      float x = amax[r];
+#pragma unroll
+      for (int v = 1; v < NW; ++v) x = fmaxf(x, amax[v * TOK + r]);
+      const int e = exponent_of(x);
+      if (r < t.rows) {
+        const int64_t place = t.begin + r;
+        *reinterpret_cast<uint32_t*>(p.q + place * p.ldq + w.n0 + 16 * wave + 4 * g) =
+            codes4(acc[0][m][0], acc[0][m][1], acc[0][m][2], acc[0][m][3], layer::pow2(-e));
+        if (wave == 0 && g == 0) store_scale(p, place, w.n0, e);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      if (16 * m + col < t.rows)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int64_t n = w.n0 + 32 * wave + 16 * r + 4 * g;
+          const uint32_t lo = layer::pack_bf16(acc[r][m][0], acc[r][m][1]), hi = layer::pack_bf16(acc[r][m][2], acc[r][m][3]);
+          uint16_t* const to = p.out + (int64_t)(t.begin + 16 * m + col) * p.ldo + n;
+          if (p.wide_out && n + 4 <= p.N) {
+            *reinterpret_cast<layer::v2u*>(to) = layer::v2u{lo, hi};
+          } else {
+            if (n < p.N) to[0] = (uint16_t)lo;
+            if (n + 1 < p.N) to[1] = (uint16_t)(lo >> 16);
+            if (n + 2 < p.N) to[2] = (uint16_t)hi;
+            if (n + 3 < p.N) to[3] = (uint16_t)(hi >> 16);
+          }
+        }
+  }
+}
+
+constexpr int lds_bytes() {
+  constexpr int ring = NW * 3 * stream_stage<1>();
+  static_assert(ring >= tile_bytes<1, 3>() && ring >= tile_bytes<2, 3>() && ring >= tile_bytes<3, 2>() && ring >= tile_bytes<4, 2>(), "LDS");
+  static_assert(ring <= 160 * 1024 && ring >= NW * 32 * 144, "LDS");
+  return ring;
+}
+
+// One tile a workgroup, by the body that its number of rows asks for: the host
+// does not know how many rows a group has.
+template <Epilogue EPI>
+__global__ __launch_bounds__(NW * 64)
+void fp8_grouped_kernel(Fp8GroupedArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[lds_bytes()];
+  const groups::Tile t = groups::find_tile(p.groups, 256, p.parts, groups::item_of(blockIdx.x, p.chunk));
+  if (t.rows <= 0) return;
+  if (t.rows <= 16) stream_body<EPI, 1, 3>(p, t, lds);
+  else if (t.rows <= 64) tile_body<EPI, 1, 3>(p, t, lds);
+  else if (t.rows <= 128) tile_body<EPI, 2, 3>(p, t, lds);
+  else if (t.rows <= 192) tile_body<EPI, 3, 2>(p, t, lds);
+  else tile_body<EPI, 4, 2>(p, t, lds);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_grouped(Fp8GroupedArgs p, hipStream_t stream) {
+  p.parts = (int32_t)(p.q ? p.N / TN : (p.N + TN - 1) / TN);
+  // at most so many tiles: whole ones, and one that is not for every group
+  const int64_t tiles = p.groups.R / 256 + (p.groups.G < p.groups.R ? p.groups.G : p.groups.R);
+  const int64_t items = tiles * p.parts;
+  p.chunk = items >= 2048 ? 32 : 1;
+  const int64_t blocks = (items + 8 * p.chunk - 1) / (8 * p.chunk) * (8 * p.chunk);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (p.q)
+    hipLaunchKernelGGL((fp8_grouped_kernel<SWIGLU>), dim3((unsigned)blocks), dim3(NW * 64), 0, stream, p);
+  else
+    hipLaunchKernelGGL((fp8_grouped_kernel<TO_BF16>), dim3((unsigned)blocks), dim3(NW * 64), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace iqp

@@ -334,6 +334,107 @@ hipError_t launch_attention_prefill(const AttnArgs& args, int D, hipStream_t str
 int64_t attention_workspace_bytes(int D);
 hipError_t launch_attention(const AttnArgs& args, int D, hipStream_t stream);
 
+// --- products whose weights depend on the row: experts, adapters -------------
+
+// R rows sorted by group: group g has the places offsets[g] .. offsets[g + 1] - 1
+// of the sorted order, place i holds entry rows[i] of the batch.
+struct RowGroups {
+  const int32_t* offsets;   // [G + 1]
+  const int32_t* rows;      // [R]
+  int64_t R;
+  int32_t G;
+};
+
+// Arguments of the grouped FP8 products (validated on the host).
+struct Fp8GroupedArgs {
+  RowGroups groups;
+  const uint8_t* a;         // E4M3 [M, K], row stride lda bytes
+  int64_t lda;
+  const int32_t* a_scales;  // packed UE8M0 words, strides in words
+  int64_t as_sm, as_sw;
+  int64_t M;
+  int32_t top;              // 0: place i reads row i of a; else row rows[i] / top
+  const uint8_t* w;         // E4M3 [G, N, K], strides ldwg, ldw bytes
+  int64_t ldwg, ldw;
+  const uint8_t* w_scales;  // UE8M0 [G, ceil(N / 128), K / 128], strides ld_wsg, ld_ws
+  int64_t ld_wsg, ld_ws;
+  int64_t N;                // SWIGLU: I gates, then I ups
+  int32_t nkb;              // K / 128
+  uint16_t* out;            // bf16 [R, N], row stride ldo elements, or
+  int64_t ldo;
+  bool wide_out;            // 16-byte stores allowed (out and ldo aligned)
+  uint8_t* q;               // SWIGLU: E4M3 [R, I], row stride ldq bytes (else NULL)
+  int64_t ldq;
+  int32_t* q_scales;        // packed UE8M0 words, strides in words
+  int64_t qs_sm, qs_sw;
+  int32_t parts;            // set by the launcher: workgroups of a tile's rows,
+  uint32_t chunk;           // consecutive ones to an XCD
+};
+hipError_t launch_fp8_grouped(Fp8GroupedArgs args, hipStream_t stream);
+
+struct MoeRouteArgs {
+  const void* logits;       // [M, E] float32, or bf16 (half), row stride ld
+  int64_t ld;
+  bool half;
+  const float* bias;        // [E] or NULL
+  int64_t M;
+  int32_t E, top, scoring;
+  bool renormalize;
+  float scale;
+  float* weights;           // [M, top]
+  int32_t* experts;
+};
+hipError_t launch_moe_route(const MoeRouteArgs& args, hipStream_t stream);
+
+constexpr int MAX_GROUPS = 1024;      // a thread a group in the sort
+constexpr int GROUP_CHUNKS = 128;     // workgroups of the sort at most
+struct GroupRowsArgs {
+  const int32_t* index;     // [R]
+  int64_t R;
+  int32_t G;
+  int32_t* offsets;         // [G + 1]
+  int32_t* rows;            // [R]
+  int32_t* slots;           // [R]
+  int32_t* counts;          // workspace: [chunks, G], where there are several
+  int64_t chunk;            // set by the launcher: entries of a workgroup
+};
+int64_t group_rows_chunk(int64_t R);
+hipError_t launch_group_rows(GroupRowsArgs args, hipStream_t stream);
+
+struct MoeCombineArgs {
+  const uint16_t* y;        // bf16 [R, d], row stride ldy
+  int64_t ldy, R;
+  const int32_t* slots;     // [M, top]
+  const float* weights;     // [M, top]
+  int32_t top;
+  const uint16_t* shared;   // bf16 [M, d], row stride lds, or NULL
+  int64_t lds;
+  int64_t M, d;
+  uint16_t* out;            // bf16 [M, d], row stride ldo
+  int64_t ldo;
+  int32_t parts;            // set by the launcher: workgroups of a row
+};
+hipError_t launch_moe_combine(MoeCombineArgs args, hipStream_t stream);
+
+struct LoraArgs {
+  RowGroups groups;
+  const uint16_t* x;        // bf16 [M, K], row stride ldx
+  int64_t ldx, M, K;
+  const uint16_t* a;        // bf16 [G, rank, K]
+  const uint16_t* b;        // bf16 [G, N, rank]
+  const float* scales;      // [G] or NULL
+  int32_t rank;
+  uint16_t* out;            // bf16 [M, N], row stride ldo
+  int64_t ldo, N;
+  bool wide_out;            // 16-byte loads and stores allowed (out and ldo aligned)
+  float* h;                 // workspace: [splits, R, lora_pitch(rank)]
+  int32_t splits;           // lora_splits(R, G, K)
+  int32_t h_pitch, parts;   // set by the launcher
+};
+int lora_splits(int64_t R, int32_t G, int64_t K);
+int lora_pitch(int32_t rank);
+hipError_t launch_lora_add(LoraArgs args, hipStream_t stream);
+
 // compute units of the current device (cached per device)
 int cu_count();
 

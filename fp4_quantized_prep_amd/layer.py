@@ -1,6 +1,7 @@
 """The operators around an attention layer with 8-bit operands: block-scaled
 FP8 product, per-head RMS norm with RoPE, the FP8 key/value cache and attention
-over it. Re-exported by the package; csrc/binding.cpp checks and marshals the
+over it; and the products beside it whose weights depend on the token: routing,
+experts, low-rank adapters. Re-exported by the package; csrc/binding.cpp checks and marshals the
 arguments of the C calls."""
 import typing
 
@@ -11,6 +12,8 @@ from . import _check, _lib
 __all__ = [
     "fp8_gemm_1x128_128x128", "fp8_gemm_workspace_bytes", "debug_fp8_gemm_kernel", "qk_norm_rope", "Fp8KvCache", "fp8_kv_cache", "kv_cache_append_fp8", "kv_cache_read_fp8",
     "attention_fp8_kv", "attention_fp8_kv_workspace_bytes", "attention_fp8_kv_workspace",
+    "RowGroups", "moe_route", "group_rows", "group_rows_workspace_bytes", "fp8_grouped_gemm_1x128_128x128", "fp8_grouped_swiglu_1x128",
+    "moe_combine", "lora_add", "lora_add_workspace_bytes",
 ]
 
 
@@ -165,3 +168,115 @@ def attention_fp8_kv(q, cache, block_table, seq_lens, cu_rows, scale: float = No
     """
     args = (q, *cache, block_table, seq_lens, cu_rows, scale, window, out, workspace)
     return _binding.attention(*args) if stream is None else _on(stream, q, _binding.attention, *args)
+
+
+class RowGroups(typing.NamedTuple):
+    """A batch's entries sorted by group (expert, adapter), as :func:`group_rows`
+    gives them. int32, contiguous."""
+    offsets: torch.Tensor  #: [n_groups + 1]: group g has the places offsets[g] .. offsets[g+1] - 1
+    rows: torch.Tensor     #: [R]: the (flat) entry at every place, -1 behind the last group
+    slots: torch.Tensor    #: in the index's shape: every entry's place, -1 for one in no group
+
+
+_SCORING = {"softmax": 0, "sigmoid": 1, "sqrt_softplus": 2}
+
+
+def moe_route(logits, top_k: int, bias=None, scoring: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+              weights=None, experts=None, stream=None):
+    """The ``top_k`` experts of every token and their weights.
+
+    logits: float32 or bf16 [M, E], rows contiguous, E up to 1024; bias: None or
+    float32 [E], added to the scores for the choice alone. scoring: "softmax",
+    "sigmoid" or "sqrt_softplus" (sqrt(log(1 + e^z))). The experts are those of the
+    largest logits, or with a bias of the largest score plus bias, the lower index
+    first where these are equal; a weight is ``scale`` times the score, divided by
+    the chosen ones' sum where ``renormalize``. An expert whose logit is -inf comes
+    last, with weight 0. Returns ``(weights, experts)``, float32 and int32 [M, top_k].
+    """
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be one of {', '.join(_SCORING)}, got {scoring!r}")
+    args = (logits, top_k, bias, _SCORING[scoring], renormalize, scale, weights, experts)
+    return _binding.route(*args) if stream is None else _on(stream, logits, _binding.route, *args)
+
+
+def group_rows_workspace_bytes(rows: int, n_groups: int) -> int:
+    """Bytes of the workspace that :func:`group_rows` needs for an index of ``rows``
+    entries (0: none)."""
+    return int(_lib.group_rows_workspace_bytes(rows, n_groups))
+
+
+def group_rows(index, n_groups: int, out=None, workspace=None, stream=None):
+    """Sorts a batch's entries by group, those of a group in their own order.
+
+    index: int32 [M] or [M, k], contiguous: the group of every entry
+    (:func:`moe_route`'s experts, or a token's adapter); one outside [0, n_groups)
+    is in none. n_groups: up to 1024. out: a :class:`RowGroups` to write to.
+    workspace: a uint8 tensor of :func:`group_rows_workspace_bytes` bytes (allocated
+    here when None); calls that share one must not overlap. Returns the
+    :class:`RowGroups`.
+    """
+    args = (index, n_groups, *(out or (None, None, None)), workspace)
+    return RowGroups(*(_binding.group(*args) if stream is None else _on(stream, index, _binding.group, *args)))
+
+
+def fp8_grouped_gemm_1x128_128x128(a, a_scales, w, w_scales, groups, gather: bool = False, out=None, stream=None):
+    """:func:`fp8_gemm_1x128_128x128` with weights of its own for every group of
+    rows: ``out[i] = a[src] w[g]^T`` for every place i of group g.
+
+    a, a_scales: as there; a row for every place (src = i), or with ``gather`` a row
+    for every token, whose entries the groups hold (src = rows[i] // k). Less than
+    2^31 bytes. w: E4M3 [n_groups, N, K], any N, and w_scales: uint8 [n_groups,
+    ceil(N/128), K/128], as :func:`fp8_quant_weight_128x128_ue8m0` gives them for
+    each group. Returns ``out``, bf16 [R, N], a row a place; places in no group are
+    left as they were (in a tensor allocated here they hold no particular values).
+    """
+    args = (a, a_scales, w, w_scales, *groups, gather, out)
+    return _binding.grouped_gemm(*args) if stream is None else _on(stream, a, _binding.grouped_gemm, *args)
+
+
+def fp8_grouped_swiglu_1x128(a, a_scales, w, w_scales, groups, gather: bool = False, q=None, q_scales=None, stream=None):
+    """The first product of a gated expert and what follows it, in one launch:
+    ``h = silu(gate) * up`` with ``[gate, up] = a[src] w[g]^T`` in float32,
+    quantised in 1x128 blocks.
+
+    Operands as in :func:`fp8_grouped_gemm_1x128_128x128`, with w [n_groups, 2 I, K]:
+    I gate rows, then I up rows, I a multiple of 128. Returns ``(q, q_scales)``: E4M3
+    codes (uint8) [R, I] and packed words int32 [R, ceil(I/512)], a row a place, the
+    operands of the second product. Places in no group as there.
+    """
+    args = (a, a_scales, w, w_scales, *groups, gather, q, q_scales)
+    return _binding.grouped_swiglu(*args) if stream is None else _on(stream, a, _binding.grouped_swiglu, *args)
+
+
+def moe_combine(y, groups, weights, shared=None, out=None, stream=None):
+    """Every token's weighted sum of its experts' rows, ``out[m] = sum_j
+    weights[m, j] y[slots[m, j]] (+ shared[m])``, in float32.
+
+    y: bf16 [R, d], a row a place, d a multiple of 8; weights: float32 in the shape
+    of the groups' slots; shared: None or bf16 [M, d] (the shared expert's rows, or a
+    residual). Entries in no group are left out. Rows contiguous, strides multiples
+    of 8. Returns ``out``, bf16 [M, d]; it may be ``shared`` itself.
+    """
+    args = (y, *groups, weights, shared, out)
+    return _binding.combine(*args) if stream is None else _on(stream, y, _binding.combine, *args)
+
+
+def lora_add_workspace_bytes(M: int, n_adapters: int, rank: int, K: int) -> int:
+    """Bytes of the workspace that :func:`lora_add` needs (0 for sizes it refuses)."""
+    return int(_lib.lora_add_workspace_bytes(M, n_adapters, rank, K))
+
+
+def lora_add(out, x, lora_a, lora_b, groups, scales=None, workspace=None, stream=None):
+    """Adds every token's low-rank adapter to the output of the projection that all
+    tokens share, in place: ``out[m] += scales[g] * lora_b[g] (lora_a[g] x[m])``.
+
+    out: bf16 [M, N], any N; x: bf16 [M, K], the projection's input, K a multiple of
+    8; rows contiguous, x's strides multiples of 8. lora_a: bf16 [n_adapters, rank,
+    K] and lora_b: bf16 [n_adapters, N, rank], contiguous and finite, rank a multiple
+    of 8 up to 128; scales: None or float32 [n_adapters]. groups: the
+    :func:`group_rows` of one adapter a token; tokens in none keep their rows' bits.
+    workspace: a uint8 tensor of :func:`lora_add_workspace_bytes` bytes (allocated here
+    when None); calls that share one must not overlap. Returns ``out``.
+    """
+    args = (out, x, lora_a, lora_b, *groups, scales, workspace)
+    return _binding.lora(*args) if stream is None else _on(stream, x, _binding.lora, *args)

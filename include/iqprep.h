@@ -40,13 +40,26 @@
  *  10. attention_fp8_kv   causal attention over that cache, for prompts, their
  *      continuations and single tokens in one ragged batch.
  *
+ * and the products beside it whose weights depend on the token:
+ *
+ *  11. moe_route   the experts of every token and their weights, from the router's
+ *      logits.
+ *  12. group_rows   a batch's entries sorted by expert or adapter: the order that
+ *      calls 13 to 16 read.
+ *  13. fp8_grouped_swiglu_1x128   the experts' first product, silu(gate) * up, and
+ *      the 1x128 quantization of the result.
+ *  14. fp8_grouped_gemm_1x128_128x128   call 7 with weights of its own for every
+ *      group of rows (the experts' second product).
+ *  15. moe_combine   every token's weighted sum of its experts' rows.
+ *  16. lora_add   low-rank adapters of many requests, added to a projection's output.
+ *
  * Conventions shared by every entry point:
  *
  *   - Every data pointer is a caller-owned DEVICE pointer on the current HIP
  *     device. The library never allocates, frees, copies or synchronizes; it
  *     enqueues kernels on `stream` (a hipStream_t; NULL = the null stream) and
  *     returns. Calls are therefore safe to capture into a HIP graph.
- *   - Inputs are never modified.
+ *   - Inputs are never modified (in-place outputs are: a cache, lora_add's out).
  *   - Sizes and leading dimensions are in elements of the named type unless
  *     stated otherwise; all offsets are computed in 64-bit.
  *   - Return value: IQP_OK, or an IQP_ERR_* code. Argument checks happen on
@@ -770,6 +783,137 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
                      const int32_t* seq_lens, const int32_t* cu_rows, int32_t S,
                      float scale, int32_t window, void* out, int64_t ldo,
                      void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * moe_route — the top_k experts of every token and their weights.
+ *
+ * With z the logits of a token (NaN where it should not be: see below), and
+ *   p_e = exp(z_e) / sum_f exp(z_f)      IQP_SCORE_SOFTMAX
+ *         1 / (1 + exp(-z_e))            IQP_SCORE_SIGMOID
+ *         sqrt(log(1 + exp(z_e)))        IQP_SCORE_SQRT_SOFTPLUS
+ * the experts are the first top_k in falling order of z_e, or with a bias of
+ * p_e + bias_e, the lower index first where these are equal, and
+ *   weight = scale * p_e / (sum of p over the chosen ones if renormalize, else 1).
+ * All in float64 and rounded to float32 once, so that the choice depends on no
+ * rounding of an exponential. An expert whose logit is -inf comes after all others
+ * and has weight 0; a token all of whose logits are -inf gets experts 0 ..
+ * top_k - 1 with weights 0. A NaN or +inf logit makes the token's weights NaN; the
+ * experts are distinct and in range all the same.
+ *
+ *   logits   float32, or bf16 where logits_bf16 is not 0, [M, E], row stride ld
+ *            (elements, >= E); 4- or 2-byte aligned. E 1 to 1024.
+ *   bias     NULL, or float32 [E], finite.
+ *   top_k    1 to min(E, 64).
+ *   weights  float32 [M, top_k];  experts  int32 [M, top_k]; both contiguous.
+ */
+#define IQP_SCORE_SOFTMAX        0
+#define IQP_SCORE_SIGMOID        1
+#define IQP_SCORE_SQRT_SOFTPLUS  2
+int moe_route(const void* logits, int64_t ld, int32_t logits_bf16, const float* bias, int64_t M, int32_t E,
+              int32_t top_k, int32_t scoring, int32_t renormalize, float scale, float* weights, int32_t* experts,
+              void* stream);
+
+/*
+ * group_rows — the R entries of index sorted by group, entries of a group in
+ * their own order: group g has the places offsets[g] .. offsets[g+1] - 1, place
+ * i holds entry rows[i], entry r is at place slots[r]. An entry outside [0, G)
+ * is in no group: its slot is -1, and rows holds -1 from offsets[G] on.
+ *
+ *   index      int32 [R]: moe_route's experts [M, top_k], or an adapter a token.
+ *   offsets    int32 [G + 1];  rows, slots  int32 [R]. G 1 to 1024.
+ *   workspace  group_rows_workspace_bytes(R, G) bytes of device memory, 4-byte
+ *              aligned (NULL where that is 0); its contents do not matter before
+ *              and mean nothing after. Calls that share one must not overlap.
+ * R == 0: offsets are all 0.
+ */
+int64_t group_rows_workspace_bytes(int64_t R, int32_t G);
+int group_rows(const int32_t* index, int64_t R, int32_t G, int32_t* offsets, int32_t* rows, int32_t* slots,
+               void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8_grouped_gemm_1x128_128x128 — fp8_gemm_1x128_128x128 with weights of its own
+ * for every group of rows, over places sorted by group (group_rows): for place i
+ * of group g
+ *   out[i, n] = bf16( sum_j 2^(ea(src,j) + ew(g,n/128,j)) sum_{k in block j} A[src,k] W[g,n,k] )
+ * with src = i where top_k is 0 (M == R), else rows[i] / top_k, the token that the
+ * place's entry belongs to (M * top_k == R). Rounding and accuracy as there.
+ *
+ * fp8_grouped_swiglu_1x128 — the same product with 2 I weight rows, gates 0 ..
+ * I - 1 and ups I .. 2 I - 1, then for channel c
+ *   h[i, c] = y_c / (1 + exp(-y_c)) * y_(I+c)       (float32)
+ * quantised from float32 as fp8_quant_1x128_ue8m0 quantises bf16: for each 128
+ * channels e = max(ceil(log2(amax / 448)), -22), codes E4M3 RNE of h 2^-e.
+ *
+ *   a, lda, a_scales, as_stride_m, as_stride_w   as in fp8_gemm_1x128_128x128, M
+ *              rows; they and their scale words each reach less than 2^31 bytes.
+ *   w          E4M3 [G, N, K] (swiglu: [G, 2 I, K]), strides ldwg, ldw (bytes,
+ *              multiples of 16, ldw up to 2^22), 16-byte aligned. w_scales UE8M0 [G,
+ *              ceil(N/128), K/128], strides ld_wsg, ld_ws (bytes).
+ *   offsets, rows, R, G   group_rows' (rows may be NULL where top_k is 0). Read on
+ *              the device; offsets outside [0, R] are clamped into it, rows that
+ *              name no token read zeros. Places in no group are not computed.
+ *   K          a multiple of 128, at most 32768;  I  a multiple of 128;  N  any.
+ *   out        bf16 [R, N], row stride ldo, as there. Rows of no group are left as
+ *              they were.
+ *   q          E4M3 [R, I], row stride ldq (bytes, a multiple of 16), 16-byte
+ *              aligned; q_scales packed words [R, ceil(I/512)] in either layout of
+ *              fp8_quant_1x128_ue8m0. Rows of no group are left as they were.
+ * R == 0, N == 0 or I == 0: no-op. The results must be finite in float32. The same
+ * call gives the same bits; a place's last bit may depend on how many rows its
+ * group has.
+ */
+int fp8_grouped_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m,
+                                   int64_t as_stride_w, int64_t M, const void* w, int64_t ldwg, int64_t ldw,
+                                   const uint8_t* w_scales, int64_t ld_wsg, int64_t ld_ws, const int32_t* offsets,
+                                   const int32_t* rows, int64_t R, int32_t G, int32_t top_k, int64_t N, int64_t K,
+                                   void* out, int64_t ldo, void* stream);
+int fp8_grouped_swiglu_1x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m,
+                             int64_t as_stride_w, int64_t M, const void* w, int64_t ldwg, int64_t ldw,
+                             const uint8_t* w_scales, int64_t ld_wsg, int64_t ld_ws, const int32_t* offsets,
+                             const int32_t* rows, int64_t R, int32_t G, int32_t top_k, int64_t I, int64_t K,
+                             void* q, int64_t ldq, int32_t* q_scales, int64_t qs_stride_m, int64_t qs_stride_w,
+                             void* stream);
+
+/*
+ * moe_combine — every token's weighted sum of its experts' rows:
+ *   out[m] = bf16( sum_j weights[m, j] y[slots[m, j]] + shared[m] )
+ * summed in float32 in the order of j. Slots outside [0, R) are left out (an
+ * expert that is not held here); a token without any gives shared's row, or zeros.
+ *
+ *   y        bf16 [R, d], row stride ldy;  shared  NULL, or bf16 [M, d], row stride
+ *            ld_shared;  out  bf16 [M, d], row stride ldo, may be shared itself
+ *            (same stride), otherwise must not overlap the inputs. 16-byte aligned,
+ *            d and the strides multiples of 8.
+ *   slots    int32 [M, top_k];  weights  float32 [M, top_k]; contiguous. top_k >= 1.
+ */
+int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, const float* weights, int64_t M,
+                int32_t top_k, int64_t d, const void* shared, int64_t ld_shared, void* out, int64_t ldo, void* stream);
+
+/*
+ * lora_add — low-rank adapters of many requests, added in place to the output of
+ * the projection that they share: for every place i of group g, with m = rows[i],
+ *   out[m] = bf16( out[m] + scales[g] * B[g] (A[g] x[m]) )
+ * (float32 sums; A[g] x[m] goes into the second product as two bf16 parts, 16
+ * significant bits). Rows in no group keep their bits.
+ *
+ *   x          bf16 [M, K], row stride ldx; 16-byte aligned, K and ldx multiples of 8.
+ *   a, b       bf16 [G, rank, K] and [G, N, rank], contiguous, 16-byte aligned, finite;
+ *              rank a multiple of 8, 8 to 128 (adapters of a lower one: zeros).
+ *   scales     NULL (1), or float32 [G].
+ *   offsets, rows, G   group_rows' of one adapter a token (R = M). Read on the device;
+ *              offsets outside [0, M] are clamped, rows outside [0, M) left out. No
+ *              row may be at two places (group_rows gives none).
+ *   out        bf16 [M, N], row stride ldo, 2-byte aligned (16-byte accesses where it
+ *              is 16-byte aligned and ldo a multiple of 8). Must not overlap the others.
+ *   workspace  lora_add_workspace_bytes(M, G, rank, K) bytes of device memory, 256-byte
+ *              aligned; its contents do not matter before and mean nothing after.
+ *              Calls that share one must not overlap.
+ * M == 0, N == 0 or G == 0: no-op. The same call gives the same bits.
+ */
+int64_t lora_add_workspace_bytes(int64_t M, int32_t G, int32_t rank, int64_t K);
+int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, const void* b, const float* scales,
+             int32_t rank, const int32_t* offsets, const int32_t* rows, int32_t G, int64_t N, void* out, int64_t ldo,
+             void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* iqp_status_string(int status);
