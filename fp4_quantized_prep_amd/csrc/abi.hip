@@ -920,7 +920,9 @@ int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, co
   if (!aligned(x, 16) || ldx % 8 || !aligned(a, 16) || !aligned(b, 16) || !aligned(scales, 4) || !aligned(offsets, 4) ||
       !aligned(rows, 4) || !aligned(out, 2))
     return IQP_ERR_UNSUPPORTED;
-  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || K > 0x7FFFFFFF || G > iqp::MAX_GROUPS) return IQP_ERR_UNSUPPORTED;
+  // x, and an adapter's rows, are addressed with 32-bit offsets
+  if (K > (1 << 22) || ldx >= (1 << 30) || M > 0x7FFFFFFF || 2 * ((M - 1) * ldx + K) >= ((int64_t)1 << 31)) return IQP_ERR_UNSUPPORTED;
+  if (N > 0x7FFFFFFF || G > iqp::MAX_GROUPS) return IQP_ERR_UNSUPPORTED;
   if (workspace_bytes < lora_add_workspace_bytes(M, G, rank, K)) return IQP_ERR_INVALID;
   if (!aligned(workspace, 256)) return IQP_ERR_UNSUPPORTED;
   const int st = device_status();
@@ -938,7 +940,7 @@ int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, co
   p.out = static_cast<uint16_t*>(out);
   p.ldo = ldo;
   p.N = N;
-  p.wide_out = aligned(out, 16) && ldo % 8 == 0;
+  p.wide_out = aligned(out, 16) && ldo % 8 == 0 && N % 8 == 0;
   p.h = static_cast<float*>(workspace);
   p.splits = iqp::lora_splits(M, G, K);
   return from_hip(iqp::launch_lora_add(p, static_cast<hipStream_t>(stream)));

@@ -426,7 +426,7 @@ struct LoraArgs {
   int32_t rank;
   uint16_t* out;            // bf16 [M, N], row stride ldo
   int64_t ldo, N;
-  bool wide_out;            // 16-byte loads and stores allowed (out and ldo aligned)
+  bool wide_out;            // 16-byte loads and stores allowed (out aligned, ldo and N multiples of 8)
   float* h;                 // workspace: [splits, R, lora_pitch(rank)]
   int32_t splits;           // lora_splits(R, G, K)
   int32_t h_pitch, parts;   // set by the launcher

@@ -2,88 +2,126 @@
 //   out[m] += s_g B_g (A_g x[m]),  A_g [r, K], B_g [N, r], m's adapter g
 // in two launches: h = A_g x (the first kernel, cut along K where there are few
 // rows, each piece's sums kept apart in float32), then out += s_g B_g h.
+#include "iq_common.h"
 #include "layer_common.h"
 #include "row_groups.h"
 
 namespace iqp {
 namespace {
 
-using layer::v4f;
-using layer::v4u;
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int LORA_ROWS = 64;     // places of a workgroup
+constexpr int SHRINK_ROWS = 16, SHRINK_WAVES = 4;   // first launch: places and waves of a workgroup
+constexpr int LORA_ROWS = 64;     // second launch: places of a workgroup
 constexpr int LORA_COLS = 256;    // output columns of a workgroup (four waves of 64)
+
+// An offset beyond every buffer: they reach less than 2^31 bytes. Joined to others
+// by "or", so that two of them stay one.
+constexpr uint32_t PAST = 0x80000000u;
+
+constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
 __device__ __forceinline__ v8bf operand(v4u v) { return __builtin_bit_cast(v8bf, v); }
 
+// the row of place r of the tile, -1 where there is none
 __device__ __forceinline__ int64_t row_of(const LoraArgs& p, const groups::Tile& t, int r) {
-  if (r >= t.rows) return -1;
-  const int m = p.groups.rows[t.begin + r];
-  return m >= 0 && m < p.M ? m : -1;
+  const int m = p.groups.rows[t.begin + (r < t.rows ? r : 0)];
+  return r < t.rows && m >= 0 && m < p.M ? m : -1;
 }
 
-// h[z, place, i] = sum of A[g, i, k] x[m, k] over piece z of K. 16x16x32 MFMA: rows
-// of A as its rows, places as its columns; operands straight from memory, 64 k a
-// step. Up to 16 places: the four waves share out the steps and their sums meet in
-// LDS; more: each wave takes 16 of them.
+// h[z, place, i] = sum of A[g, i, k] x[m, k] over piece z of K, 16 places a
+// workgroup. Its waves share out K in steps of 64 and stream them through LDS rings
+// of their own (rows of 128 bytes, 16-byte chunk c of row r at c ^ r % 8, so that
+// the operand reads meet distinct banks); their sums meet in LDS. 16x16x32 MFMA: rows
+// of A as its rows, places as its columns. Operands straight from memory would take
+// the address unit 64 cycles a load, a line for every lane, for the 16 of whole
+// lines (4632x64x1536: 17.5 us, so 9.4).
 template <int RT>
-__global__ __launch_bounds__(256)
-void lora_shrink_kernel(LoraArgs p) {
-  constexpr int PITCH = 16 * RT + 4;
-  __shared__ __attribute__((aligned(16))) float part[4 * 16 * PITCH];
-  const groups::Tile t = groups::find_tile(p.groups, LORA_ROWS, p.splits, groups::item_of(blockIdx.x, 1));
+constexpr int shrink_stage() { return 2048 * (1 + RT); }
+
+template <int RT, int NST>
+__device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
+  constexpr int PITCH = 16 * RT + 4, STAGE = shrink_stage<RT>(), NCOPY = 2 * (1 + RT);
+  static_assert(4 * SHRINK_ROWS * PITCH <= NST * STAGE, "a wave's sums, in its ring's place");
+  const groups::Tile t = groups::find_tile(p.groups, SHRINK_ROWS, p.splits, groups::item_of(blockIdx.x, 1));
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool few = t.rows <= 16;
-  const int r0 = few ? 0 : 16 * wave;
-  if (r0 >= t.rows) return;            // (more than 16 rows: no barrier below)
-  const int64_t m = row_of(p, t, r0 + col);
-  const uint16_t* const x = p.x + (m < 0 ? 0 : m) * p.ldx;      // columns of rows that are none are not kept
-  const uint16_t* a[RT];
+  const int steps = (int)((p.K + 63) / 64), K = (int)p.K;
+  const int first = (int)((int64_t)steps * t.part / p.splits) + wave;
+  const int last = (int)((int64_t)steps * (t.part + 1) / p.splits);
+  const rsrc_t rx = make_rsrc(p.x, 2 * (uint64_t)((p.M - 1) * p.ldx + p.K));
+  const rsrc_t ra = make_rsrc(p.a + (int64_t)t.group * p.rank * p.K, 2 * (uint64_t)p.rank * p.K);
+  // copy c moves rows 8 c + lane / 8; rows that are none read zeros
+  const int chunk = (lane & 7) ^ (lane >> 3 & 7);
+  uint32_t vx[2], va[2 * RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int r = 16 * i + col < p.rank ? 16 * i + col : p.rank - 1;      // likewise
-    a[i] = p.a + ((int64_t)t.group * p.rank + r) * p.K;
+  for (int c = 0; c < 2; ++c) {
+    const int64_t m = row_of(p, t, 8 * c + (lane >> 3));
+    vx[c] = m < 0 ? PAST : (uint32_t)(2 * (m * p.ldx + 8 * chunk));
   }
-  const int steps = (int)((p.K + 63) / 64);
-  const int first = (int)((int64_t)steps * t.part / p.splits), last = (int)((int64_t)steps * (t.part + 1) / p.splits);
+#pragma unroll
+  for (int c = 0; c < 2 * RT; ++c) {
+    const int r = 8 * c + (lane >> 3);
+    va[c] = r < p.rank ? 2 * (uint32_t)(r * K + 8 * chunk) : PAST;
+  }
+  uint8_t* const ring = lds + wave * NST * STAGE;
+  auto copy = [&](int s, int st) __attribute__((always_inline)) {
+    // past the last column x reads zeros, and whatever A holds there goes with them
+    const uint32_t past = s < last ? 0 : PAST, tail = 64 * s + 8 * chunk < K ? past : PAST;
+    uint8_t* const b = ring + st * STAGE;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(b + 1024 * c), 16, (vx[c] + 128 * s) | tail, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < 2 * RT; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + 1024 * (2 + c)), 16, (va[c] + 128 * s) | past, 0, 0, 0);
+  };
+#pragma unroll
+  for (int st = 0; st < NST; ++st) copy(first + st * SHRINK_WAVES, st);
+  __builtin_amdgcn_sched_barrier(0);
   v4f acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  const v4u zero = {0u, 0u, 0u, 0u};
-#pragma unroll 2
-  for (int s = few ? first + wave : first; s < last; s += few ? 4 : 1) {
-    v4u fx[2], fa[2][RT];
+  constexpr int WAIT = waitcnt_vm((NST - 1) * NCOPY);
+  const int c0 = 128 * col + 16 * (g ^ (col & 7)), c1 = 128 * col + 16 * ((4 + g) ^ (col & 7));
+  int st = 0;
+  for (int s = first; s < last; s += SHRINK_WAVES) {
+    __builtin_amdgcn_s_waitcnt(WAIT);
+    asm volatile("" ::: "memory");
+    const uint8_t* const b = ring + st * STAGE;
+    v4u fx[2], fa[RT][2];
+    fx[0] = *reinterpret_cast<const v4u*>(b + c0);
+    fx[1] = *reinterpret_cast<const v4u*>(b + c1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t k = 64 * (int64_t)s + 32 * h + 8 * g;
-      const bool in = k < p.K;
-      fx[h] = in ? *reinterpret_cast<const v4u*>(x + k) : zero;
-#pragma unroll
-      for (int i = 0; i < RT; ++i) fa[h][i] = in ? *reinterpret_cast<const v4u*>(a[i] + k) : zero;
+    for (int i = 0; i < RT; ++i) {
+      fa[i][0] = *reinterpret_cast<const v4u*>(b + 2048 * (1 + i) + c0);
+      fa[i][1] = *reinterpret_cast<const v4u*>(b + 2048 * (1 + i) + c1);
     }
+    // the stage is read: refill it
+    __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    copy(s + NST * SHRINK_WAVES, st);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(fa[h][i]), operand(fx[h]), acc[i], 0, 0, 0);
+      for (int i = 0; i < RT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(fa[i][h]), operand(fx[h]), acc[i], 0, 0, 0);
+    st = st + 1 < NST ? st + 1 : 0;
   }
-  float* const to = p.h + ((int64_t)t.part * p.groups.R + t.begin) * (16 * RT);
-  if (!few) {
-    if (r0 + col < t.rows)
-#pragma unroll
-      for (int i = 0; i < RT; ++i) *reinterpret_cast<v4f*>(to + (r0 + col) * (16 * RT) + 16 * i + 4 * g) = acc[i];
-    return;
-  }
+  __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
+  __syncthreads();
+  float* const part = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int i = 0; i < RT; ++i) *reinterpret_cast<v4f*>(part + (16 * wave + col) * PITCH + 16 * i + 4 * g) = acc[i];
   __syncthreads();
-  for (int i = threadIdx.x; i < t.rows * 4 * RT; i += 256) {
+  float* const to = p.h + ((int64_t)t.part * p.groups.R + t.begin) * (16 * RT);
+  for (int i = threadIdx.x; i < t.rows * 4 * RT; i += 64 * SHRINK_WAVES) {
     const int r = i / (4 * RT), c = 4 * (i % (4 * RT));
     v4f sum = *reinterpret_cast<const v4f*>(part + r * PITCH + c);
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
+    for (int w = 1; w < SHRINK_WAVES; ++w) {
       const v4f v = *reinterpret_cast<const v4f*>(part + (16 * w + r) * PITCH + c);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] += v[e];
@@ -92,98 +130,156 @@ void lora_shrink_kernel(LoraArgs p) {
   }
 }
 
-// out += s B h. MFMA: rows of B as its rows, places as its columns; row 4 g + i of
-// tile t is column 16 g + 4 t + i of the wave's 64, so that a lane has sixteen
-// consecutive ones of one place. h goes in as two bf16 parts (16 significant
-// bits together): the second product costs less than the output's way to memory,
-// and h rounded to one would be off as much as the output's own rounding.
+template <int RT, int NST>
+__global__ __launch_bounds__(64 * SHRINK_WAVES)
+void lora_shrink_kernel(LoraArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[SHRINK_WAVES * NST * shrink_stage<RT>()];
+  shrink<RT, NST>(p, lds);
+}
+
+// h of the tile's places, added up once for the workgroup and scaled, in two bf16
+// parts (16 significant bits together: the second product costs less than the
+// output's way to memory, and h rounded to one would be off as much as the output's
+// own rounding). Eight values a thread and turn; `parts` rows of 64 KT + 8, the
+// high parts first.
 template <int KT>
+__device__ __forceinline__ void split_h(const LoraArgs& p, const groups::Tile& t, __bf16* parts) {
+  constexpr int HP = 64 * KT + 8;
+  const float scale = p.scales ? p.scales[t.group] : 1.f;
+  for (int c = threadIdx.x; c < t.rows * (4 * KT); c += 256) {
+    const int r = c / (4 * KT), k = 8 * (c % (4 * KT));
+    v8bf hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hi[e] = lo[e] = (__bf16)0.f;
+    if (k < p.rank) {
+      const float* const h = p.h + ((int64_t)t.begin + r) * p.h_pitch + k;
+      v4f v[8][2];      // all pieces' loads, then their sum in order
+#pragma unroll
+      for (int z = 0; z < 8; ++z)
+        if (z < p.splits) {
+          const float* const q = h + (int64_t)z * p.groups.R * p.h_pitch;
+          v[z][0] = *reinterpret_cast<const v4f*>(q);
+          v[z][1] = *reinterpret_cast<const v4f*>(q + 4);
+        }
+#pragma unroll
+      for (int z = 1; z < 8; ++z)
+        if (z < p.splits)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[0][0][e] += v[z][0][e];
+            v[0][1][e] += v[z][1][e];
+          }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = v[0][e / 4][e & 3] * scale;
+        hi[e] = (__bf16)x;
+        lo[e] = (__bf16)(x - (float)hi[e]);
+      }
+    }
+    *reinterpret_cast<v8bf*>(parts + r * HP + k) = hi;
+    *reinterpret_cast<v8bf*>(parts + r * HP + 32 * KT + k) = lo;
+  }
+}
+
+// out += s B h, 64 columns a wave. MFMA: rows of B as its rows, places as its
+// columns. The products pass through the wave's part of LDS, 16 places at a time,
+// so that loads and stores of out cover whole stretches of a row: 16 bytes a lane
+// (WIDE, where out's alignment allows it), else 2 bytes a lane. All old values are
+// asked for before anything is multiplied.
+template <int KT, bool WIDE>
 __global__ __launch_bounds__(256)
 void lora_expand_kernel(LoraArgs p) {
-  const groups::Tile t = groups::find_tile(p.groups, LORA_ROWS, p.parts, groups::item_of(blockIdx.x, 1));
+  constexpr int PITCH = 68, HP = 64 * KT + 8;      // of a product's row (floats), of h's two parts (bf16)
+  __shared__ __attribute__((aligned(16))) float lds[4 * 16 * PITCH];
+  __shared__ __attribute__((aligned(16))) __bf16 parts[LORA_ROWS * HP];
+  const groups::Tile t = groups::find_tile<true>(p.groups, LORA_ROWS, p.parts, groups::item_of(blockIdx.x, 1));
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  split_h<KT>(p, t, parts);
+  __syncthreads();
   const int64_t n0 = (int64_t)t.part * LORA_COLS + 64 * wave;
   if (n0 >= p.N) return;
-  const v4u zero = {0u, 0u, 0u, 0u};
+  float* const mine = lds + wave * 16 * PITCH;
+  // WIDE: 8 rows at a time, 8 columns a lane (N is a multiple of 8 where this is asked
+  // for: lanes past the last column leave the row); else a row and a column a lane
+  constexpr int TURNS = WIDE ? 2 : 16;
+  const int c = WIDE ? 8 * (lane & 7) : lane;
+  const bool in = n0 + c < p.N;
+  int64_t m[4][TURNS];
+  v4u wide[4][WIDE ? 2 : 1];
+  uint16_t narrow[4][WIDE ? 1 : 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (16 * i < t.rows)
+#pragma unroll
+      for (int r = 0; r < TURNS; ++r) {
+        m[i][r] = row_of(p, t, 16 * i + (WIDE ? 8 * r + (lane >> 3) : r));
+        const uint16_t* const from = p.out + (m[i][r] < 0 ? 0 : m[i][r]) * p.ldo + n0 + (in ? c : 0);
+        if constexpr (WIDE) wide[i][r] = *reinterpret_cast<const v4u*>(from);
+        else narrow[i][r] = *from;
+      }
   v4u b[KT][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    int64_t n = n0 + 16 * (col >> 2) + 4 * i + (col & 3);
+    int64_t n = n0 + 16 * i + col;
     n = n < p.N ? n : p.N - 1;         // columns past the last one are not kept
     const uint16_t* const row = p.b + (t.group * p.N + n) * p.rank;
 #pragma unroll
-    for (int s = 0; s < KT; ++s) b[s][i] = 32 * s + 8 * g < p.rank ? *reinterpret_cast<const v4u*>(row + 32 * s + 8 * g) : zero;
+    for (int s = 0; s < KT; ++s)       // (past the rank h is zero)
+      b[s][i] = *reinterpret_cast<const v4u*>(row + (32 * s + 8 * g < p.rank ? 32 * s + 8 * g : 0));
   }
-  const float scale = p.scales ? p.scales[t.group] : 1.f;
-  const int64_t n = n0 + 16 * g;
-  for (int r0 = 0; r0 < t.rows; r0 += 16) {
-    const int64_t m = row_of(p, t, r0 + col);
-    const float* const h = p.h + ((int64_t)t.begin + (r0 + col < t.rows ? r0 + col : 0)) * p.h_pitch;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r0 = 16 * i;
+    if (r0 >= t.rows) break;
+    const __bf16* const h = parts + (r0 + col < t.rows ? r0 + col : 0) * HP + 8 * g;
     v4f acc[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < 4; ++q) acc[q] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < KT; ++s) {
-      const int k = 32 * s + 8 * g;
-      v8bf hi, lo;
+      const v8bf hi = *reinterpret_cast<const v8bf*>(h + 32 * s), lo = *reinterpret_cast<const v8bf*>(h + 32 * (KT + s));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) hi[e] = lo[e] = (__bf16)0.f;
-      if (k < p.rank) {
-        float v[8] = {};
-        for (int z = 0; z < p.splits; ++z) {
-          const float* const q = h + (int64_t)z * p.groups.R * p.h_pitch + k;
-          const v4f v0 = *reinterpret_cast<const v4f*>(q), v1 = *reinterpret_cast<const v4f*>(q + 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] += v0[e];
-            v[4 + e] += v1[e];
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = v[e] * scale;
-          hi[e] = (__bf16)x;
-          lo[e] = (__bf16)(x - (float)hi[e]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(b[s][i]), lo, acc[i], 0, 0, 0);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(b[s][i]), hi, acc[i], 0, 0, 0);
+      for (int q = 0; q < 4; ++q) {
+        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(b[s][q]), lo, acc[q], 0, 0, 0);
+        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(b[s][q]), hi, acc[q], 0, 0, 0);
       }
     }
-    if (m < 0) continue;
-    uint16_t* const out = p.out + m * p.ldo + n;
-    if (p.wide_out && n + 16 <= p.N) {
+    asm volatile("" ::: "memory");   // the wave's own reads, its writes, its reads: in order
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const v4u o = *reinterpret_cast<const v4u*>(out + 8 * c);
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<v4f*>(mine + col * PITCH + 16 * q + 4 * g) = acc[q];
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int r = 0; r < TURNS; ++r) {
+      uint16_t* const to = p.out + m[i][r] * p.ldo + n0 + c;
+      if constexpr (WIDE) {
+        const float* const from = mine + (8 * r + (lane >> 3)) * PITCH + c;
+        const v4f lo = *reinterpret_cast<const v4f*>(from), hi = *reinterpret_cast<const v4f*>(from + 4);
+        const v4u o = wide[i][r];
         v4u d;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          d[e] = layer::pack_bf16(layer::bf16_lo(o[e]) + acc[2 * c + e / 2][2 * (e & 1)],
-                                  layer::bf16_hi(o[e]) + acc[2 * c + e / 2][2 * (e & 1) + 1]);
-        *reinterpret_cast<v4u*>(out + 8 * c) = d;
+        for (int e = 0; e < 4; ++e) {
+          const float x = e < 2 ? lo[2 * e] : hi[2 * e - 4], y = e < 2 ? lo[2 * e + 1] : hi[2 * e - 3];
+          d[e] = layer::pack_bf16(layer::bf16_lo(o[e]) + x, layer::bf16_hi(o[e]) + y);
+        }
+        if (in && m[i][r] >= 0) *reinterpret_cast<v4u*>(to) = d;
+      } else {
+        if (in && m[i][r] >= 0) *to = (uint16_t)layer::pack_bf16(layer::bf16_lo(narrow[i][r]) + mine[r * PITCH + lane], 0.f);
       }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (n + c < p.N) out[c] = (uint16_t)layer::pack_bf16(layer::bf16_lo(out[c]) + acc[c / 4][c & 3], 0.f);
     }
   }
 }
 
-int64_t tiles_of(const RowGroups& g) { return g.R / LORA_ROWS + (g.G < g.R ? g.G : g.R); }
+int64_t tiles_of(int64_t R, int32_t G, int rows) { return R / rows + (G < R ? G : R); }
 
 }  // namespace
 
-// Pieces of K: enough that the first launch has 512 workgroups, of eight steps at least
+// Pieces of K: enough that the first launch has 512 workgroups, of two steps a wave at least
 int lora_splits(int64_t R, int32_t G, int64_t K) {
-  const int64_t tiles = tiles_of(RowGroups{nullptr, nullptr, R, G}), steps = (K + 63) / 64;
+  const int64_t tiles = tiles_of(R, G, SHRINK_ROWS), steps = (K + 63) / 64;
   int64_t z = 512 / (tiles > 0 ? tiles : 1);
-  if (z > steps / 8) z = steps / 8;
+  if (z > steps / (2 * SHRINK_WAVES)) z = steps / (2 * SHRINK_WAVES);
   return z < 1 ? 1 : z > 8 ? 8 : (int)z;
 }
 
@@ -192,15 +288,20 @@ int lora_pitch(int32_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <
 hipError_t launch_lora_add(LoraArgs p, hipStream_t stream) {
   p.h_pitch = lora_pitch(p.rank);
   p.parts = (int32_t)((p.N + LORA_COLS - 1) / LORA_COLS);
-  const int64_t tiles = tiles_of(p.groups);
-  const int64_t shrink = (tiles * p.splits + 7) / 8 * 8, expand = (tiles * p.parts + 7) / 8 * 8;
+  const int64_t shrink = (tiles_of(p.groups.R, p.groups.G, SHRINK_ROWS) * p.splits + 7) / 8 * 8;
+  const int64_t expand = (tiles_of(p.groups.R, p.groups.G, LORA_ROWS) * p.parts + 7) / 8 * 8;
   if (shrink > 0x7FFFFFFF || expand > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const auto first = p.h_pitch == 16 ? lora_shrink_kernel<1> : p.h_pitch == 32 ? lora_shrink_kernel<2> : p.h_pitch == 64 ? lora_shrink_kernel<4> : lora_shrink_kernel<8>;
-  hipLaunchKernelGGL(first, dim3((unsigned)shrink), dim3(256), 0, stream, p);
+  // (LDS for two workgroups a CU up to rank 64)
+  const auto first = p.h_pitch == 16   ? lora_shrink_kernel<1, 4>
+                     : p.h_pitch == 32 ? lora_shrink_kernel<2, 3>
+                     : p.h_pitch == 64 ? lora_shrink_kernel<4, 2>
+                                       : lora_shrink_kernel<8, 2>;
+  hipLaunchKernelGGL(first, dim3((unsigned)shrink), dim3(64 * SHRINK_WAVES), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const auto second = p.rank <= 32 ? lora_expand_kernel<1> : p.rank <= 64 ? lora_expand_kernel<2> : lora_expand_kernel<4>;
-  hipLaunchKernelGGL(second, dim3((unsigned)expand), dim3(256), 0, stream, p);
+  const auto wide = p.rank <= 32 ? lora_expand_kernel<1, true> : p.rank <= 64 ? lora_expand_kernel<2, true> : lora_expand_kernel<4, true>;
+  const auto narrow = p.rank <= 32 ? lora_expand_kernel<1, false> : p.rank <= 64 ? lora_expand_kernel<2, false> : lora_expand_kernel<4, false>;
+  hipLaunchKernelGGL(p.wide_out ? wide : narrow, dim3((unsigned)expand), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -29,9 +29,11 @@ struct Tile {
 
 // Tile number `item`, where every group's rows are cut into tiles of tm (the
 // last one shorter) and each tile has `parts` parts; a group's items follow one
-// another part by part, its tiles innermost, so that neighbours share weights.
+// another part by part, its tiles innermost, so that neighbours share weights, or
+// (TILE_BY_TILE) tile by tile, so that they share rows.
 // All lanes of all waves call it and get the same answer. Offsets are kept
 // inside [0, R] whatever they hold. 256 groups a round of loads.
+template <bool TILE_BY_TILE = false>
 __device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts, int64_t item) {
   const int lane = threadIdx.x & 63;
   int64_t done = 0;
@@ -53,7 +55,7 @@ __device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts,
         const int at = 63 - __builtin_clzll(__ballot((done + upto - tiles) * parts <= item));
         const int mine = __builtin_amdgcn_readlane(tiles, at);
         const int local = (int)(item - (done + __builtin_amdgcn_readlane(upto, at) - mine) * parts);
-        const int part = local / mine, t = local - part * mine;
+        const int part = TILE_BY_TILE ? local % parts : local / mine, t = TILE_BY_TILE ? local / parts : local - part * mine;
         const int rows = __builtin_amdgcn_readlane(n, at) - t * tm;
         return {g0 + 64 * q + at, __builtin_amdgcn_readlane(b, at) + t * tm, rows < tm ? rows : tm, part};
       }

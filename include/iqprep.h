@@ -896,7 +896,8 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
  * (float32 sums; A[g] x[m] goes into the second product as two bf16 parts, 16
  * significant bits). Rows in no group keep their bits.
  *
- *   x          bf16 [M, K], row stride ldx; 16-byte aligned, K and ldx multiples of 8.
+ *   x          bf16 [M, K], row stride ldx; 16-byte aligned, K and ldx multiples of 8, K
+ *              at most 2^22; it reaches less than 2^31 bytes.
  *   a, b       bf16 [G, rank, K] and [G, N, rank], contiguous, 16-byte aligned, finite;
  *              rank a multiple of 8, 8 to 128 (adapters of a lower one: zeros).
  *   scales     NULL (1), or float32 [G].
@@ -904,7 +905,7 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
  *              offsets outside [0, M] are clamped, rows outside [0, M) left out. No
  *              row may be at two places (group_rows gives none).
  *   out        bf16 [M, N], row stride ldo, 2-byte aligned (16-byte accesses where it
- *              is 16-byte aligned and ldo a multiple of 8). Must not overlap the others.
+ *              is 16-byte aligned and ldo and N multiples of 8). Must not overlap the others.
  *   workspace  lora_add_workspace_bytes(M, G, rank, K) bytes of device memory, 256-byte
  *              aligned; its contents do not matter before and mean nothing after.
  *              Calls that share one must not overlap.

@@ -105,7 +105,7 @@ def test_lora_refusals(iqp):
     for bad in (dict(M=-1), dict(K=-1), dict(rank=-1), dict(G=-1), dict(N=-1), dict(wb=-1), dict(x=0), dict(a=0), dict(b=0), dict(off=0),
                 dict(rows=0), dict(o=0), dict(w=0), dict(K=0), dict(rank=0), dict(ldx=248), dict(ldo=99), dict(wb=need - 1)):
         assert call(**bad) == inv, bad
-    for bad in (dict(rank=12), dict(rank=136), dict(K=252), dict(x=8), dict(ldx=260), dict(a=8), dict(b=8), dict(sc=18), dict(off=18),
+    for bad in (dict(rank=12), dict(rank=136), dict(K=252), dict(K=(1 << 22) + 8, ldx=1 << 23, wb=1 << 40), dict(x=8), dict(ldx=260), dict(a=8), dict(b=8), dict(sc=18), dict(off=18), dict(ldx=1 << 30), dict(M=(1 << 20) + 1, ldx=1024, wb=1 << 40),
                 dict(rows=18), dict(o=17), dict(M=1 << 31), dict(N=1 << 31, ldo=1 << 31), dict(G=1025), dict(w=128)):
         assert call(**bad) == uns, bad
     assert call(M=0) == iqp.IQP_OK and call(N=0) == iqp.IQP_OK and call(G=0) == iqp.IQP_OK
