@@ -187,73 +187,79 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // Half-steps of 64: while the MFMAs of one run, the operands of the next are
-  // read. One barrier a block, between its halves: by then every wave has read
-  // all of block j, whose stage is refilled, and block j + 1 has landed (only
-  // the NST - 2 blocks after it may be in flight).
+  // Half-steps of 64. The places' operands of the next half are read one by one as
+  // the MFMAs are done with those of this one, the weights' before all of them. One
+  // barrier a block, behind the first MFMAs of its second half: by then every wave
+  // has read all of block j, whose stage is refilled, and block j + 1 has landed
+  // (only the NST - 2 blocks after it may be in flight).
   constexpr int WAIT = waitcnt_vm((NST - 2) * NCOPY);
   const int row = lane & 31, swz = (row >> 1) & 7;
-  v8i fw[2][AN], fa[2][AM];
+  v8i fw[2][AN], fa[AM];
   uint32_t as_word[AM];
-  auto read_half = [&](int st, auto khc) __attribute__((always_inline)) {
-    constexpr int kh = decltype(khc)::value;
+  auto read_a = [&](int st, int kh, int u) __attribute__((always_inline)) {
+    const uint8_t* b = la + st * A_BYTES + KB * (32 * (2 * u + wm) + row);
     const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
-#pragma unroll
-    for (int u = 0; u < AM; ++u) {
-      const uint8_t* b = la + st * A_BYTES + KB * (32 * (2 * u + wm) + row);
-      fa[kh][u] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
-    }
+    fa[u] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
+  };
+  auto read_w = [&](int st, int kh) __attribute__((always_inline)) {
+    const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
 #pragma unroll
     for (int i = 0; i < AN; ++i) {
       const uint8_t* b = lw + st * W_BYTES + KB * ((EPI == SWIGLU ? 128 * i + 32 * wn : 64 * wn + 32 * i) + row);
       fw[kh][i] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
     }
   };
-  auto read_scales = [&](int st) __attribute__((always_inline)) {
-#pragma unroll
-    for (int u = 0; u < AM; ++u) as_word[u] = *reinterpret_cast<const uint32_t*>(ls + st * S_BYTES + 4 * (32 * (2 * u + wm) + row));
+  auto read_scale = [&](int st, int u) __attribute__((always_inline)) {
+    as_word[u] = *reinterpret_cast<const uint32_t*>(ls + st * S_BYTES + 4 * (32 * (2 * u + wm) + row));
   };
-  using H0 = std::integral_constant<int, 0>;
-  using H1 = std::integral_constant<int, 1>;
   {
     constexpr int FIRST = waitcnt_vm((NST - 1) * NCOPY);
     __builtin_amdgcn_s_waitcnt(FIRST);
   }
   block_barrier();
-  read_scales(0);
-  read_half(0, H0{});
+  read_w(0, 0);
+#pragma unroll
+  for (int u = 0; u < AM; ++u) {
+    read_scale(0, u);
+    read_a(0, 0, u);
+  }
   int st = 0;
   for (int j = 0; j < nkb; ++j) {
     const int ws[2] = {scale_of(wsc0, j), scale_of(wsc1, j)};
     int as[AM];
-#pragma unroll
-    for (int u = 0; u < AM; ++u) as[u] = (int)(as_word[u] >> (8 * (j & 3)));
-    read_half(st, H1{});
+    read_w(st, 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < AN; ++i)
+    for (int u = 0; u < AM; ++u) {
+      as[u] = (int)(as_word[u] >> (8 * (j & 3)));
 #pragma unroll
-      for (int u = 0; u < AM; ++u)
-        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[0][i], fa[0][u], acc[i][u], 0, 0, 0, ws[i], 0, as[u]);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
-    __builtin_amdgcn_s_waitcnt(WAIT);
-    block_barrier();
+      for (int i = 0; i < AN; ++i)
+        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[0][i], fa[u], acc[i][u], 0, 0, 0, ws[i], 0, as[u]);
+      __builtin_amdgcn_sched_barrier(0);
+      read_a(st, 1, u);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     const int st1 = st + 1 < NST ? st + 1 : 0;
-    read_scales(st1);
-    read_half(st1, H0{});
-    __builtin_amdgcn_sched_barrier(0);
-    // the copies one by one between the MFMAs: issued together they would hold
-    // the wave until the address unit has taken them all
 #pragma unroll
-    for (int i = 0; i < AN; ++i)
+    for (int u = 0; u < AM; ++u) {
 #pragma unroll
-      for (int u = 0; u < AM; ++u) {
-        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[1][i], fa[1][u], acc[i][u], 0, 0, 0, ws[i], 0, as[u]);
-#pragma unroll
-        for (int c = NCOPY * (i * AM + u) / (AN * AM); c < NCOPY * (i * AM + u + 1) / (AN * AM); ++c) copy(j + NST, st, c);
-        __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < AN; ++i)
+        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[1][i], fa[u], acc[i][u], 0, 0, 0, ws[i], 0, as[u]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (u == 0) {
+        __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
+        __builtin_amdgcn_s_waitcnt(WAIT);
+        block_barrier();
+        read_w(st1, 0);
       }
+      read_scale(st1, u);
+      read_a(st1, 0, u);
+      // the copies one by one between the MFMAs: issued together they would hold
+      // the wave until the address unit has taken them all
+#pragma unroll
+      for (int c = NCOPY * u / AM; c < NCOPY * (u + 1) / AM; ++c) copy(j + NST, st, c);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     st = st1;
   }
 
