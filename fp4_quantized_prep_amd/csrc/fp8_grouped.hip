@@ -19,7 +19,10 @@ enum Epilogue { TO_BF16, SWIGLU };
 
 constexpr int SLAB = 1024;   // bytes of one wave-wide copy to LDS
 constexpr int TN = 256;      // weight rows of a workgroup (SWIGLU: 128 gates and their 128 ups)
-constexpr int NW = 8;        // its waves
+constexpr int NW = 4;        // its waves
+constexpr int WN = NW / 2;   // waves along the weight rows in the tile body, two along the places
+constexpr int AN = TN / 32 / WN;   // 32-row tiles of a wave there (SWIGLU: half of them gates)
+constexpr int RT = TN / 16 / NW;   // 16-row tiles of a wave in the stream body (likewise)
 
 constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
@@ -104,8 +107,8 @@ __device__ __forceinline__ void store_scale(const Fp8GroupedArgs& p, int64_t pla
     for (int b = (block & 3) + 1; b < 4; ++b) word[b] = 0;
 }
 
-// Tile body: 256 weight rows x up to TM = 64 AM places, eight waves of 64 x 32 AM
-// (4 by 2; the places in tiles of 32 that alternate between the two). K block by
+// Tile body: 256 weight rows x up to TM = 64 AM places, four waves of 128 x 32 AM
+// (2 by 2; the places in tiles of 32 that alternate between the two). K block by
 // K block through NST LDS stages, 8 rows of 128 bytes a copy, the 16-byte chunks
 // of LDS row r permuted by (r / 2) % 8 so that the operand reads meet distinct
 // banks; weight row n of a 32-row tile sits in LDS row 8 ((n / 4) % 4) + 4 (n / 16)
@@ -117,13 +120,13 @@ constexpr int tile_bytes() { return NST * (TN * KB + 64 * AM * (KB + 4)); }
 
 template <Epilogue EPI, int AM, int NST>
 __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups::Tile& t, uint8_t* lds) {
-  constexpr int TM = 64 * AM, AN = 2;
+  constexpr int TM = 64 * AM;
   constexpr int W_BYTES = TN * KB, A_BYTES = TM * KB, S_BYTES = TM * 4;
   constexpr int WC = W_BYTES / SLAB / NW, AC = A_BYTES / SLAB / NW, NCOPY = WC + AC + 1;
-  static_assert(WC == 4 && AC == AM, "whole slabs");
+  static_assert(WC * NW * SLAB == W_BYTES && AC * NW * SLAB == A_BYTES && WC % 2 == 0, "whole slabs");
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wave & 3, wm = wave >> 2;
+  const int wn = wave % WN, wm = wave / WN;
   uint8_t* const lw = lds;
   uint8_t* const la = lw + NST * W_BYTES;
   uint8_t* const ls = la + NST * A_BYTES;
@@ -170,8 +173,8 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     }
   };
 
-  // the weight scales of the wave's two 32-row tiles
-  const uint32_t wsc0 = scale_lanes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : 64 * wn)) / 128, lane);
+  // the weight scales of the first and the second half of the wave's rows
+  const uint32_t wsc0 = scale_lanes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : 32 * AN * wn)) / 128, lane);
   const uint32_t wsc1 = EPI == SWIGLU ? scale_lanes(p, w, (p.N / 2 + w.n0) / 128, lane) : wsc0;
 #pragma unroll
   for (int i = 0; i < NST; ++i)
@@ -201,11 +204,14 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
     fa[u] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
   };
+  auto lds_row = [&](int i) __attribute__((always_inline)) {
+    return EPI == SWIGLU ? 128 * (i / (AN / 2)) + 32 * (AN / 2 * wn + i % (AN / 2)) : 32 * (AN * wn + i);
+  };
   auto read_w = [&](int st, int kh) __attribute__((always_inline)) {
     const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
 #pragma unroll
     for (int i = 0; i < AN; ++i) {
-      const uint8_t* b = lw + st * W_BYTES + KB * ((EPI == SWIGLU ? 128 * i + 32 * wn : 64 * wn + 32 * i) + row);
+      const uint8_t* b = lw + st * W_BYTES + KB * (lds_row(i) + row);
       fw[kh][i] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
     }
   };
@@ -234,7 +240,7 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
       as[u] = (int)(as_word[u] >> (8 * (j & 3)));
 #pragma unroll
       for (int i = 0; i < AN; ++i)
-        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[0][i], fa[u], acc[i][u], 0, 0, 0, ws[i], 0, as[u]);
+        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[0][i], fa[u], acc[i][u], 0, 0, 0, ws[i / (AN / 2)], 0, as[u]);
       __builtin_amdgcn_sched_barrier(0);
       read_a(st, 1, u);
       __builtin_amdgcn_sched_barrier(0);
@@ -244,7 +250,7 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     for (int u = 0; u < AM; ++u) {
 #pragma unroll
       for (int i = 0; i < AN; ++i)
-        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[1][i], fa[u], acc[i][u], 0, 0, 0, ws[i], 0, as[u]);
+        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[1][i], fa[u], acc[i][u], 0, 0, 0, ws[i / (AN / 2)], 0, as[u]);
       __builtin_amdgcn_sched_barrier(0);
       if (u == 0) {
         __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
@@ -272,10 +278,12 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     for (int u = 0; u < AM; ++u) {
       float m = 0.f;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        acc[0][u][r] = swiglu(acc[0][u][r], acc[1][u][r]);
-        m = fmaxf(m, fabsf(acc[0][u][r]));
-      }
+      for (int i = 0; i < AN / 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          acc[i][u][r] = swiglu(acc[i][u][r], acc[AN / 2 + i][u][r]);
+          m = fmaxf(m, fabsf(acc[i][u][r]));
+        }
       m = fmaxf(m, __shfl_xor(m, 32));
       if (half == 0) amax[wn * TM + 32 * (2 * u + wm) + row] = m;
     }
@@ -283,15 +291,21 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
 #pragma unroll
     for (int u = 0; u < AM; ++u) {
       const int r = 32 * (2 * u + wm) + row;
-      const float m = fmaxf(fmaxf(amax[r], amax[TM + r]), fmaxf(amax[2 * TM + r], amax[3 * TM + r]));
+      float m = amax[r];
+#pragma unroll
+      for (int v = 1; v < WN; ++v) m = fmaxf(m, amax[v * TM + r]);
       const int e = exponent_of(m);
       const float mul = layer::pow2(-e);
       if (r < t.rows) {
         const int64_t place = t.begin + r;
-        uint32_t d[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = codes4(acc[0][u][4 * i], acc[0][u][4 * i + 1], acc[0][u][4 * i + 2], acc[0][u][4 * i + 3], mul);
-        *reinterpret_cast<v4u*>(p.q + place * p.ldq + w.n0 + 32 * wn + 16 * half) = v4u{d[0], d[1], d[2], d[3]};
+        for (int i = 0; i < AN / 2; ++i) {
+          const v16f& h = acc[i][u];
+          uint32_t d[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) d[k] = codes4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3], mul);
+          *reinterpret_cast<v4u*>(p.q + place * p.ldq + w.n0 + 32 * (AN / 2 * wn + i) + 16 * half) = v4u{d[0], d[1], d[2], d[3]};
+        }
         if (wn == 0 && half == 0) store_scale(p, place, w.n0, e);
       }
     }
@@ -300,8 +314,8 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     // whole stretches of a row
     constexpr int PITCH = 64 * AN + 16, LANES = 4 * AN;   // bytes of a place's row; 16-byte pieces of it
     uint8_t* const mine = lds + wave * 32 * PITCH;
-    const int64_t n0 = w.n0 + 64 * wn;
-    const int rows_n = p.N - n0 < 64 ? (int)(p.N - n0) : 64;
+    const int64_t n0 = w.n0 + 32 * AN * wn;
+    const int rows_n = p.N - n0 < 32 * AN ? (int)(p.N - n0) : 32 * AN;
 #pragma unroll
     for (int u = 0; u < AM; ++u) {
       const int m = 32 * (2 * u + wm);
@@ -317,7 +331,7 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
       }
       asm volatile("" ::: "memory");   // the wave's own writes, then its own reads: in order
       uint16_t* const to = p.out + (int64_t)(t.begin + m) * p.ldo + n0;
-      if (p.wide_out && rows_n == 64) {
+      if (p.wide_out && rows_n == 32 * AN) {
 #pragma unroll
         for (int i = 0; i < 32; i += 64 / LANES) {
           const int r = i + lane / LANES, c = lane % LANES;
@@ -326,7 +340,9 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
         }
       } else {
         for (int r = 0; r < rows_m; ++r)
-          if (lane < rows_n) to[r * p.ldo + lane] = *reinterpret_cast<const uint16_t*>(mine + r * PITCH + 2 * lane);
+#pragma unroll
+          for (int c = 0; c < 32 * AN; c += 64)
+            if (c + lane < rows_n) to[r * p.ldo + c + lane] = *reinterpret_cast<const uint16_t*>(mine + r * PITCH + 2 * (c + lane));
       }
       asm volatile("" ::: "memory");
     }
@@ -340,12 +356,12 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
 // rows, places as its columns. Workgroups start the K blocks at different
 // places, as all rows lie at equal strides and would share memory channels.
 template <int MT>
-constexpr int stream_stage() { return (32 + 16 * MT) * KB + 256; }
+constexpr int stream_stage() { return (16 * RT + 16 * MT) * KB + 256; }
 
 template <Epilogue EPI, int MT, int NST>
 __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const groups::Tile& t, uint8_t* lds) {
   constexpr int TOK = 16 * MT, STAGE = stream_stage<MT>();
-  constexpr int WC = 4, AC = TOK / 8, NCOPY = WC + AC + 1;
+  constexpr int WR = 16 * RT, WC = WR / 8, AC = TOK / 8, NCOPY = WC + AC + 1;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Weights w = weights_of<EPI>(p, t);
@@ -359,7 +375,7 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
 #pragma unroll
   for (int c = 0; c < WC; ++c) {
     const int r = 8 * c + (lane >> 3);
-    const int n = EPI == SWIGLU ? 16 * wave + (r & 15) : 32 * wave + r;
+    const int n = EPI == SWIGLU ? WR / 2 * wave + r % (WR / 2) : WR * wave + r;
     vw[c] = (uint32_t)(n * (int)p.ldw + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
   }
 #pragma unroll
@@ -380,22 +396,22 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
     uint8_t* const b = ring + st * STAGE;
 #pragma unroll
     for (int c = 0; c < WC; ++c)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rows[c / 2], (lds_void*)(b + SLAB * c), 16, (vw[c] + u) | past, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rows[c / (WC / 2)], (lds_void*)(b + SLAB * c), 16, (vw[c] + u) | past, 0, 0, 0);
 #pragma unroll
     for (int c = 0; c < AC; ++c)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + 32 * KB + SLAB * c), 16, (va[c] + u) | past, 0, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(b + (32 + TOK) * KB), 4, (vs + 4 * (j >> 2) * (int)p.as_sw) | past, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + WR * KB + SLAB * c), 16, (va[c] + u) | past, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(b + (WR + TOK) * KB), 4, (vs + 4 * (j >> 2) * (int)p.as_sw) | past, 0, 0, 0);
   };
 
-  const uint32_t wsc0 = scale_lanes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : 32 * wave)) / 128, lane);
+  const uint32_t wsc0 = scale_lanes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : WR * wave)) / 128, lane);
   const uint32_t wsc1 = EPI == SWIGLU ? scale_lanes(p, w, (p.N / 2 + w.n0) / 128, lane) : wsc0;
 #pragma unroll
   for (int st = 0; st < NST; ++st) copy(st, st);
   __builtin_amdgcn_sched_barrier(0);
 
-  v4f acc[2][MT];
+  v4f acc[RT][MT];
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[r][m] = v4f{0.f, 0.f, 0.f, 0.f};
   constexpr int WAIT = waitcnt_vm((NST - 1) * NCOPY);
@@ -408,19 +424,19 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
     const int j = block_of(i);
     const uint8_t* const b = ring + st * STAGE;
     const int ws[2] = {scale_of(wsc0, j), scale_of(wsc1, j)};
-    v8i fw[2], fa[MT];
+    v8i fw[RT], fa[MT];
     int as[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-      as[m] = (int)(*reinterpret_cast<const uint32_t*>(b + (32 + TOK) * KB + 4 * (16 * m + col)) >> (8 * (j & 3)));
+      as[m] = (int)(*reinterpret_cast<const uint32_t*>(b + (WR + TOK) * KB + 4 * (16 * m + col)) >> (8 * (j & 3)));
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < RT; ++r) {
       const uint8_t* x = b + KB * (16 * r + col);
       fw[r] = make_v8i(*reinterpret_cast<const v4u*>(x + c0), *reinterpret_cast<const v4u*>(x + c1));
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const uint8_t* x = b + 32 * KB + KB * (16 * m + col);
+      const uint8_t* x = b + WR * KB + KB * (16 * m + col);
       fa[m] = make_v8i(*reinterpret_cast<const v4u*>(x + c0), *reinterpret_cast<const v4u*>(x + c1));
     }
     // the stage is read: refill it
@@ -430,10 +446,10 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
     copy(i + NST, st);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        acc[r][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[r], fa[m], acc[r][m], 0, 0, 0, ws[r], 0, as[m]);
+        acc[r][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[r], fa[m], acc[r][m], 0, 0, 0, ws[r / (RT / 2)], 0, as[m]);
     st = st + 1 < NST ? st + 1 : 0;
   }
 
@@ -445,10 +461,12 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
     for (int m = 0; m < MT; ++m) {
       float x = 0.f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        acc[0][m][r] = swiglu(acc[0][m][r], acc[1][m][r]);
-        x = fmaxf(x, fabsf(acc[0][m][r]));
-      }
+      for (int i = 0; i < RT / 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[i][m][r] = swiglu(acc[i][m][r], acc[RT / 2 + i][m][r]);
+          x = fmaxf(x, fabsf(acc[i][m][r]));
+        }
       x = fmaxf(x, __shfl_xor(x, 16));
       x = fmaxf(x, __shfl_xor(x, 32));
       if (g == 0) amax[wave * TOK + 16 * m + col] = x;
@@ -463,8 +481,10 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
       const int e = exponent_of(x);
       if (r < t.rows) {
         const int64_t place = t.begin + r;
-        *reinterpret_cast<uint32_t*>(p.q + place * p.ldq + w.n0 + 16 * wave + 4 * g) =
-            codes4(acc[0][m][0], acc[0][m][1], acc[0][m][2], acc[0][m][3], layer::pow2(-e));
+#pragma unroll
+        for (int i = 0; i < RT / 2; ++i)
+          *reinterpret_cast<uint32_t*>(p.q + place * p.ldq + w.n0 + WR / 2 * wave + 16 * i + 4 * g) =
+              codes4(acc[i][m][0], acc[i][m][1], acc[i][m][2], acc[i][m][3], layer::pow2(-e));
         if (wave == 0 && g == 0) store_scale(p, place, w.n0, e);
       }
     }
@@ -473,8 +493,8 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
     for (int m = 0; m < MT; ++m)
       if (16 * m + col < t.rows)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int64_t n = w.n0 + 32 * wave + 16 * r + 4 * g;
+        for (int r = 0; r < RT; ++r) {
+          const int64_t n = w.n0 + WR * wave + 16 * r + 4 * g;
           const uint32_t lo = layer::pack_bf16(acc[r][m][0], acc[r][m][1]), hi = layer::pack_bf16(acc[r][m][2], acc[r][m][3]);
           uint16_t* const to = p.out + (int64_t)(t.begin + 16 * m + col) * p.ldo + n;
           if (p.wide_out && n + 4 <= p.N) {
@@ -490,9 +510,9 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
 }
 
 constexpr int lds_bytes() {
-  constexpr int ring = NW * 3 * stream_stage<1>();
+  constexpr int stream = NW * 3 * stream_stage<1>(), tile = tile_bytes<2, 3>(), ring = stream > tile ? stream : tile;
   static_assert(ring >= tile_bytes<1, 3>() && ring >= tile_bytes<2, 3>() && ring >= tile_bytes<3, 2>() && ring >= tile_bytes<4, 2>(), "LDS");
-  static_assert(ring <= 160 * 1024 && ring >= NW * 32 * 144, "LDS");
+  static_assert(ring <= 160 * 1024 && ring >= NW * 32 * (64 * AN + 16), "LDS");
   return ring;
 }
 
