@@ -806,8 +806,7 @@ int moe_route(const void* logits, int64_t ld, int32_t logits_bf16, const float* 
 
 int64_t group_rows_workspace_bytes(int64_t R, int32_t G) {
   if (R <= 0 || R > 0x7FFFFFFF || G <= 0 || G > iqp::MAX_GROUPS) return 0;
-  const int64_t chunk = iqp::group_rows_chunk(R), chunks = (R + chunk - 1) / chunk;
-  return chunks > 1 ? chunks * G * 4 : 0;
+  return iqp::group_rows_counts(R) * G * 4;
 }
 
 int group_rows(const int32_t* index, int64_t R, int32_t G, int32_t* offsets, int32_t* rows, int32_t* slots, void* workspace,

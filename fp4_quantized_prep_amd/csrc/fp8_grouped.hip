@@ -339,10 +339,18 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
           if (r < rows_m) *reinterpret_cast<v4u*>(to + r * p.ldo + 8 * c) = v;
         }
       } else {
-        for (int r = 0; r < rows_m; ++r)
+        for (int r0 = 0; r0 < rows_m; r0 += 8) {      // eight rows' reads, then their stores
+          uint16_t v[8][AN / 2];
 #pragma unroll
-          for (int c = 0; c < 32 * AN; c += 64)
-            if (c + lane < rows_n) to[r * p.ldo + c + lane] = *reinterpret_cast<const uint16_t*>(mine + r * PITCH + 2 * (c + lane));
+          for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int c = 0; c < AN / 2; ++c) v[r][c] = *reinterpret_cast<const uint16_t*>(mine + (r0 + r) * PITCH + 2 * (64 * c + lane));
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int c = 0; c < AN / 2; ++c)
+              if (r0 + r < rows_m && 64 * c + lane < rows_n) to[(r0 + r) * p.ldo + 64 * c + lane] = v[r][c];
+        }
       }
       asm volatile("" ::: "memory");
     }

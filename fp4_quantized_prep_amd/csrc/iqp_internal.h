@@ -399,6 +399,7 @@ struct GroupRowsArgs {
   int64_t chunk;            // set by the launcher: entries of a workgroup
 };
 int64_t group_rows_chunk(int64_t R);
+int64_t group_rows_counts(int64_t R);
 hipError_t launch_group_rows(GroupRowsArgs args, hipStream_t stream);
 
 struct MoeCombineArgs {

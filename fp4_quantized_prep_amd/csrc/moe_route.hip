@@ -9,38 +9,60 @@ namespace {
 
 // ---------------------------------------------------------------- the router
 
-// A float64 as an unsigned integer of the same order, NaN above all (zeros of
-// either sign alike); never 0.
-__device__ __forceinline__ uint64_t order_of(double v) {
-  if (v != v) return ~0ull;
+// A choice and its expert as an unsigned integer of the order that the experts are
+// taken in: the order of float64, NaN above all, zeros of either sign alike, with
+// the index, counted down, in place of the last ten bits. A logit (float32 at
+// most) keeps all of its bits; a sum of score and bias keeps 42 of its mantissa,
+// eight fewer than its score is good to. Never 0.
+__device__ __forceinline__ uint64_t key_of(double v, int e) {
   const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
-  return b >> 63 ? ~b : b | 1ull << 63;
+  const uint64_t k = v != v ? ~0ull : b >> 63 ? ~b : b | 1ull << 63;
+  return (k & ~1023ull) | (uint64_t)(1023 - e);
 }
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
-  const uint64_t o = (uint64_t)hi << 32 | lo;
+__device__ __forceinline__ int expert_of(uint64_t key) { return 1023 - (int)(key & 1023); }
+
+// the logit that a key was made of
+__device__ __forceinline__ double logit_of(uint64_t key) {
+  return __longlong_as_double((long long)(key >> 63 ? (key & ~1023ull) ^ 1ull << 63 : ~(key | 1023ull)));
+}
+
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
   return o > v ? o : v;
 }
 
-// the largest of the 64 lanes, in every lane
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-  v = dpp_max<0x111, 0xF>(v);
-  v = dpp_max<0x112, 0xF>(v);
-  v = dpp_max<0x114, 0xF>(v);
-  v = dpp_max<0x118, 0xF>(v);
-  v = dpp_max<0x142, 0xA>(v);
-  v = dpp_max<0x143, 0xC>(v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63);
-  return (uint64_t)hi << 32 | lo;
+// the largest of a token's lanes (a row of 16, or all), in each of them
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (LANES == 16) {
+    v = dpp_max<0xB1>(v);      // lane ^ 1, ^ 2, mirrored in 8, in 16
+    v = dpp_max<0x4E>(v);
+    v = dpp_max<0x141>(v);
+    return dpp_max<0x140>(v);
+  } else {
+    v = dpp_max<0x111>(v);     // shifted by 1, 2, 4, 8, row to row, half to half
+    v = dpp_max<0x112>(v);
+    v = dpp_max<0x114>(v);
+    v = dpp_max<0x118>(v);
+    v = dpp_max<0x142, 0xA>(v);
+    v = dpp_max<0x143, 0xC>(v);
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  }
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
+// of 64 bits: the upper halves, then the lower ones of the lanes that have the largest
+template <int LANES>
+__device__ __forceinline__ uint64_t lanes_max(uint64_t v) {
+  const uint32_t hi = lanes_max<LANES>((uint32_t)(v >> 32));
+  return (uint64_t)hi << 32 | lanes_max<LANES>((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+}
+
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double v) {
 #pragma unroll
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+  for (int m = LANES / 2; m; m >>= 1) v += __shfl_xor(v, m);
   return v;
 }
 
@@ -49,14 +71,15 @@ __device__ __forceinline__ double score_of(double z, int scoring) {
   return sqrt((z > 0.0 ? z : 0.0) + log1p(exp(-fabs(z))));    // sqrt of softplus
 }
 
-// A wave a token, expert 64 v + lane its lane's v-th value. Scores and choices are
-// float64, so that which expert is taken does not hang on how an exponential is
-// rounded; the order is by choice, then by index.
-template <int VPL>
+// LANES lanes a token, expert LANES v + lane its lane's v-th value. Scores and
+// choices are float64, so that which expert is taken does not hang on how an
+// exponential is rounded. Bound by its instructions: 256 experts, top 8, with a bias:
+// 4.5 us for a token (2.5 of it a launch), 9.1 for 4632, whose logits' read takes 1.
+template <int LANES, int VPL>
 __global__ __launch_bounds__(256)
 void moe_route_kernel(MoeRouteArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t m = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & (LANES - 1);
+  const int64_t m = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
   if (m >= p.M) return;
   const auto logit = [&](int e) __attribute__((always_inline)) {
     return p.half ? (double)__uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.logits)[m * p.ld + e] << 16)
@@ -65,75 +88,65 @@ void moe_route_kernel(MoeRouteArgs p) {
   const double NONE = -__builtin_inf();
   double z[VPL];
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) z[v] = 64 * v + lane < p.E ? logit(64 * v + lane) : NONE;
+  for (int v = 0; v < VPL; ++v) {
+    const int e = LANES * v + lane;
+    const double x = logit(e < p.E ? e : 0);
+    z[v] = e < p.E ? x : NONE;
+  }
   double top = 0.0, sum = 1.0;     // of softmax over all experts, where that is asked for
   if (p.scoring == IQP_SCORE_SOFTMAX && (p.bias || !p.renormalize)) {
     top = NONE;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) top = z[v] > top ? z[v] : top;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) {
+    for (int d = LANES / 2; d; d >>= 1) {
       const double o = __shfl_xor(top, d);
       top = o > top ? o : top;
     }
     sum = 0.0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) sum += z[v] == NONE ? 0.0 : exp(z[v] - top);
-    sum = wave_sum(sum);
+    sum = lanes_sum<LANES>(sum);
   }
   uint64_t key[VPL];
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    const int e = 64 * v + lane;
+    const int e = LANES * v + lane;
     double c = z[v];
-    if (p.bias && e < p.E && c != NONE)
-      c = (p.scoring == IQP_SCORE_SOFTMAX ? exp(c - top) / sum : score_of(c, p.scoring)) + (double)p.bias[e];
-    key[v] = e < p.E ? order_of(c) : 0;
+    if (p.bias) {
+      const double b = (double)p.bias[e < p.E ? e : 0];
+      c = c == NONE ? NONE : (p.scoring == IQP_SCORE_SOFTMAX ? exp(c - top) / sum : score_of(c, p.scoring)) + b;
+    }
+    key[v] = e < p.E ? key_of(c, e) : 0;
   }
-  int mine = 0;      // lane j: the j-th expert
+  uint64_t mine = 0, first = 0;      // lane j: the j-th choice
   for (int j = 0; j < p.top; ++j) {
     uint64_t best = key[0];
-    int at = 0;
 #pragma unroll
-    for (int v = 1; v < VPL; ++v)
-      if (key[v] > best) {
-        best = key[v];
-        at = v;
-      }
-    const uint64_t most = wave_max(best);
-    uint64_t who = __ballot(best == most);
-    int e = 64 * at + lane, lead = __ffsll((unsigned long long)who) - 1;
-    // lanes with the same choice: the lowest index has the lowest v, then the lowest lane
-    for (uint64_t rest = who & (who - 1); rest; rest &= rest - 1) {
-      const int other = __ffsll((unsigned long long)rest) - 1;
-      if (__builtin_amdgcn_readlane(at, other) < __builtin_amdgcn_readlane(at, lead)) lead = other;
-    }
-    e = __builtin_amdgcn_readlane(e, lead);
-    if (lane == lead)
+    for (int v = 1; v < VPL; ++v) best = key[v] > best ? key[v] : best;
+    best = lanes_max<LANES>(best);
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) key[v] = v == at ? 0 : key[v];
-    mine = lane == j ? e : mine;
+    for (int v = 0; v < VPL; ++v) key[v] = key[v] == best ? 0 : key[v];
+    first = j == 0 ? best : first;
+    mine = lane == j ? best : mine;
   }
+  const int e = lane < p.top ? expert_of(mine) : 0;
+  const double zs = p.bias ? logit(e) : logit_of(mine);
   double w = 0.0;
-  const double zs = logit(mine);
   if (p.scoring == IQP_SCORE_SOFTMAX) {
-    if (!p.bias && p.renormalize) {
-      const double first = __shfl(zs, 0);      // the largest logit
-      w = zs == NONE ? 0.0 : exp(zs - first);
-    } else {
-      w = zs == NONE ? 0.0 : exp(zs - top) / sum;
-    }
+    const bool chosen = !p.bias && p.renormalize;      // relative to the largest chosen one alone
+    w = zs == NONE ? 0.0 : exp(zs - (chosen ? logit_of(first) : top)) / (chosen ? 1.0 : sum);
   } else {
     w = score_of(zs, p.scoring);
   }
   w = lane < p.top ? w : 0.0;
   if (p.renormalize) {
-    const double total = wave_sum(w);
+    const double total = lanes_sum<LANES>(w);
     w = total == 0.0 ? 0.0 : w / total;
   }
   if (lane < p.top) {
     p.weights[m * p.top + lane] = (float)(w * (double)p.scale);
-    p.experts[m * p.top + lane] = mine;
+    p.experts[m * p.top + lane] = e;
   }
 }
 
@@ -167,6 +180,7 @@ void group_count_kernel(GroupRowsArgs p) {
 __global__ __launch_bounds__(SORT_THREADS)
 void group_place_kernel(GroupRowsArgs p) {
   __shared__ int at[SORT_WAVES * MAX_GROUPS];
+  __shared__ int counted[2 * MAX_GROUPS];
   __shared__ int sums[SORT_WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t first = (int64_t)blockIdx.x * p.chunk, end = first + p.chunk < p.R ? first + p.chunk : p.R;
@@ -181,15 +195,32 @@ void group_place_kernel(GroupRowsArgs p) {
   __syncthreads();
   // thread g: its group's entries before this chunk, and in all
   int before = 0, all = 0;
+  if (!p.counts && gridDim.x > 1) {
+    for (int g = tid; g < p.G; g += SORT_THREADS) counted[g] = counted[MAX_GROUPS + g] = 0;
+    __syncthreads();
+    for (int64_t i = tid; i < p.R; i += SORT_THREADS) {
+      const int g = group_of(p, i);
+      if (g < p.G) atomicAdd(&counted[i < first ? g : MAX_GROUPS + g], 1);
+    }
+    __syncthreads();
+  }
   if (tid < p.G) {
     if (gridDim.x == 1) {
 #pragma unroll
       for (int w = 0; w < SORT_WAVES; ++w) all += at[w * p.G + tid];
+    } else if (!p.counts) {
+      before = counted[tid];
+      all = before + counted[MAX_GROUPS + tid];
     } else {
-      for (unsigned c = 0; c < gridDim.x; ++c) {
-        const int n = p.counts[(int64_t)c * p.G + tid];
-        before += c < blockIdx.x ? n : 0;
-        all += n;
+      for (unsigned c0 = 0; c0 < gridDim.x; c0 += 16) {      // (16 loads at a time)
+        int n[16];
+#pragma unroll
+        for (unsigned c = 0; c < 16; ++c) n[c] = p.counts[(int64_t)(c0 + c < gridDim.x ? c0 + c : 0) * p.G + tid];
+#pragma unroll
+        for (unsigned c = 0; c < 16; ++c) {
+          before += c0 + c < blockIdx.x ? n[c] : 0;
+          all += c0 + c < gridDim.x ? n[c] : 0;
+        }
       }
     }
   }
@@ -279,13 +310,22 @@ void moe_combine_kernel(MoeCombineArgs p) {
 }  // namespace
 
 hipError_t launch_moe_route(const MoeRouteArgs& p, hipStream_t stream) {
-  const int64_t blocks = (p.M + 3) / 4;
+  // A wave a token takes less time where tokens are few, a row of 16 lanes fewer
+  // instructions (us, wave / row, with a bias: 64 experts, 1024 tokens 3.9 / 4.7, 4632
+  // 7.7 / 5.3; 256 experts, 4632 tokens 9.0 / 13.6, 16384 22.3 / 20.6).
+  const bool rows = p.E <= 256 && p.top <= 16 && p.M >= 40 * (int64_t)p.E;
+  const int64_t blocks = rows ? (p.M + 15) / 16 : (p.M + 3) / 4;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const auto kern = p.E <= 64    ? moe_route_kernel<1>
-                    : p.E <= 128 ? moe_route_kernel<2>
-                    : p.E <= 256 ? moe_route_kernel<4>
-                    : p.E <= 512 ? moe_route_kernel<8>
-                                 : moe_route_kernel<16>;
+  const auto kern = rows ? (p.E <= 16    ? moe_route_kernel<16, 1>
+                            : p.E <= 32  ? moe_route_kernel<16, 2>
+                            : p.E <= 64  ? moe_route_kernel<16, 4>
+                            : p.E <= 128 ? moe_route_kernel<16, 8>
+                                         : moe_route_kernel<16, 16>)
+                    : p.E <= 64  ? moe_route_kernel<64, 1>
+                    : p.E <= 128 ? moe_route_kernel<64, 2>
+                    : p.E <= 256 ? moe_route_kernel<64, 4>
+                    : p.E <= 512 ? moe_route_kernel<64, 8>
+                                 : moe_route_kernel<64, 16>;
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
@@ -296,11 +336,20 @@ int64_t group_rows_chunk(int64_t R) {
   return share <= 2048 ? 2048 : (share + SORT_THREADS - 1) / SORT_THREADS * SORT_THREADS;
 }
 
+// Chunks that a launch of their own counts; 0 where every workgroup counts all
+// entries itself (us, itself / a launch: 4096 entries of 256 groups 6.0 / 7.4, 8192
+// 6.9 / 7.6, 16384 8.5 / 7.8, 37056 12.3 / 8.5).
+int64_t group_rows_counts(int64_t R) {
+  const int64_t chunk = group_rows_chunk(R), chunks = (R + chunk - 1) / chunk;
+  return chunks > 4 ? chunks : 0;
+}
+
 hipError_t launch_group_rows(GroupRowsArgs p, hipStream_t stream) {
   p.chunk = group_rows_chunk(p.R);
   int64_t chunks = (p.R + p.chunk - 1) / p.chunk;
   if (chunks < 1) chunks = 1;
-  if (chunks > 1) {
+  if (group_rows_counts(p.R) == 0) p.counts = nullptr;
+  if (p.counts) {
     hipLaunchKernelGGL(group_count_kernel, dim3((unsigned)chunks), dim3(SORT_THREADS), 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

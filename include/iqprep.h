@@ -795,7 +795,8 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
  * p_e + bias_e, the lower index first where these are equal, and
  *   weight = scale * p_e / (sum of p over the chosen ones if renormalize, else 1).
  * All in float64 and rounded to float32 once, so that the choice depends on no
- * rounding of an exponential. An expert whose logit is -inf comes after all others
+ * rounding of an exponential; sums p_e + bias_e whose first 42 mantissa bits agree
+ * count as equal. An expert whose logit is -inf comes after all others
  * and has weight 0; a token all of whose logits are -inf gets experts 0 ..
  * top_k - 1 with weights 0. A NaN or +inf logit makes the token's weights NaN; the
  * experts are distinct and in range all the same.
