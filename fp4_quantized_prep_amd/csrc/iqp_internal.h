@@ -368,7 +368,8 @@ struct Fp8GroupedArgs {
   int32_t* q_scales;        // packed UE8M0 words, strides in words
   int64_t qs_sm, qs_sw;
   int32_t parts;            // set by the launcher: workgroups of a tile's rows,
-  uint32_t chunk;           // consecutive ones to an XCD
+  uint32_t chunk;           // consecutive ones to an XCD,
+  bool large_first;         // the order of the tiles
 };
 hipError_t launch_fp8_grouped(Fp8GroupedArgs args, hipStream_t stream);
 

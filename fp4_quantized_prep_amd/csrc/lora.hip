@@ -43,7 +43,7 @@ template <int RT, int NST>
 __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
   constexpr int PITCH = 16 * RT + 4, STAGE = shrink_stage<RT>(), NCOPY = 2 * (1 + RT);
   static_assert(4 * SHRINK_ROWS * PITCH <= NST * STAGE, "a wave's sums, in its ring's place");
-  const groups::Tile t = groups::find_tile(p.groups, SHRINK_ROWS, p.splits, groups::item_of(blockIdx.x, 1));
+  const groups::Tile t = groups::find_tile(p.groups, SHRINK_ROWS, p.splits, groups::item_of(blockIdx.x, 1), groups::BY_PART);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -192,7 +192,7 @@ void lora_expand_kernel(LoraArgs p) {
   constexpr int PITCH = 68, HP = 64 * KT + 8;      // of a product's row (floats), of h's two parts (bf16)
   __shared__ __attribute__((aligned(16))) float lds[4 * 16 * PITCH];
   __shared__ __attribute__((aligned(16))) __bf16 parts[LORA_ROWS * HP];
-  const groups::Tile t = groups::find_tile<true>(p.groups, LORA_ROWS, p.parts, groups::item_of(blockIdx.x, 1));
+  const groups::Tile t = groups::find_tile(p.groups, LORA_ROWS, p.parts, groups::item_of(blockIdx.x, 1), groups::BY_TILE);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -27,41 +27,52 @@ struct Tile {
   int group, begin, rows, part;
 };
 
+// The order of the tiles: group by group, and within a group
+//   BY_PART     part by part, its tiles innermost: neighbours share weights;
+//   BY_TILE     tile by tile: neighbours share rows;
+//   LARGE_FIRST as BY_PART, but all groups' whole tiles first, then those of more
+//               than tm / 2 rows, then the others: few tiles end together.
+enum Order { BY_PART, BY_TILE, LARGE_FIRST };
+
 // Tile number `item`, where every group's rows are cut into tiles of tm (the
-// last one shorter) and each tile has `parts` parts; a group's items follow one
-// another part by part, its tiles innermost, so that neighbours share weights, or
-// (TILE_BY_TILE) tile by tile, so that they share rows.
-// All lanes of all waves call it and get the same answer. Offsets are kept
-// inside [0, R] whatever they hold. 256 groups a round of loads.
-template <bool TILE_BY_TILE = false>
-__device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts, int64_t item) {
+// last one shorter) and each tile has `parts` parts. All lanes of all waves call it
+// and get the same answer. Offsets are kept inside [0, R] whatever they hold. 256
+// groups a round of loads.
+__device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts, int64_t item, Order order) {
   const int lane = threadIdx.x & 63;
   int64_t done = 0;
-  for (int g0 = 0; g0 < g.G; g0 += 256) {
-    int begin[4], end[4];
+  for (int pass = 0; pass < (order == LARGE_FIRST ? 3 : 1); ++pass)
+    for (int g0 = 0; g0 < g.G; g0 += 256) {
+      int begin[4], end[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e = g0 + 64 * q + lane, c = e < g.G ? e : g.G - 1;
-      begin[q] = g.offsets[c];
-      end[q] = e < g.G ? g.offsets[c + 1] : 0;
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int b = clamp_place(g, begin[q]), n = clamp_place(g, end[q]) - b;
-      const int tiles = n > 0 ? (int)(((unsigned)n + tm - 1) / (unsigned)tm) : 0;
-      const int upto = wave_scan(tiles);
-      const int total = __builtin_amdgcn_readlane(upto, 63);
-      if (item < (done + total) * parts) {
-        const int at = 63 - __builtin_clzll(__ballot((done + upto - tiles) * parts <= item));
-        const int mine = __builtin_amdgcn_readlane(tiles, at);
-        const int local = (int)(item - (done + __builtin_amdgcn_readlane(upto, at) - mine) * parts);
-        const int part = TILE_BY_TILE ? local % parts : local / mine, t = TILE_BY_TILE ? local / parts : local - part * mine;
-        const int rows = __builtin_amdgcn_readlane(n, at) - t * tm;
-        return {g0 + 64 * q + at, __builtin_amdgcn_readlane(b, at) + t * tm, rows < tm ? rows : tm, part};
+      for (int q = 0; q < 4; ++q) {
+        const int e = g0 + 64 * q + lane, c = e < g.G ? e : g.G - 1;
+        begin[q] = g.offsets[c];
+        end[q] = e < g.G ? g.offsets[c + 1] : 0;
       }
-      done += total;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int b = clamp_place(g, begin[q]), n = clamp_place(g, end[q]) - b > 0 ? clamp_place(g, end[q]) - b : 0;
+        const int whole = (int)((unsigned)n / (unsigned)tm), rest = n - whole * tm;
+        int tiles = whole + (rest > 0 ? 1 : 0), t0 = 0;
+        if (order == LARGE_FIRST) {
+          t0 = pass ? whole : 0;
+          tiles = pass == 0 ? whole : (pass == 1 ? rest > tm / 2 : rest > 0 && rest <= tm / 2) ? 1 : 0;
+        }
+        const int upto = wave_scan(tiles);
+        const int total = __builtin_amdgcn_readlane(upto, 63);
+        if (item < (done + total) * parts) {
+          const int at = 63 - __builtin_clzll(__ballot((done + upto - tiles) * parts <= item));
+          const int mine = __builtin_amdgcn_readlane(tiles, at);
+          const int local = (int)(item - (done + __builtin_amdgcn_readlane(upto, at) - mine) * parts);
+          const int part = order == BY_TILE ? local % parts : local / mine;
+          const int t = __builtin_amdgcn_readlane(t0, at) + (order == BY_TILE ? local / parts : local - part * mine);
+          const int rows = __builtin_amdgcn_readlane(n, at) - t * tm;
+          return {g0 + 64 * q + at, __builtin_amdgcn_readlane(b, at) + t * tm, rows < tm ? rows : tm, part};
+        }
+        done += total;
+      }
     }
-  }
   return {0, 0, 0, 0};
 }
 
