@@ -846,7 +846,6 @@ int fp8_grouped_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_
   if (st != IQP_OK) return st;
   p.out = static_cast<uint16_t*>(out);
   p.ldo = ldo;
-  p.wide_out = aligned(out, 16) && ldo % 8 == 0;
   return from_hip(iqp::launch_fp8_grouped(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -939,7 +938,6 @@ int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, co
   p.out = static_cast<uint16_t*>(out);
   p.ldo = ldo;
   p.N = N;
-  p.wide_out = aligned(out, 16) && ldo % 8 == 0 && N % 8 == 0;
   p.h = static_cast<float*>(workspace);
   p.splits = iqp::lora_splits(M, G, K);
   return from_hip(iqp::launch_lora_add(p, static_cast<hipStream_t>(stream)));

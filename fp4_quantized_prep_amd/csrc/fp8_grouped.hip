@@ -311,7 +311,8 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     }
   } else {
     // through the wave's part of LDS, 32 places at a time, so that a store covers
-    // whole stretches of a row
+    // whole stretches of a row, 16 bytes a lane whatever its alignment; a row's last
+    // columns, fewer than eight, go one by one
     constexpr int PITCH = 64 * AN + 16, LANES = 4 * AN;   // bytes of a place's row; 16-byte pieces of it
     uint8_t* const mine = lds + wave * 32 * PITCH;
     const int64_t n0 = w.n0 + 32 * AN * wn;
@@ -331,25 +332,14 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
       }
       asm volatile("" ::: "memory");   // the wave's own writes, then its own reads: in order
       uint16_t* const to = p.out + (int64_t)(t.begin + m) * p.ldo + n0;
-      if (p.wide_out && rows_n == 32 * AN) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 64 / LANES) {
-          const int r = i + lane / LANES, c = lane % LANES;
-          const v4u v = *reinterpret_cast<const v4u*>(mine + r * PITCH + 16 * c);
-          if (r < rows_m) *reinterpret_cast<v4u*>(to + r * p.ldo + 8 * c) = v;
-        }
-      } else {
-        for (int r0 = 0; r0 < rows_m; r0 += 8) {      // eight rows' reads, then their stores
-          uint16_t v[8][AN / 2];
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int c = 0; c < AN / 2; ++c) v[r][c] = *reinterpret_cast<const uint16_t*>(mine + (r0 + r) * PITCH + 2 * (64 * c + lane));
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int c = 0; c < AN / 2; ++c)
-              if (r0 + r < rows_m && 64 * c + lane < rows_n) to[(r0 + r) * p.ldo + 64 * c + lane] = v[r][c];
+      for (int i = 0; i < 32; i += 64 / LANES) {
+        const int r = i + lane / LANES, c = 8 * (lane % LANES);
+        const v4u v = *reinterpret_cast<const v4u*>(mine + r * PITCH + 2 * c);
+        if (r < rows_m) {
+          if (c + 8 <= rows_n) *reinterpret_cast<groups::v4u_any*>(to + r * p.ldo + c) = v;
+          else
+            for (int e = 0; c + e < rows_n; ++e) to[r * p.ldo + c + e] = *reinterpret_cast<const uint16_t*>(mine + r * PITCH + 2 * (c + e));
         }
       }
       asm volatile("" ::: "memory");
@@ -505,8 +495,8 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
           const int64_t n = w.n0 + WR * wave + 16 * r + 4 * g;
           const uint32_t lo = layer::pack_bf16(acc[r][m][0], acc[r][m][1]), hi = layer::pack_bf16(acc[r][m][2], acc[r][m][3]);
           uint16_t* const to = p.out + (int64_t)(t.begin + 16 * m + col) * p.ldo + n;
-          if (p.wide_out && n + 4 <= p.N) {
-            *reinterpret_cast<layer::v2u*>(to) = layer::v2u{lo, hi};
+          if (n + 4 <= p.N) {
+            *reinterpret_cast<groups::v2u_any*>(to) = layer::v2u{lo, hi};
           } else {
             if (n < p.N) to[0] = (uint16_t)lo;
             if (n + 1 < p.N) to[1] = (uint16_t)(lo >> 16);

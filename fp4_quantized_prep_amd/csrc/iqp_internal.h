@@ -362,7 +362,6 @@ struct Fp8GroupedArgs {
   int32_t nkb;              // K / 128
   uint16_t* out;            // bf16 [R, N], row stride ldo elements, or
   int64_t ldo;
-  bool wide_out;            // 16-byte stores allowed (out and ldo aligned)
   uint8_t* q;               // SWIGLU: E4M3 [R, I], row stride ldq bytes (else NULL)
   int64_t ldq;
   int32_t* q_scales;        // packed UE8M0 words, strides in words
@@ -428,7 +427,6 @@ struct LoraArgs {
   int32_t rank;
   uint16_t* out;            // bf16 [M, N], row stride ldo
   int64_t ldo, N;
-  bool wide_out;            // 16-byte loads and stores allowed (out aligned, ldo and N multiples of 8)
   float* h;                 // workspace: [splits, R, lora_pitch(rank)]
   int32_t splits;           // lora_splits(R, G, K)
   int32_t h_pitch, parts;   // set by the launcher

@@ -183,10 +183,11 @@ __device__ __forceinline__ void split_h(const LoraArgs& p, const groups::Tile& t
 
 // out += s B h, 64 columns a wave. MFMA: rows of B as its rows, places as its
 // columns. The products pass through the wave's part of LDS, 16 places at a time,
-// so that loads and stores of out cover whole stretches of a row: 16 bytes a lane
-// (WIDE, where out's alignment allows it), else 2 bytes a lane. All old values are
+// so that loads and stores of out cover whole stretches of a row, 16 bytes a lane
+// whatever its alignment (a column a lane, for an odd stride, took 999x2115 17 us, so
+// TIME); a row's last columns, fewer than eight, go one by one. All old values are
 // asked for before anything is multiplied.
-template <int KT, bool WIDE>
+template <int KT>
 __global__ __launch_bounds__(256)
 void lora_expand_kernel(LoraArgs p) {
   constexpr int PITCH = 68, HP = 64 * KT + 8;      // of a product's row (floats), of h's two parts (bf16)
@@ -201,23 +202,18 @@ void lora_expand_kernel(LoraArgs p) {
   const int64_t n0 = (int64_t)t.part * LORA_COLS + 64 * wave;
   if (n0 >= p.N) return;
   float* const mine = lds + wave * 16 * PITCH;
-  // WIDE: 8 rows at a time, 8 columns a lane (N is a multiple of 8 where this is asked
-  // for: lanes past the last column leave the row); else a row and a column a lane
-  constexpr int TURNS = WIDE ? 2 : 16;
-  const int c = WIDE ? 8 * (lane & 7) : lane;
-  const bool in = n0 + c < p.N;
-  int64_t m[4][TURNS];
-  v4u wide[4][WIDE ? 2 : 1];
-  uint16_t narrow[4][WIDE ? 1 : 16];
+  // 8 rows at a time, 8 columns a lane, of which `cols` there are
+  const int c = 8 * (lane & 7), cols = p.N - n0 - c < 8 ? (int)(p.N - n0 - c) : 8;
+  int64_t m[4][2];
+  v4u old[4][2];
+  const bool any = p.N - n0 >= 8;      // lanes without eight columns ask for the first ones then, and drop them
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (16 * i < t.rows)
 #pragma unroll
-      for (int r = 0; r < TURNS; ++r) {
-        m[i][r] = row_of(p, t, 16 * i + (WIDE ? 8 * r + (lane >> 3) : r));
-        const uint16_t* const from = p.out + (m[i][r] < 0 ? 0 : m[i][r]) * p.ldo + n0 + (in ? c : 0);
-        if constexpr (WIDE) wide[i][r] = *reinterpret_cast<const v4u*>(from);
-        else narrow[i][r] = *from;
+      for (int r = 0; r < 2; ++r) {
+        m[i][r] = row_of(p, t, 16 * i + 8 * r + (lane >> 3));
+        if (any) old[i][r] = *reinterpret_cast<const groups::v4u_any*>(p.out + (m[i][r] < 0 ? 0 : m[i][r]) * p.ldo + n0 + (cols == 8 ? c : 0));
       }
   v4u b[KT][4];
 #pragma unroll
@@ -251,21 +247,22 @@ void lora_expand_kernel(LoraArgs p) {
     for (int q = 0; q < 4; ++q) *reinterpret_cast<v4f*>(mine + col * PITCH + 16 * q + 4 * g) = acc[q];
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int r = 0; r < TURNS; ++r) {
+    for (int r = 0; r < 2; ++r) {
+      if (m[i][r] < 0 || cols <= 0) continue;
       uint16_t* const to = p.out + m[i][r] * p.ldo + n0 + c;
-      if constexpr (WIDE) {
-        const float* const from = mine + (8 * r + (lane >> 3)) * PITCH + c;
+      const float* const from = mine + (8 * r + (lane >> 3)) * PITCH + c;
+      if (cols == 8) {
         const v4f lo = *reinterpret_cast<const v4f*>(from), hi = *reinterpret_cast<const v4f*>(from + 4);
-        const v4u o = wide[i][r];
+        const v4u o = old[i][r];
         v4u d;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float x = e < 2 ? lo[2 * e] : hi[2 * e - 4], y = e < 2 ? lo[2 * e + 1] : hi[2 * e - 3];
           d[e] = layer::pack_bf16(layer::bf16_lo(o[e]) + x, layer::bf16_hi(o[e]) + y);
         }
-        if (in && m[i][r] >= 0) *reinterpret_cast<v4u*>(to) = d;
+        *reinterpret_cast<groups::v4u_any*>(to) = d;
       } else {
-        if (in && m[i][r] >= 0) *to = (uint16_t)layer::pack_bf16(layer::bf16_lo(narrow[i][r]) + mine[r * PITCH + lane], 0.f);
+        for (int e = 0; e < cols; ++e) to[e] = (uint16_t)layer::pack_bf16(layer::bf16_lo(to[e]) + from[e], 0.f);
       }
     }
   }
@@ -299,9 +296,8 @@ hipError_t launch_lora_add(LoraArgs p, hipStream_t stream) {
   hipLaunchKernelGGL(first, dim3((unsigned)shrink), dim3(64 * SHRINK_WAVES), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const auto wide = p.rank <= 32 ? lora_expand_kernel<1, true> : p.rank <= 64 ? lora_expand_kernel<2, true> : lora_expand_kernel<4, true>;
-  const auto narrow = p.rank <= 32 ? lora_expand_kernel<1, false> : p.rank <= 64 ? lora_expand_kernel<2, false> : lora_expand_kernel<4, false>;
-  hipLaunchKernelGGL(p.wide_out ? wide : narrow, dim3((unsigned)expand), dim3(256), 0, stream, p);
+  const auto second = p.rank <= 32 ? lora_expand_kernel<1> : p.rank <= 64 ? lora_expand_kernel<2> : lora_expand_kernel<4>;
+  hipLaunchKernelGGL(second, dim3((unsigned)expand), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

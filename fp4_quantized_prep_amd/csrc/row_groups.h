@@ -8,6 +8,10 @@ namespace iqp {
 namespace {
 namespace groups {
 
+// 8 and 16 bytes at any even address: the card's vector memory takes them there too, in one access
+typedef unsigned v2u_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // inclusive sum over the 64 lanes
 __device__ __forceinline__ int wave_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8

@@ -905,8 +905,8 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
  *   offsets, rows, G   group_rows' of one adapter a token (R = M). Read on the device;
  *              offsets outside [0, M] are clamped, rows outside [0, M) left out. No
  *              row may be at two places (group_rows gives none).
- *   out        bf16 [M, N], row stride ldo, 2-byte aligned (16-byte accesses where it
- *              is 16-byte aligned and ldo and N multiples of 8). Must not overlap the others.
+ *   out        bf16 [M, N], row stride ldo, 2-byte aligned (fastest where 16-byte
+ *              aligned with ldo a multiple of 8). Must not overlap the others.
  *   workspace  lora_add_workspace_bytes(M, G, rank, K) bytes of device memory, 256-byte
  *              aligned; its contents do not matter before and mean nothing after.
  *              Calls that share one must not overlap.
