@@ -184,8 +184,8 @@ __device__ __forceinline__ void split_h(const LoraArgs& p, const groups::Tile& t
 // out += s B h, 64 columns a wave. MFMA: rows of B as its rows, places as its
 // columns. The products pass through the wave's part of LDS, 16 places at a time,
 // so that loads and stores of out cover whole stretches of a row, 16 bytes a lane
-// whatever its alignment (a column a lane, for an odd stride, took 999x2115 17 us, so
-// TIME); a row's last columns, fewer than eight, go one by one. All old values are
+// whatever its alignment (a column a lane, for an odd stride, took 999x2115 16 us, so
+// 10); a row's last columns, fewer than eight, go one by one. All old values are
 // asked for before anything is multiplied.
 template <int KT>
 __global__ __launch_bounds__(256)
@@ -197,24 +197,16 @@ void lora_expand_kernel(LoraArgs p) {
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  split_h<KT>(p, t, parts);
-  __syncthreads();
-  const int64_t n0 = (int64_t)t.part * LORA_COLS + 64 * wave;
-  if (n0 >= p.N) return;
-  float* const mine = lds + wave * 16 * PITCH;
-  // 8 rows at a time, 8 columns a lane, of which `cols` there are
-  const int c = 8 * (lane & 7), cols = p.N - n0 - c < 8 ? (int)(p.N - n0 - c) : 8;
-  int64_t m[4][2];
-  v4u old[4][2];
-  const bool any = p.N - n0 >= 8;      // lanes without eight columns ask for the first ones then, and drop them
+  // rows of the tile, 8 at a time: lane / 8; all asked for at once
+  int row[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (16 * i < t.rows)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        m[i][r] = row_of(p, t, 16 * i + 8 * r + (lane >> 3));
-        if (any) old[i][r] = *reinterpret_cast<const groups::v4u_any*>(p.out + (m[i][r] < 0 ? 0 : m[i][r]) * p.ldo + n0 + (cols == 8 ? c : 0));
-      }
+    for (int r = 0; r < 2; ++r) {
+      const int at = 16 * i + 8 * r + (lane >> 3);
+      row[i][r] = p.groups.rows[t.begin + (at < t.rows ? at : 0)];
+    }
+  const int64_t n0 = (int64_t)t.part * LORA_COLS + 64 * wave;
   v4u b[KT][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -225,6 +217,30 @@ void lora_expand_kernel(LoraArgs p) {
     for (int s = 0; s < KT; ++s)       // (past the rank h is zero)
       b[s][i] = *reinterpret_cast<const v4u*>(row + (32 * s + 8 * g < p.rank ? 32 * s + 8 * g : 0));
   }
+  split_h<KT>(p, t, parts);
+  __syncthreads();
+  if (n0 >= p.N) return;
+  float* const mine = lds + wave * 16 * PITCH;
+  // 8 columns a lane, of which `cols` there are
+  const int c = 8 * (lane & 7), cols = p.N - n0 - c < 8 ? (int)(p.N - n0 - c) : 8;
+  uint16_t* to[4][2];
+  bool kept[4][2];
+  v4u old[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int m = row[i][r];
+      const bool is = m >= 0 && m < p.M;
+      to[i][r] = p.out + (is ? m : 0) * p.ldo + n0 + (cols == 8 ? c : 0);
+      kept[i][r] = is && cols > 0 && 16 * i + 8 * r + (lane >> 3) < t.rows;
+    }
+  // (lanes without a row or eight columns ask for others, and drop them)
+  if (p.N - n0 >= 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) old[i][r] = *reinterpret_cast<const groups::v4u_any*>(to[i][r]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r0 = 16 * i;
@@ -248,8 +264,7 @@ void lora_expand_kernel(LoraArgs p) {
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      if (m[i][r] < 0 || cols <= 0) continue;
-      uint16_t* const to = p.out + m[i][r] * p.ldo + n0 + c;
+      if (!kept[i][r]) continue;
       const float* const from = mine + (8 * r + (lane >> 3)) * PITCH + c;
       if (cols == 8) {
         const v4f lo = *reinterpret_cast<const v4f*>(from), hi = *reinterpret_cast<const v4f*>(from + 4);
@@ -260,9 +275,9 @@ void lora_expand_kernel(LoraArgs p) {
           const float x = e < 2 ? lo[2 * e] : hi[2 * e - 4], y = e < 2 ? lo[2 * e + 1] : hi[2 * e - 3];
           d[e] = layer::pack_bf16(layer::bf16_lo(o[e]) + x, layer::bf16_hi(o[e]) + y);
         }
-        *reinterpret_cast<groups::v4u_any*>(to) = d;
+        *reinterpret_cast<groups::v4u_any*>(to[i][r]) = d;
       } else {
-        for (int e = 0; e < cols; ++e) to[e] = (uint16_t)layer::pack_bf16(layer::bf16_lo(to[e]) + from[e], 0.f);
+        for (int e = c; e < c + cols; ++e) to[i][r][e] = (uint16_t)layer::pack_bf16(layer::bf16_lo(to[i][r][e]) + from[e - c], 0.f);
       }
     }
   }

@@ -52,11 +52,12 @@ __device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts,
       for (int q = 0; q < 4; ++q) {
         const int e = g0 + 64 * q + lane, c = e < g.G ? e : g.G - 1;
         begin[q] = g.offsets[c];
-        end[q] = e < g.G ? g.offsets[c + 1] : 0;
+        end[q] = g.offsets[c + 1];
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int b = clamp_place(g, begin[q]), n = clamp_place(g, end[q]) - b > 0 ? clamp_place(g, end[q]) - b : 0;
+        const int b = clamp_place(g, begin[q]), d = clamp_place(g, end[q]) - b;
+        const int n = d > 0 && g0 + 64 * q + lane < g.G ? d : 0;
         const int whole = (int)((unsigned)n / (unsigned)tm), rest = n - whole * tm;
         int tiles = whole + (rest > 0 ? 1 : 0), t0 = 0;
         if (order == LARGE_FIRST) {
