@@ -81,3 +81,34 @@ def test_lora_workspace(gpu_lib):
     gpu_lib.lora_add(one, x.cuda(), a.cuda(), b.cuda(), gr, workspace=ws[:need])
     gpu_lib.lora_add(two, x.cuda(), a.cuda(), b.cuda(), gr)
     assert torch.equal(one, two) and bool((ws[need:] == 255).all())
+
+
+def test_lora_many_adapters(gpu_lib):
+    """More adapters than a round of the search for a tile looks at."""
+    g = gen(5)
+    counts = [int(c) for c in g.integers(0, 3, 600)]
+    counts[598] = 90
+    plan, out, x, a, b, s = case(g, counts, 7, 72, 136, 8)
+    want, tol = X.lora(out, x, a, b, plan[0], plan[1], s)
+    got = out.cuda()
+    gpu_lib.lora_add(got, x.cuda(), a.cuda(), b.cuda(), gpu_lib.RowGroups(*(t.cuda() for t in plan)), scales=s.cuda())
+    assert bool(((got.cpu().double() - want).abs() <= tol).all())
+
+
+def test_lora_bad_plan(gpu_lib):
+    """Offsets out of range or falling and rows that name no token: nothing else is
+    written, the good groups' rows are right."""
+    g = gen(6)
+    plan, out, x, a, b, s = case(g, [4, 30, 5, 0, 8], 0, 100, 64, 16)
+    M = out.shape[0]
+    rows = plan[1].clone()
+    rows[2], rows[3] = -9, 1 << 30
+    offsets = torch.tensor([-5, 4, 2, 2, 1 << 30, -(1 << 31)], dtype=torch.int32)
+    buf = torch.full((M + 20, 100), 5.0, dtype=torch.bfloat16, device="cuda")
+    buf[10:10 + M] = out.cuda()
+    gpu_lib.lora_add(buf[10:10 + M], x.cuda(), a.cuda(), b.cuda(), gpu_lib.RowGroups(offsets.cuda(), rows.cuda(), plan[2].cuda()), scales=s.cuda())
+    want, tol = X.lora(out, x, a, b, torch.tensor([0, 4, 4, 4, 4, 4]), rows, s)
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[rows[4:].long()] = False                  # (places of the group that begins past the last one)
+    assert bool(((buf[10:10 + M].cpu().double() - want).abs() <= tol)[keep].all())
+    assert bool((buf[:10] == 5.0).all()) and bool((buf[10 + M:] == 5.0).all())

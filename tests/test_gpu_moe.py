@@ -306,3 +306,71 @@ def test_combine_one_dim(gpu_lib):
     y, w = X.bf16(g, 6, 64), torch.ones(6)
     out = gpu_lib.moe_combine(y.cuda(), groups_on_gpu(gpu_lib, plan), w.cuda())
     assert torch.equal(out.cpu(), y[plan[2].long()])
+
+
+# ------------------------------------------------- the kernels' other variants
+
+@pytest.mark.parametrize("E,top", [(1, 1), (8, 8), (16, 3), (17, 16), (32, 4), (60, 6), (64, 8), (100, 16), (128, 4), (200, 5), (256, 8)])
+@pytest.mark.parametrize("scoring,bias,half", [("softmax", False, False), ("sigmoid", True, False), ("sqrt_softplus", True, True), ("softmax", True, False)])
+def test_route_many_tokens(gpu_lib, E, top, scoring, bias, half):
+    """Batches that go to the kernel of 16 lanes a token (and a token more than a
+    workgroup has), with masked experts, against the plain form on some rows and
+    the few tokens' kernel on all."""
+    print("route many", E, top, scoring, bias, half, flush=True)
+    g = gen(14, E, top)
+    M = 40 * E + 5
+    z = torch.from_numpy(g.standard_normal((M, E)).astype(np.float32) * 3)
+    z[::7, ::3] = -float("inf")
+    z[5] = -float("inf")
+    z = z.to(torch.bfloat16) if half else z
+    b = torch.from_numpy(g.standard_normal(E).astype(np.float32)) if bias else None
+    dev = dict(bias=None if b is None else b.cuda(), scoring=scoring, scale=0.75)
+    w, e = gpu_lib.moe_route(z.cuda(), top, **dev)
+    some = torch.cat((torch.arange(min(M, 64)), torch.arange(M - 20, M))).unique()
+    want, ids = X.route(z[some], top, b, scoring, True, 0.75)
+    assert torch.equal(e.cpu()[some], ids)
+    assert bool(((w.cpu()[some].double() - want).abs() <= 2.0 ** -24 * (1 + 2.0 ** -10) * want.abs() + 2.0 ** -149).all())
+    step = max(1, 40 * E - 1)
+    for lo in range(0, M, step):
+        few = gpu_lib.moe_route(z[lo:lo + step].cuda(), top, **dev)
+        assert torch.equal(few[1], e[lo:lo + step])
+        # (sums of the chosen scores are added up in another order)
+        assert bool(((few[0] - w[lo:lo + step]).abs() <= 2.0 ** -23 * w[lo:lo + step]).all())
+
+
+def test_grouped_many_tiles(gpu_lib):
+    """More groups than a round of the search for a tile looks at, and items enough
+    for the order by eight chunks."""
+    g = gen(15)
+    for G, N in ((1000, 300), (300, 4000)):
+        print("many tiles", G, N, flush=True)
+        counts = [int(c) for c in g.integers(0, 4, G)]
+        counts[G - 2] = 270
+        plan, a, ab, w, ws, src = operands(g, counts, 3, N, 128)
+        out = gpu_lib.fp8_grouped_gemm_1x128_128x128(a.cuda(), X.words_of(ab).cuda(), w.cuda(), ws.cuda(), groups_on_gpu(gpu_lib, plan))
+        y, bound = X.product(a, ab, w, ws, plan[0], src)
+        X.check_product(out.cpu(), y, bound)
+
+
+def test_grouped_long_k(gpu_lib):
+    """The longest K that is taken, with few rows and with a whole tile of them."""
+    g = gen(16)
+    for counts in ([3, 0, 1], [20, 260]):
+        print("long k", counts, flush=True)
+        plan, a, ab, w, ws, src = operands(g, counts, 0, 256, 32768)
+        out = gpu_lib.fp8_grouped_gemm_1x128_128x128(a.cuda(), X.words_of(ab).cuda(), w.cuda(), ws.cuda(), groups_on_gpu(gpu_lib, plan))
+        y, bound = X.product(a, ab, w, ws, plan[0], src)
+        X.check_product(out.cpu(), y, bound)
+
+
+def test_grouped_offset_start(gpu_lib):
+    """Places before the first group and between none: left as they were."""
+    g = gen(17)
+    plan, a, ab, w, ws, src = operands(g, [9, 20, 4], 0, 256, 256)
+    offsets = torch.tensor([5, 9, 29, 31], dtype=torch.int32)
+    out = torch.full((33, 256), 6.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.fp8_grouped_gemm_1x128_128x128(a.cuda(), X.words_of(ab).cuda(), w.cuda(), ws.cuda(),
+                                           gpu_lib.RowGroups(offsets.cuda(), plan[1].cuda(), plan[2].cuda()), out=out)
+    y, bound = X.product(a, ab, w, ws, offsets, src)
+    X.check_product(out.cpu(), y, bound)
+    assert bool((out[:5] == 6.0).all()) and bool((out[31:] == 6.0).all())
