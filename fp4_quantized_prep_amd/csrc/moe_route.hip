@@ -260,8 +260,9 @@ void group_place_kernel(GroupRowsArgs p) {
       const int base = at[wave * p.G + g];
       to = base + rank;
       if (rank == 0) at[wave * p.G + g] = base + __popcll(same);
-      p.rows[to] = (int)i;
+      if (to < p.R) p.rows[to] = (int)i;      // (always, unless another call writes to the workspace meanwhile)
     }
+    asm volatile("" ::: "memory");   // the wave's own writes, then its own reads: in order
     if (i < mine_end) {
       p.slots[i] = to;
       if (i >= total) p.rows[i] = -1;      // behind the last group
@@ -330,18 +331,19 @@ hipError_t launch_moe_route(const MoeRouteArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// entries of a workgroup: at most GROUP_CHUNKS of them
+// Entries of a workgroup, of which there are at most GROUP_CHUNKS. An entry a thread
+// (two: 1024 entries 4.6 us for 3.8, 16384 7.8 for 6.9).
 int64_t group_rows_chunk(int64_t R) {
   const int64_t share = (R + GROUP_CHUNKS - 1) / GROUP_CHUNKS;
-  return share <= 2048 ? 2048 : (share + SORT_THREADS - 1) / SORT_THREADS * SORT_THREADS;
+  return share <= 1024 ? 1024 : (share + SORT_THREADS - 1) / SORT_THREADS * SORT_THREADS;
 }
 
 // Chunks that a launch of their own counts; 0 where every workgroup counts all
-// entries itself (us, itself / a launch: 4096 entries of 256 groups 6.0 / 7.4, 8192
-// 6.9 / 7.6, 16384 8.5 / 7.8, 37056 12.3 / 8.5).
+// entries itself (us, itself / a launch, 256 groups: 2048 entries 4.5 / 5.8, 8192 5.8 /
+// 6.7, 12000 6.6 / 6.8, 16384 7.5 / 6.8).
 int64_t group_rows_counts(int64_t R) {
   const int64_t chunk = group_rows_chunk(R), chunks = (R + chunk - 1) / chunk;
-  return chunks > 4 ? chunks : 0;
+  return chunks > 8 ? chunks : 0;
 }
 
 hipError_t launch_group_rows(GroupRowsArgs p, hipStream_t stream) {

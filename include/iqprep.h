@@ -787,7 +787,7 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
 /*
  * moe_route — the top_k experts of every token and their weights.
  *
- * With z the logits of a token (NaN where it should not be: see below), and
+ * With z the logits of a token, and
  *   p_e = exp(z_e) / sum_f exp(z_f)      IQP_SCORE_SOFTMAX
  *         1 / (1 + exp(-z_e))            IQP_SCORE_SIGMOID
  *         sqrt(log(1 + exp(z_e)))        IQP_SCORE_SQRT_SOFTPLUS
@@ -798,8 +798,9 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
  * rounding of an exponential; sums p_e + bias_e whose first 42 mantissa bits agree
  * count as equal. An expert whose logit is -inf comes after all others
  * and has weight 0; a token all of whose logits are -inf gets experts 0 ..
- * top_k - 1 with weights 0. A NaN or +inf logit makes the token's weights NaN; the
- * experts are distinct and in range all the same.
+ * top_k - 1 with weights 0. A NaN logit comes before all others; it, and +inf under
+ * IQP_SCORE_SOFTMAX, make weights of the token NaN, of other tokens none. The experts
+ * of a token are distinct and in range whatever its logits hold.
  *
  *   logits   float32, or bf16 where logits_bf16 is not 0, [M, E], row stride ld
  *            (elements, >= E); 4- or 2-byte aligned. E 1 to 1024.
@@ -821,7 +822,8 @@ int moe_route(const void* logits, int64_t ld, int32_t logits_bf16, const float* 
  * is in no group: its slot is -1, and rows holds -1 from offsets[G] on.
  *
  *   index      int32 [R]: moe_route's experts [M, top_k], or an adapter a token.
- *   offsets    int32 [G + 1];  rows, slots  int32 [R]. G 1 to 1024.
+ *   offsets    int32 [G + 1];  rows, slots  int32 [R]. G 1 to 1024. None may overlap
+ *              another or index.
  *   workspace  group_rows_workspace_bytes(R, G) bytes of device memory, 4-byte
  *              aligned (NULL where that is 0); its contents do not matter before
  *              and mean nothing after. Calls that share one must not overlap.
@@ -854,11 +856,13 @@ int group_rows(const int32_t* index, int64_t R, int32_t G, int32_t* offsets, int
  *              the device; offsets outside [0, R] are clamped into it, rows that
  *              name no token read zeros. Places in no group are not computed.
  *   K          a multiple of 128, at most 32768;  I  a multiple of 128;  N  any.
- *   out        bf16 [R, N], row stride ldo, as there. Rows of no group are left as
- *              they were.
+ *   out        bf16 [R, N], row stride ldo (elements, >= N), 2-byte aligned (fastest
+ *              where 16-byte aligned with ldo a multiple of 8).
  *   q          E4M3 [R, I], row stride ldq (bytes, a multiple of 16), 16-byte
  *              aligned; q_scales packed words [R, ceil(I/512)] in either layout of
- *              fp8_quant_1x128_ue8m0. Rows of no group are left as they were.
+ *              fp8_quant_1x128_ue8m0.
+ *              Rows of no group are left as they were in all three, and none of them
+ *              may overlap the inputs.
  * R == 0, N == 0 or I == 0: no-op. The results must be finite in float32. The same
  * call gives the same bits; a place's last bit may depend on how many rows its
  * group has.
