@@ -6,6 +6,27 @@
 //   out = bf16(y), or, the weights' rows being I gates and I ups,
 //   h[i, c] = y_c / (1 + exp(-y_c)) y_(I + c), quantised in 1x128 blocks as
 //   fp8_quant_1x128_ue8m0 does, from the float32 values.
+//
+// A workgroup computes 256 weight rows (128 gates and their 128 ups, so that it
+// holds whole blocks of h) of one tile of at most 256 places. The host knows
+// neither how many rows a group has nor which groups have any, so every workgroup
+// looks its tile up in the offsets, and the body goes by the tile's rows: up to 16
+// the weights are streamed past them, each wave on its own; up to 64, 128, 192 and
+// 256 tiles of matrix-core products whose waves share operands in LDS.
+//
+// Up to about 32 rows a group the read of the weights bounds it (64 groups of 4096 x
+// 7168, 16 rows each: 313 us, 6.0 TB/s; 32: 319; 64: 328; 8 rows in 8 groups of 7168 x
+// 2048: 20 us, 5.8). Above, neither the read nor the products alone, but nearly their
+// sum: 300 us and 24 us for every 1000 rows (37056 rows in 64 groups: 1.15 ms, 1.88
+// PFLOP/s; of 768 rows each 2.2; the same with one group's weights for all 2.5, with
+// zeros for a 2.5, with both 2.9: the card lowers its clock under these products, and
+// weights from memory cost a sixth of the time). What did not help there: stages of
+// half a block, four deep (1214 us: requests of 64 bytes); weights asked into L2 two
+// blocks ahead (1213); a third stage for the weights of the 192-row tile; K blocks in
+// another order for each workgroup (643 us for 772 where a is zero and the weights are
+// shared, nothing with data); 8, 16, 64 or 128 tiles in a row to an XCD; eight waves of
+// 64 x 128 instead of four of 128 x 128 (512 tokens: 387 us for 367). A K of 2048 leaves
+// 7 us of a tile's 43 to its first loads and its stores.
 #include <type_traits>
 
 #include "iq_common.h"
@@ -66,13 +87,19 @@ __device__ __forceinline__ Weights weights_of(const Fp8GroupedArgs& p, const gro
   return w;
 }
 
-// the scale bytes of 128-row tile `tile` of the group's weights, 4 K blocks a lane
-__device__ __forceinline__ uint32_t scale_lanes(const Fp8GroupedArgs& p, const Weights& w, int64_t tile, int lane) {
+// The scale bytes of 128-row tile `tile` of the group's weights, 4 K blocks a lane:
+// asked for before the first copies, put together behind them.
+struct ScaleBytes {
+  uint8_t b[4];
+  __device__ __forceinline__ uint32_t lanes() const { return b[0] | b[1] << 8 | b[2] << 16 | (uint32_t)b[3] << 24; }
+};
+
+__device__ __forceinline__ ScaleBytes scale_bytes(const Fp8GroupedArgs& p, const Weights& w, int64_t tile, int lane) {
   const int64_t last = (p.N + 127) / 128 - 1;
   const uint8_t* const s = w.scales + (tile < last ? tile : last) * p.ld_ws;
-  uint32_t v = 0;
+  ScaleBytes v;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) v |= (uint32_t)s[4 * lane + b < p.nkb ? 4 * lane + b : 0] << (8 * b);
+  for (int b = 0; b < 4; ++b) v.b[b] = s[4 * lane + b < p.nkb ? 4 * lane + b : 0];
   return v;
 }
 
@@ -174,13 +201,14 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
   };
 
   // the weight scales of the first and the second half of the wave's rows
-  const uint32_t wsc0 = scale_lanes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : 32 * AN * wn)) / 128, lane);
-  const uint32_t wsc1 = EPI == SWIGLU ? scale_lanes(p, w, (p.N / 2 + w.n0) / 128, lane) : wsc0;
+  const ScaleBytes wb0 = scale_bytes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : 32 * AN * wn)) / 128, lane);
+  const ScaleBytes wb1 = EPI == SWIGLU ? scale_bytes(p, w, (p.N / 2 + w.n0) / 128, lane) : wb0;
 #pragma unroll
   for (int i = 0; i < NST; ++i)
 #pragma unroll
     for (int c = 0; c < NCOPY; ++c) copy(i, i, c);
   __builtin_amdgcn_sched_barrier(0);
+  const uint32_t wsc0 = wb0.lanes(), wsc1 = EPI == SWIGLU ? wb1.lanes() : wsc0;
 
   v16f acc[AN][AM];
 #pragma unroll
@@ -337,8 +365,10 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
         const int r = i + lane / LANES, c = 8 * (lane % LANES);
         const v4u v = *reinterpret_cast<const v4u*>(mine + r * PITCH + 2 * c);
         if (r < rows_m) {
-          if (c + 8 <= rows_n) *reinterpret_cast<groups::v4u_any*>(to + r * p.ldo + c) = v;
-          else
+          if (c + 8 <= rows_n) {
+            if (p.stream_out) __builtin_nontemporal_store(v, reinterpret_cast<groups::v4u_any*>(to + r * p.ldo + c));
+            else *reinterpret_cast<groups::v4u_any*>(to + r * p.ldo + c) = v;
+          } else
             for (int e = 0; c + e < rows_n; ++e) to[r * p.ldo + c + e] = *reinterpret_cast<const uint16_t*>(mine + r * PITCH + 2 * (c + e));
         }
       }
@@ -348,8 +378,8 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
 }
 
 // Stream body, for up to 16 MT places: the product is then a read of the
-// weights. Each wave owns 32 of the workgroup's 256 rows (SWIGLU: 16 gates and
-// their 16 ups) and walks all K blocks with an LDS ring of its own: no barrier
+// weights. Each wave owns 64 of the workgroup's 256 rows (SWIGLU: 32 gates and
+// their 32 ups) and walks all K blocks with an LDS ring of its own: no barrier
 // in the loop, only the wave's wait counts. 16x16x128 MFMA: weight rows as its
 // rows, places as its columns. Workgroups start the K blocks at different
 // places, as all rows lie at equal strides and would share memory channels.
@@ -401,11 +431,12 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(b + (WR + TOK) * KB), 4, (vs + 4 * (j >> 2) * (int)p.as_sw) | past, 0, 0, 0);
   };
 
-  const uint32_t wsc0 = scale_lanes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : WR * wave)) / 128, lane);
-  const uint32_t wsc1 = EPI == SWIGLU ? scale_lanes(p, w, (p.N / 2 + w.n0) / 128, lane) : wsc0;
+  const ScaleBytes wb0 = scale_bytes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : WR * wave)) / 128, lane);
+  const ScaleBytes wb1 = EPI == SWIGLU ? scale_bytes(p, w, (p.N / 2 + w.n0) / 128, lane) : wb0;
 #pragma unroll
   for (int st = 0; st < NST; ++st) copy(st, st);
   __builtin_amdgcn_sched_barrier(0);
+  const uint32_t wsc0 = wb0.lanes(), wsc1 = EPI == SWIGLU ? wb1.lanes() : wsc0;
 
   v4f acc[RT][MT];
 #pragma unroll
@@ -507,19 +538,17 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
   }
 }
 
-constexpr int lds_bytes() {
-  constexpr int stream = NW * 3 * stream_stage<1>(), tile = tile_bytes<2, 3>(), ring = stream > tile ? stream : tile;
-  static_assert(ring >= tile_bytes<1, 3>() && ring >= tile_bytes<2, 3>() && ring >= tile_bytes<3, 2>() && ring >= tile_bytes<4, 2>(), "LDS");
-  static_assert(ring <= 160 * 1024 && ring >= NW * 32 * (64 * AN + 16), "LDS");
-  return ring;
-}
+constexpr int STREAM_LDS = NW * 3 * stream_stage<1>(), TILE_LDS = tile_bytes<2, 3>();      // 126 and 146 KiB
+constexpr int LDS_BYTES = STREAM_LDS > TILE_LDS ? STREAM_LDS : TILE_LDS;
+static_assert(LDS_BYTES >= tile_bytes<1, 3>() && LDS_BYTES >= tile_bytes<3, 2>() && LDS_BYTES >= tile_bytes<4, 2>(), "LDS");
+static_assert(LDS_BYTES <= 160 * 1024 && LDS_BYTES >= NW * 32 * (64 * AN + 16), "LDS");
 
 // One tile a workgroup, by the body that its number of rows asks for: the host
 // does not know how many rows a group has.
 template <Epilogue EPI>
 __global__ __launch_bounds__(NW * 64)
 void fp8_grouped_kernel(Fp8GroupedArgs p) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[lds_bytes()];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
   const groups::Tile t = groups::find_tile(p.groups, 256, p.parts, groups::item_of(blockIdx.x, p.chunk), p.large_first ? groups::LARGE_FIRST : groups::BY_PART);
   if (t.rows <= 0) return;
   if (t.rows <= 16) stream_body<EPI, 1, 3>(p, t, lds);
@@ -536,7 +565,13 @@ hipError_t launch_fp8_grouped(Fp8GroupedArgs p, hipStream_t stream) {
   // at most so many tiles: whole ones, and one that is not for every group
   const int64_t tiles = p.groups.R / 256 + (p.groups.G < p.groups.R ? p.groups.G : p.groups.R);
   const int64_t items = tiles * p.parts;
+  // A CU's neighbours on its XCD share weights and rows where tiles are many (37056 rows,
+  // 64 groups of 4096 x 7168, us: 1 in a row 1216, 8 to 32 1160, 128 1199); with few of
+  // them every XCD has to get its part.
   p.chunk = items >= 2048 ? 32 : 1;
+  // An output that the caches cannot keep for its reader goes past them (531 MB, K
+  // 2048: 632 us for 644).
+  p.stream_out = p.groups.R * p.N * 2 > ((int64_t)256 << 20);
   // Where the CUs get about two tiles each, of which some may be whole ones, the
   // large ones come first (777 tokens, 4 of 40 experts, K 1536, us: N 2115 46 / 38);
   // with more of them the search for them costs more than it gives (512 tokens, 8 of

@@ -368,7 +368,8 @@ struct Fp8GroupedArgs {
   int64_t qs_sm, qs_sw;
   int32_t parts;            // set by the launcher: workgroups of a tile's rows,
   uint32_t chunk;           // consecutive ones to an XCD,
-  bool large_first;         // the order of the tiles
+  bool large_first;         // the order of the tiles,
+  bool stream_out;          // whether out's stores go past the caches
 };
 hipError_t launch_fp8_grouped(Fp8GroupedArgs args, hipStream_t stream);
 

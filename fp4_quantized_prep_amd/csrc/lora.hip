@@ -2,6 +2,11 @@
 //   out[m] += s_g B_g (A_g x[m]),  A_g [r, K], B_g [N, r], m's adapter g
 // in two launches: h = A_g x (the first kernel, cut along K where there are few
 // rows, each piece's sums kept apart in float32), then out += s_g B_g h.
+//
+// The second is bound by out's way from and to memory (4632x8192, rank 64: 34 us for
+// 30 at a copy's rate), the first by A's way from L2, once for every 16 rows (K 1536:
+// 9.4 us); few rows by two launches and what they wait for one after the other (64
+// tokens of 32 adapters, 1536x7168, rank 16: 4.2 and 4.5 us for 10 MB).
 #include "iq_common.h"
 #include "layer_common.h"
 #include "row_groups.h"

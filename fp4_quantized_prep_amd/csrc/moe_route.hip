@@ -176,7 +176,9 @@ void group_count_kernel(GroupRowsArgs p) {
 
 // Stable: an entry's place is the number of entries of lower groups, of its group
 // in chunks and waves before its own (the integer atomics add in any order), and
-// of its group before it in its wave.
+// of its group before it in its wave (found by comparing the bits of the 64 lanes'
+// groups). Bound by its few dependent steps: 8 entries 3.4 us, 2048 of 256 groups 4.5,
+// 37056 8.2 with the counts' launch, for 1.2 MB.
 __global__ __launch_bounds__(SORT_THREADS)
 void group_place_kernel(GroupRowsArgs p) {
   __shared__ int at[SORT_WAVES * MAX_GROUPS];
@@ -272,7 +274,9 @@ void group_place_kernel(GroupRowsArgs p) {
 
 // ------------------------------------------------------------ the weighted sum
 
-// 8 columns a thread; up to eight of the token's rows are loaded before any is added
+// 8 columns a thread; up to eight of the token's rows are loaded before any is added.
+// Bound by HBM: 4632 tokens of 8 rows of 7168 and a shared one, 664 MB, 129 us, as
+// fast as a copy; 16 tokens 4.4 us, most of it a launch.
 __global__ __launch_bounds__(256)
 void moe_combine_kernel(MoeCombineArgs p) {
   const int64_t m = blockIdx.x / p.parts;
