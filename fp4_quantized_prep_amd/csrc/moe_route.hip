@@ -188,42 +188,45 @@ void group_place_kernel(GroupRowsArgs p) {
   const int64_t first = (int64_t)blockIdx.x * p.chunk, end = first + p.chunk < p.R ? first + p.chunk : p.R;
   const int64_t share = ((p.chunk + SORT_THREADS - 1) / SORT_THREADS) * 64;      // entries of a wave
   const int64_t mine = first + wave * share, mine_end = mine + share < end ? mine + share : end;
+  // the wave's first entries (all that it has, up to 2^17 in all) and the counts are
+  // asked for before anything waits
+  const int own = mine + lane < mine_end ? group_of(p, mine + lane) : p.G;
+  // thread g: its group's entries before this chunk, and in all
+  int before = 0, all = 0;
+  if (p.counts && tid < p.G)
+    for (unsigned c0 = 0; c0 < gridDim.x; c0 += 16) {      // (16 loads at a time)
+      int n[16];
+#pragma unroll
+      for (unsigned c = 0; c < 16; ++c) n[c] = p.counts[(int64_t)(c0 + c < gridDim.x ? c0 + c : 0) * p.G + tid];
+#pragma unroll
+      for (unsigned c = 0; c < 16; ++c) {
+        before += c0 + c < blockIdx.x ? n[c] : 0;
+        all += c0 + c < gridDim.x ? n[c] : 0;
+      }
+    }
+  const bool count_all = !p.counts && gridDim.x > 1;
   for (int g = tid; g < SORT_WAVES * p.G; g += SORT_THREADS) at[g] = 0;
+  if (count_all)
+    for (int g = tid; g < p.G; g += SORT_THREADS) counted[g] = counted[MAX_GROUPS + g] = 0;
   __syncthreads();
-  for (int64_t i = mine + lane; i < mine_end; i += 64) {
+  if (own < p.G) atomicAdd(&at[wave * p.G + own], 1);
+  for (int64_t i = mine + 64 + lane; i < mine_end; i += 64) {
     const int g = group_of(p, i);
     if (g < p.G) atomicAdd(&at[wave * p.G + g], 1);
   }
-  __syncthreads();
-  // thread g: its group's entries before this chunk, and in all
-  int before = 0, all = 0;
-  if (!p.counts && gridDim.x > 1) {
-    for (int g = tid; g < p.G; g += SORT_THREADS) counted[g] = counted[MAX_GROUPS + g] = 0;
-    __syncthreads();
+  if (count_all)
     for (int64_t i = tid; i < p.R; i += SORT_THREADS) {
       const int g = group_of(p, i);
       if (g < p.G) atomicAdd(&counted[i < first ? g : MAX_GROUPS + g], 1);
     }
-    __syncthreads();
-  }
-  if (tid < p.G) {
-    if (gridDim.x == 1) {
-#pragma unroll
-      for (int w = 0; w < SORT_WAVES; ++w) all += at[w * p.G + tid];
-    } else if (!p.counts) {
+  __syncthreads();
+  if (tid < p.G && !p.counts) {
+    if (count_all) {
       before = counted[tid];
       all = before + counted[MAX_GROUPS + tid];
     } else {
-      for (unsigned c0 = 0; c0 < gridDim.x; c0 += 16) {      // (16 loads at a time)
-        int n[16];
 #pragma unroll
-        for (unsigned c = 0; c < 16; ++c) n[c] = p.counts[(int64_t)(c0 + c < gridDim.x ? c0 + c : 0) * p.G + tid];
-#pragma unroll
-        for (unsigned c = 0; c < 16; ++c) {
-          before += c0 + c < blockIdx.x ? n[c] : 0;
-          all += c0 + c < gridDim.x ? n[c] : 0;
-        }
-      }
+      for (int w = 0; w < SORT_WAVES; ++w) all += at[w * p.G + tid];
     }
   }
   const int upto = groups::wave_scan(all);
@@ -250,7 +253,7 @@ void group_place_kernel(GroupRowsArgs p) {
   const int bits = 32 - __builtin_clz(p.G);      // of 0 .. G
   for (int64_t i0 = mine; i0 < mine_end; i0 += 64) {
     const int64_t i = i0 + lane;
-    const int g = i < mine_end ? group_of(p, i) : p.G;
+    const int g = i0 == mine ? own : i < mine_end ? group_of(p, i) : p.G;
     uint64_t same = ~0ull;
     for (int b = 0; b < bits; ++b) {
       const uint64_t set = __ballot(g >> b & 1);
