@@ -223,8 +223,6 @@ void lora_expand_kernel(LoraArgs p) {
       b[s][i] = *reinterpret_cast<const v4u*>(row + (32 * s + 8 * g < p.rank ? 32 * s + 8 * g : 0));
   }
   split_h<KT>(p, t, parts);
-  __syncthreads();
-  if (n0 >= p.N) return;
   float* const mine = lds + wave * 16 * PITCH;
   // 8 columns a lane, of which `cols` there are
   const int c = 8 * (lane & 7), cols = p.N - n0 - c < 8 ? (int)(p.N - n0 - c) : 8;
@@ -246,6 +244,10 @@ void lora_expand_kernel(LoraArgs p) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) old[i][r] = *reinterpret_cast<const groups::v4u_any*>(to[i][r]);
+  // (LDS alone is waited for: the old values are still on their way)
+  __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
+  block_barrier();
+  if (n0 >= p.N) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r0 = 16 * i;
