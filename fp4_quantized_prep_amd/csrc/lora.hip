@@ -294,10 +294,12 @@ int64_t tiles_of(int64_t R, int32_t G, int rows) { return R / rows + (G < R ? G 
 
 }  // namespace
 
-// Pieces of K: enough that the first launch has 512 workgroups, of two steps a wave at least
+// Pieces of K: enough that the first launch has 256 workgroups, of two steps a wave at
+// least (us in all, 128 / 256 / 512 workgroups: 64 tokens of 32 adapters 8.1 / 7.6 / 7.8, 999
+// of 20 18.3 / 16.8 / 17.9, 1024 of 4 15.5 / 13.3 / 14.4: the second launch reads every piece)
 int lora_splits(int64_t R, int32_t G, int64_t K) {
   const int64_t tiles = tiles_of(R, G, SHRINK_ROWS), steps = (K + 63) / 64;
-  int64_t z = 512 / (tiles > 0 ? tiles : 1);
+  int64_t z = 256 / (tiles > 0 ? tiles : 1);
   if (z > steps / (2 * SHRINK_WAVES)) z = steps / (2 * SHRINK_WAVES);
   return z < 1 ? 1 : z > 8 ? 8 : (int)z;
 }
