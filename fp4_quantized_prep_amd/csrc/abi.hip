@@ -904,7 +904,7 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
 
 int64_t lora_add_workspace_bytes(int64_t M, int32_t G, int32_t rank, int64_t K) {
   if (M <= 0 || M > 0x7FFFFFFF || G <= 0 || G > iqp::MAX_GROUPS || rank < 8 || rank > 128 || K <= 0) return 0;
-  return iqp::lora_splits(M, G, K) * M * iqp::lora_pitch(rank) * 4;
+  return iqp::lora_splits(M, G, rank, K) * M * iqp::lora_pitch(rank) * 4;
 }
 
 int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, const void* b, const float* scales, int32_t rank,
@@ -939,7 +939,7 @@ int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, co
   p.ldo = ldo;
   p.N = N;
   p.h = static_cast<float*>(workspace);
-  p.splits = iqp::lora_splits(M, G, K);
+  p.splits = iqp::lora_splits(M, G, rank, K);
   return from_hip(iqp::launch_lora_add(p, static_cast<hipStream_t>(stream)));
 }
 

@@ -429,10 +429,10 @@ struct LoraArgs {
   uint16_t* out;            // bf16 [M, N], row stride ldo
   int64_t ldo, N;
   float* h;                 // workspace: [splits, R, lora_pitch(rank)]
-  int32_t splits;           // lora_splits(R, G, K)
+  int32_t splits;           // lora_splits(R, G, rank, K)
   int32_t h_pitch, parts;   // set by the launcher
 };
-int lora_splits(int64_t R, int32_t G, int64_t K);
+int lora_splits(int64_t R, int32_t G, int32_t rank, int64_t K);
 int lora_pitch(int32_t rank);
 hipError_t launch_lora_add(LoraArgs args, hipStream_t stream);
 

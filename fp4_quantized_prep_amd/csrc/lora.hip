@@ -16,7 +16,7 @@ namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int SHRINK_ROWS = 16, SHRINK_WAVES = 4;   // first launch: places and waves of a workgroup
+constexpr int SHRINK_WAVES = 4;   // first launch: waves of a workgroup
 constexpr int LORA_ROWS = 64;     // second launch: places of a workgroup
 constexpr int LORA_COLS = 256;    // output columns of a workgroup (four waves of 64)
 
@@ -34,21 +34,21 @@ __device__ __forceinline__ int64_t row_of(const LoraArgs& p, const groups::Tile&
   return r < t.rows && m >= 0 && m < p.M ? m : -1;
 }
 
-// h[z, place, i] = sum of A[g, i, k] x[m, k] over piece z of K, 16 places a
+// h[z, place, i] = sum of A[g, i, k] x[m, k] over piece z of K, 16 MT places a
 // workgroup. Its waves share out K in steps of 64 and stream them through LDS rings
 // of their own (rows of 128 bytes, 16-byte chunk c of row r at c ^ r % 8, so that
 // the operand reads meet distinct banks); their sums meet in LDS. 16x16x32 MFMA: rows
 // of A as its rows, places as its columns. Operands straight from memory would take
 // the address unit 64 cycles a load, a line for every lane, for the 16 of whole
 // lines (4632x64x1536: 17.5 us, so 9.4).
-template <int RT>
-constexpr int shrink_stage() { return 2048 * (1 + RT); }
+template <int MT, int RT>
+constexpr int shrink_stage() { return 2048 * (MT + RT); }
 
-template <int RT, int NST>
+template <int MT, int RT, int NST>
 __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
-  constexpr int PITCH = 16 * RT + 4, STAGE = shrink_stage<RT>(), NCOPY = 2 * (1 + RT);
-  static_assert(4 * SHRINK_ROWS * PITCH <= NST * STAGE, "a wave's sums, in its ring's place");
-  const groups::Tile t = groups::find_tile(p.groups, SHRINK_ROWS, p.splits, groups::item_of(blockIdx.x, 1), groups::BY_PART);
+  constexpr int PITCH = 16 * RT + 4, STAGE = shrink_stage<MT, RT>(), NCOPY = 2 * (MT + RT);
+  static_assert(4 * 16 * MT * PITCH <= NST * STAGE, "a wave's sums, in its ring's place");
+  const groups::Tile t = groups::find_tile(p.groups, 16 * MT, p.splits, groups::item_of(blockIdx.x, 1), groups::BY_PART);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -59,9 +59,9 @@ __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
   const rsrc_t ra = make_rsrc(p.a + (int64_t)t.group * p.rank * p.K, 2 * (uint64_t)p.rank * p.K);
   // copy c moves rows 8 c + lane / 8; rows that are none read zeros
   const int chunk = (lane & 7) ^ (lane >> 3 & 7);
-  uint32_t vx[2], va[2 * RT];
+  uint32_t vx[2 * MT], va[2 * RT];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < 2 * MT; ++c) {
     const int64_t m = row_of(p, t, 8 * c + (lane >> 3));
     vx[c] = m < 0 ? PAST : (uint32_t)(2 * (m * p.ldx + 8 * chunk));
   }
@@ -76,18 +76,20 @@ __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
     const uint32_t past = s < last ? 0 : PAST, tail = 64 * s + 8 * chunk < K ? past : PAST;
     uint8_t* const b = ring + st * STAGE;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 2 * MT; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(b + 1024 * c), 16, (vx[c] + 128 * s) | tail, 0, 0, 0);
 #pragma unroll
     for (int c = 0; c < 2 * RT; ++c)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + 1024 * (2 + c)), 16, (va[c] + 128 * s) | past, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + 1024 * (2 * MT + c)), 16, (va[c] + 128 * s) | past, 0, 0, 0);
   };
 #pragma unroll
   for (int st = 0; st < NST; ++st) copy(first + st * SHRINK_WAVES, st);
   __builtin_amdgcn_sched_barrier(0);
-  v4f acc[RT];
+  v4f acc[MT][RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int u = 0; u < MT; ++u)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[u][i] = v4f{0.f, 0.f, 0.f, 0.f};
   constexpr int WAIT = waitcnt_vm((NST - 1) * NCOPY);
   const int c0 = 128 * col + 16 * (g ^ (col & 7)), c1 = 128 * col + 16 * ((4 + g) ^ (col & 7));
   int st = 0;
@@ -95,13 +97,16 @@ __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
     __builtin_amdgcn_s_waitcnt(WAIT);
     asm volatile("" ::: "memory");
     const uint8_t* const b = ring + st * STAGE;
-    v4u fx[2], fa[RT][2];
-    fx[0] = *reinterpret_cast<const v4u*>(b + c0);
-    fx[1] = *reinterpret_cast<const v4u*>(b + c1);
+    v4u fx[MT][2], fa[RT][2];
+#pragma unroll
+    for (int u = 0; u < MT; ++u) {
+      fx[u][0] = *reinterpret_cast<const v4u*>(b + 2048 * u + c0);
+      fx[u][1] = *reinterpret_cast<const v4u*>(b + 2048 * u + c1);
+    }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      fa[i][0] = *reinterpret_cast<const v4u*>(b + 2048 * (1 + i) + c0);
-      fa[i][1] = *reinterpret_cast<const v4u*>(b + 2048 * (1 + i) + c1);
+      fa[i][0] = *reinterpret_cast<const v4u*>(b + 2048 * (MT + i) + c0);
+      fa[i][1] = *reinterpret_cast<const v4u*>(b + 2048 * (MT + i) + c1);
     }
     // the stage is read: refill it
     __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
@@ -112,14 +117,19 @@ __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(fa[i][h]), operand(fx[h]), acc[i], 0, 0, 0);
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+          acc[u][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(fa[i][h]), operand(fx[u][h]), acc[u][i], 0, 0, 0);
     st = st + 1 < NST ? st + 1 : 0;
   }
   __builtin_amdgcn_s_waitcnt(WAITCNT_VM0);
   __syncthreads();
   float* const part = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int i = 0; i < RT; ++i) *reinterpret_cast<v4f*>(part + (16 * wave + col) * PITCH + 16 * i + 4 * g) = acc[i];
+  for (int u = 0; u < MT; ++u)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) *reinterpret_cast<v4f*>(part + (16 * (MT * wave + u) + col) * PITCH + 16 * i + 4 * g) = acc[u][i];
   __syncthreads();
   float* const to = p.h + ((int64_t)t.part * p.groups.R + t.begin) * (16 * RT);
   for (int i = threadIdx.x; i < t.rows * 4 * RT; i += 64 * SHRINK_WAVES) {
@@ -127,7 +137,7 @@ __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
     v4f sum = *reinterpret_cast<const v4f*>(part + r * PITCH + c);
 #pragma unroll
     for (int w = 1; w < SHRINK_WAVES; ++w) {
-      const v4f v = *reinterpret_cast<const v4f*>(part + (16 * w + r) * PITCH + c);
+      const v4f v = *reinterpret_cast<const v4f*>(part + (16 * MT * w + r) * PITCH + c);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] += v[e];
     }
@@ -135,11 +145,11 @@ __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
   }
 }
 
-template <int RT, int NST>
+template <int MT, int RT, int NST>
 __global__ __launch_bounds__(64 * SHRINK_WAVES)
 void lora_shrink_kernel(LoraArgs p) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[SHRINK_WAVES * NST * shrink_stage<RT>()];
-  shrink<RT, NST>(p, lds);
+  __shared__ __attribute__((aligned(16))) uint8_t lds[SHRINK_WAVES * NST * shrink_stage<MT, RT>()];
+  shrink<MT, RT, NST>(p, lds);
 }
 
 // h of the tile's places, added up once for the workgroup and scaled, in two bf16
@@ -292,13 +302,20 @@ void lora_expand_kernel(LoraArgs p) {
 
 int64_t tiles_of(int64_t R, int32_t G, int rows) { return R / rows + (G < R ? G : R); }
 
+// Places of the first launch's workgroups: 32 for larger ranks where the tiles are many,
+// so that A comes from L2 half as often (us in all, 16 / 32: rank 64, 1536x7168, 4632
+// tokens of 8 adapters 38.2 / 30.0, 2048 23.9 / 20.4, 1024 16.5 / 17.6, 64 of 32 10.2 /
+// 11.5; rank 128, 4632 tokens 62.0 / 43.9; 8192x1536, rank 64, 4632 41.9 / 40.1, 2048 24.1 /
+// 25.1).
+int shrink_rows(int64_t R, int32_t G, int32_t rank) { return rank > 32 && tiles_of(R, G, 16) >= 128 ? 32 : 16; }
+
 }  // namespace
 
 // Pieces of K: enough that the first launch has 256 workgroups, of two steps a wave at
 // least (us in all, 128 / 256 / 512 workgroups: 64 tokens of 32 adapters 8.1 / 7.6 / 7.8, 999
 // of 20 18.3 / 16.8 / 17.9, 1024 of 4 15.5 / 13.3 / 14.4: the second launch reads every piece)
-int lora_splits(int64_t R, int32_t G, int64_t K) {
-  const int64_t tiles = tiles_of(R, G, SHRINK_ROWS), steps = (K + 63) / 64;
+int lora_splits(int64_t R, int32_t G, int32_t rank, int64_t K) {
+  const int64_t tiles = tiles_of(R, G, shrink_rows(R, G, rank)), steps = (K + 63) / 64;
   int64_t z = 256 / (tiles > 0 ? tiles : 1);
   if (z > steps / (2 * SHRINK_WAVES)) z = steps / (2 * SHRINK_WAVES);
   return z < 1 ? 1 : z > 8 ? 8 : (int)z;
@@ -309,14 +326,15 @@ int lora_pitch(int32_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <
 hipError_t launch_lora_add(LoraArgs p, hipStream_t stream) {
   p.h_pitch = lora_pitch(p.rank);
   p.parts = (int32_t)((p.N + LORA_COLS - 1) / LORA_COLS);
-  const int64_t shrink = (tiles_of(p.groups.R, p.groups.G, SHRINK_ROWS) * p.splits + 7) / 8 * 8;
+  const int64_t shrink = (tiles_of(p.groups.R, p.groups.G, shrink_rows(p.groups.R, p.groups.G, p.rank)) * p.splits + 7) / 8 * 8;
   const int64_t expand = (tiles_of(p.groups.R, p.groups.G, LORA_ROWS) * p.parts + 7) / 8 * 8;
   if (shrink > 0x7FFFFFFF || expand > 0x7FFFFFFF) return hipErrorInvalidValue;
-  // (LDS for two workgroups a CU up to rank 64)
-  const auto first = p.h_pitch == 16   ? lora_shrink_kernel<1, 4>
-                     : p.h_pitch == 32 ? lora_shrink_kernel<2, 3>
-                     : p.h_pitch == 64 ? lora_shrink_kernel<4, 2>
-                                       : lora_shrink_kernel<8, 2>;
+  // (16 places: LDS for two workgroups a CU up to rank 64)
+  const bool wide = shrink_rows(p.groups.R, p.groups.G, p.rank) == 32;
+  const auto first = p.h_pitch == 16   ? lora_shrink_kernel<1, 1, 4>
+                     : p.h_pitch == 32 ? lora_shrink_kernel<1, 2, 3>
+                     : p.h_pitch == 64 ? (wide ? lora_shrink_kernel<2, 4, 2> : lora_shrink_kernel<1, 4, 2>)
+                                       : (wide ? lora_shrink_kernel<2, 8, 2> : lora_shrink_kernel<1, 8, 2>);
   hipLaunchKernelGGL(first, dim3((unsigned)shrink), dim3(64 * SHRINK_WAVES), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -112,3 +112,14 @@ def test_lora_bad_plan(gpu_lib):
     keep[rows[4:].long()] = False                  # (places of the group that begins past the last one)
     assert bool(((buf[10:10 + M].cpu().double() - want).abs() <= tol)[keep].all())
     assert bool((buf[:10] == 5.0).all()) and bool((buf[10 + M:] == 5.0).all())
+
+
+def test_lora_many_rows_large_rank(gpu_lib):
+    """Batches whose first launch has 32 rows a workgroup, on both sides of its border."""
+    for counts, rank in (([1100, 37, 0, 900], 64), ([1900, 17], 40), ([2048], 128), ([2080, 1], 72)):
+        print("lora large", counts, rank, flush=True)
+        plan, out, x, a, b, s = case(gen(7, rank), counts, 5, 40, 200, rank)
+        want, tol = X.lora(out, x, a, b, plan[0], plan[1], s)
+        got = out.cuda()
+        gpu_lib.lora_add(got, x.cuda(), a.cuda(), b.cuda(), gpu_lib.RowGroups(*(t.cuda() for t in plan)), scales=s.cuda())
+        assert bool(((got.cpu().double() - want).abs() <= tol).all())
