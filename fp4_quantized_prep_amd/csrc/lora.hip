@@ -236,6 +236,9 @@ void lora_expand_kernel(LoraArgs p) {
   float* const mine = lds + wave * 16 * PITCH;
   // 8 columns a lane, of which `cols` there are
   const int c = 8 * (lane & 7), cols = p.N - n0 - c < 8 ? (int)(p.N - n0 - c) : 8;
+  // Lanes with fewer ask for the row's last eight and keep `cols` of them; lanes
+  // without a row or a column ask for others, and drop them.
+  const int64_t at = cols == 8 ? n0 + c : p.N - 8;
   uint16_t* to[4][2];
   bool kept[4][2];
   v4u old[4][2];
@@ -245,11 +248,10 @@ void lora_expand_kernel(LoraArgs p) {
     for (int r = 0; r < 2; ++r) {
       const int m = row[i][r];
       const bool is = m >= 0 && m < p.M;
-      to[i][r] = p.out + (is ? m : 0) * p.ldo + n0 + (cols == 8 ? c : 0);
+      to[i][r] = p.out + (is ? m : 0) * p.ldo + at;
       kept[i][r] = is && cols > 0 && 16 * i + 8 * r + (lane >> 3) < t.rows;
     }
-  // (lanes without a row or eight columns ask for others, and drop them)
-  if (p.N - n0 >= 8)
+  if (p.N >= 8)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -283,9 +285,9 @@ void lora_expand_kernel(LoraArgs p) {
     for (int r = 0; r < 2; ++r) {
       if (!kept[i][r]) continue;
       const float* const from = mine + (8 * r + (lane >> 3)) * PITCH + c;
+      const v4u o = old[i][r];
       if (cols == 8) {
         const v4f lo = *reinterpret_cast<const v4f*>(from), hi = *reinterpret_cast<const v4f*>(from + 4);
-        const v4u o = old[i][r];
         v4u d;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -293,8 +295,15 @@ void lora_expand_kernel(LoraArgs p) {
           d[e] = layer::pack_bf16(layer::bf16_lo(o[e]) + x, layer::bf16_hi(o[e]) + y);
         }
         *reinterpret_cast<groups::v4u_any*>(to[i][r]) = d;
+      } else if (p.N >= 8) {
+#pragma unroll
+        for (int e = 1; e < 8; ++e)
+          if (e >= 8 - cols) {
+            const float x = e & 1 ? layer::bf16_hi(o[e / 2]) : layer::bf16_lo(o[e / 2]);
+            to[i][r][e] = (uint16_t)layer::pack_bf16(x + from[e - (8 - cols)], 0.f);
+          }
       } else {
-        for (int e = c; e < c + cols; ++e) to[i][r][e] = (uint16_t)layer::pack_bf16(layer::bf16_lo(to[i][r][e]) + from[e - c], 0.f);
+        for (int e = 8 - cols; e < 8; ++e) to[i][r][e] = (uint16_t)layer::pack_bf16(layer::bf16_lo(to[i][r][e]) + from[e - (8 - cols)], 0.f);
       }
     }
   }
