@@ -65,7 +65,8 @@ __device__ __forceinline__ uint32_t source_row(const Fp8GroupedArgs& p, const gr
 
 // what the bodies read of a group's weights
 struct Weights {
-  rsrc_t rows[2];            // TO_BF16: 256 rows from n0 on, twice; SWIGLU: 128 gates, 128 ups
+  const uint8_t* base[2];    // TO_BF16: 256 rows from n0 on, twice; SWIGLU: 128 gates, 128 ups
+  uint64_t bytes;            // of each
   const uint8_t* scales;     // of the group
   int64_t n0;                // first row (SWIGLU: first channel)
 };
@@ -76,14 +77,10 @@ __device__ __forceinline__ Weights weights_of(const Fp8GroupedArgs& p, const gro
   const uint8_t* const base = p.w + t.group * p.ldwg;
   w.scales = p.w_scales + t.group * p.ld_wsg;
   w.n0 = (int64_t)t.part * (EPI == SWIGLU ? TN / 2 : TN);
-  if constexpr (EPI == SWIGLU) {
-    const uint64_t bytes = (uint64_t)(TN / 2 - 1) * p.ldw + (uint64_t)KB * p.nkb;
-    w.rows[0] = make_rsrc(base + w.n0 * p.ldw, bytes);
-    w.rows[1] = make_rsrc(base + (p.N / 2 + w.n0) * p.ldw, bytes);
-  } else {
-    const int64_t rows = p.N - w.n0 < TN ? p.N - w.n0 : TN;
-    w.rows[0] = w.rows[1] = make_rsrc(base + w.n0 * p.ldw, (uint64_t)(rows - 1) * p.ldw + (uint64_t)KB * p.nkb);
-  }
+  const int64_t rows = EPI == SWIGLU ? TN / 2 : p.N - w.n0 < TN ? p.N - w.n0 : TN;
+  w.base[0] = base + w.n0 * p.ldw;
+  w.base[1] = EPI == SWIGLU ? base + (p.N / 2 + w.n0) * p.ldw : w.base[0];
+  w.bytes = (uint64_t)(rows - 1) * p.ldw + (uint64_t)KB * p.nkb;
   return w;
 }
 
@@ -160,8 +157,8 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
   const Weights w = weights_of<EPI>(p, t);
   const int nkb = p.nkb;
   const int64_t nw = (nkb + 3) / 4;
-  const rsrc_t ra = make_rsrc(p.a, (uint64_t)(p.M - 1) * p.lda + (uint64_t)KB * nkb);
-  const rsrc_t rs = make_rsrc(p.a_scales, 4 * (uint64_t)((p.M - 1) * p.as_sm + (nw - 1) * p.as_sw + 1));
+  const uint64_t a_bytes = (uint64_t)(p.M - 1) * p.lda + (uint64_t)KB * nkb;
+  const uint64_t s_bytes = 4 * (uint64_t)((p.M - 1) * p.as_sm + (nw - 1) * p.as_sw + 1);
 
   // copies: slab i of this wave is LDS rows 8 (wave + NW i) + lane / 8
   uint32_t vw[WC], va[AC], vs;
@@ -184,19 +181,22 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     vs = src == PAST ? PAST : 4 * src * (uint32_t)p.as_sm;
   }
 
-  // copy c (0 .. NCOPY - 1) of block j into stage st
+  // Copy c (0 .. NCOPY - 1) of block j into stage st. Past the last block the buffers
+  // are of no bytes: the copies read zeros, with the offset left at 0.
   auto copy = [&](int j, int st, int c) __attribute__((always_inline)) {
-    const uint32_t past = j < nkb ? 0 : PAST;
+    const bool in = j < nkb;
+    const int at = in ? KB * j : 0;
     if (c < WC) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rows[c / (WC / 2)], (lds_void*)(lw + st * W_BYTES + SLAB * (wave + NW * c)), 16,
-                                               (vw[c] + KB * j) | past, 0, 0, 0);
+      const int h = c / (WC / 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(w.base[h], in ? w.bytes : 0), (lds_void*)(lw + st * W_BYTES + SLAB * (wave + NW * c)),
+                                               16, vw[c], at, 0, 0);
     } else if (c < WC + AC) {
       const int k = c - WC;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(la + st * A_BYTES + SLAB * (wave + NW * k)), 16,
-                                               (va[k] + KB * j) | past, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(p.a, in ? a_bytes : 0), (lds_void*)(la + st * A_BYTES + SLAB * (wave + NW * k)), 16,
+                                               va[k], at, 0, 0);
     } else {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(ls + st * S_BYTES + 256 * (wave % AM)), 4,
-                                               (vs + 4 * (j >> 2) * (int)p.as_sw) | past, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(p.a_scales, in ? s_bytes : 0), (lds_void*)(ls + st * S_BYTES + 256 * (wave % AM)), 4,
+                                               vs, in ? 4 * (j >> 2) * (int)p.as_sw : 0, 0, 0);
     }
   };
 
@@ -218,30 +218,27 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // Half-steps of 64. The places' operands of the next half are read one by one as
-  // the MFMAs are done with those of this one, the weights' before all of them. One
-  // barrier a block, behind the first MFMAs of its second half: by then every wave
-  // has read all of block j, whose stage is refilled, and block j + 1 has landed
-  // (only the NST - 2 blocks after it may be in flight).
+  // Half-steps of 64 columns. The next half's operands are read while this one's are
+  // multiplied: the weights' into registers of their own, the places' one by one as
+  // the MFMAs are done with them. One barrier a block, behind the first MFMAs of its
+  // second half: by then every wave has read all of block j, whose stage is refilled,
+  // and block j + 1 has landed (only the NST - 2 blocks after it may be in flight).
+  // With one wave a SIMD, what is not an MFMA has to fit beside one: reads and copies
+  // go between the MFMAs one at a time, and offsets are scalar (HOW MUCH).
   constexpr int WAIT = waitcnt_vm((NST - 2) * NCOPY);
   const int row = lane & 31, swz = (row >> 1) & 7;
   v8i fw[2][AN], fa[AM];
   uint32_t as_word[AM];
+  auto read = [&](const uint8_t* b, int kh) __attribute__((always_inline)) {
+    const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
+    return make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
+  };
   auto read_a = [&](int st, int kh, int u) __attribute__((always_inline)) {
-    const uint8_t* b = la + st * A_BYTES + KB * (32 * (2 * u + wm) + row);
-    const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
-    fa[u] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
+    fa[u] = read(la + st * A_BYTES + KB * (32 * (2 * u + wm) + row), kh);
   };
-  auto lds_row = [&](int i) __attribute__((always_inline)) {
-    return EPI == SWIGLU ? 128 * (i / (AN / 2)) + 32 * (AN / 2 * wn + i % (AN / 2)) : 32 * (AN * wn + i);
-  };
-  auto read_w = [&](int st, int kh) __attribute__((always_inline)) {
-    const int c0 = 16 * ((4 * kh + 2 * half) ^ swz), c1 = 16 * ((4 * kh + 2 * half + 1) ^ swz);
-#pragma unroll
-    for (int i = 0; i < AN; ++i) {
-      const uint8_t* b = lw + st * W_BYTES + KB * (lds_row(i) + row);
-      fw[kh][i] = make_v8i(*reinterpret_cast<const v4u*>(b + c0), *reinterpret_cast<const v4u*>(b + c1));
-    }
+  auto read_w = [&](int st, int kh, int i) __attribute__((always_inline)) {
+    const int r = EPI == SWIGLU ? 128 * (i / (AN / 2)) + 32 * (AN / 2 * wn + i % (AN / 2)) : 32 * (AN * wn + i);
+    fw[kh][i] = read(lw + st * W_BYTES + KB * (r + row), kh);
   };
   auto read_scale = [&](int st, int u) __attribute__((always_inline)) {
     as_word[u] = *reinterpret_cast<const uint32_t*>(ls + st * S_BYTES + 4 * (32 * (2 * u + wm) + row));
@@ -251,7 +248,8 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     __builtin_amdgcn_s_waitcnt(FIRST);
   }
   block_barrier();
-  read_w(0, 0);
+#pragma unroll
+  for (int i = 0; i < AN; ++i) read_w(0, 0, i);
 #pragma unroll
   for (int u = 0; u < AM; ++u) {
     read_scale(0, u);
@@ -259,41 +257,47 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
   }
   int st = 0;
   for (int j = 0; j < nkb; ++j) {
+    const int st1 = st + 1 < NST ? st + 1 : 0;
     const int ws[2] = {scale_of(wsc0, j), scale_of(wsc1, j)};
     int as[AM];
-    read_w(st, 1);
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < AM; ++u) {
       as[u] = (int)(as_word[u] >> (8 * (j & 3)));
 #pragma unroll
-      for (int i = 0; i < AN; ++i)
+      for (int i = 0; i < AN; ++i) {
         acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[0][i], fa[u], acc[i][u], 0, 0, 0, ws[i / (AN / 2)], 0, as[u]);
-      __builtin_amdgcn_sched_barrier(0);
-      read_a(st, 1, u);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    const int st1 = st + 1 < NST ? st + 1 : 0;
-#pragma unroll
-    for (int u = 0; u < AM; ++u) {
-#pragma unroll
-      for (int i = 0; i < AN; ++i)
-        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[1][i], fa[u], acc[i][u], 0, 0, 0, ws[i / (AN / 2)], 0, as[u]);
-      __builtin_amdgcn_sched_barrier(0);
-      if (u == 0) {
-        __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
-        __builtin_amdgcn_s_waitcnt(WAIT);
-        block_barrier();
-        read_w(st1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (u == 0) read_w(st, 1, i);
+        if (i == AN - 1) read_a(st, 1, u);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      read_scale(st1, u);
-      read_a(st1, 0, u);
-      // the copies one by one between the MFMAs: issued together they would hold
-      // the wave until the address unit has taken them all
-#pragma unroll
-      for (int c = NCOPY * u / AM; c < NCOPY * (u + 1) / AM; ++c) copy(j + NST, st, c);
-      __builtin_amdgcn_sched_barrier(0);
     }
+    // the slots behind the MFMAs of the second half, but for the first one's
+    constexpr int SLOTS = AN * AM - 1;
+#pragma unroll
+    for (int u = 0; u < AM; ++u)
+#pragma unroll
+      for (int i = 0; i < AN; ++i) {
+        acc[i][u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[1][i], fa[u], acc[i][u], 0, 0, 0, ws[i / (AN / 2)], 0, as[u]);
+        __builtin_amdgcn_sched_barrier(0);
+        const int slot = u * AN + i - 1;
+        if (slot == 0) {
+          __builtin_amdgcn_s_waitcnt(WAITCNT_LGKM0);
+          __builtin_amdgcn_s_waitcnt(WAIT);
+          block_barrier();
+        }
+        if (slot >= 0) {
+#pragma unroll
+          for (int c = NCOPY * slot / SLOTS; c < NCOPY * (slot + 1) / SLOTS; ++c) copy(j + NST, st, c);
+#pragma unroll
+          for (int k = AN * slot / SLOTS; k < AN * (slot + 1) / SLOTS; ++k) read_w(st1, 0, k);
+          if (i == AN - 1) {
+            read_scale(st1, u);
+            read_a(st1, 0, u);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     st = st1;
   }
 
@@ -394,6 +398,7 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Weights w = weights_of<EPI>(p, t);
   const int nkb = p.nkb;
+  const rsrc_t rw[2] = {make_rsrc(w.base[0], w.bytes), make_rsrc(w.base[1], w.bytes)};
   const int rot = (int)((unsigned)(t.part * 5 + t.group * 3) % (unsigned)nkb);
   const int64_t nw = (nkb + 3) / 4;
   const rsrc_t ra = make_rsrc(p.a, (uint64_t)(p.M - 1) * p.lda + (uint64_t)KB * nkb);
@@ -424,7 +429,7 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
     uint8_t* const b = ring + st * STAGE;
 #pragma unroll
     for (int c = 0; c < WC; ++c)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rows[c / (WC / 2)], (lds_void*)(b + SLAB * c), 16, (vw[c] + u) | past, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw[c / (WC / 2)], (lds_void*)(b + SLAB * c), 16, (vw[c] + u) | past, 0, 0, 0);
 #pragma unroll
     for (int c = 0; c < AC; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(b + WR * KB + SLAB * c), 16, (va[c] + u) | past, 0, 0, 0);
