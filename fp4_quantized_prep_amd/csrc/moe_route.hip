@@ -22,11 +22,6 @@ __device__ __forceinline__ uint64_t key_of(double v, int e) {
 
 __device__ __forceinline__ int expert_of(uint64_t key) { return 1023 - (int)(key & 1023); }
 
-// the logit that a key was made of
-__device__ __forceinline__ double logit_of(uint64_t key) {
-  return __longlong_as_double((long long)(key >> 63 ? (key & ~1023ull) ^ 1ull << 63 : ~(key | 1023ull)));
-}
-
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
   const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
@@ -74,70 +69,128 @@ __device__ __forceinline__ double score_of(double z, int scoring) {
 // LANES lanes a token, expert LANES v + lane its lane's v-th value. Scores and
 // choices are float64, so that which expert is taken does not hang on how an
 // exponential is rounded. Bound by its instructions: 256 experts, top 8, with a bias:
-// 4.5 us for a token (2.5 of it a launch), 9.1 for 4632, whose logits' read takes 1.
+// 4.4 us for a token (2.5 of it a launch), 8.5 for 4632 (2 of it the scores, 2.5 the
+// choice), whose logits' read takes 1; 1024 experts 10.7 and 25.
 template <int LANES, int VPL>
 __global__ __launch_bounds__(256)
 void moe_route_kernel(MoeRouteArgs p) {
   const int lane = threadIdx.x & (LANES - 1);
   const int64_t m = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
   if (m >= p.M) return;
-  const auto logit = [&](int e) __attribute__((always_inline)) {
-    return p.half ? (double)__uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.logits)[m * p.ld + e] << 16)
-                  : (double)reinterpret_cast<const float*>(p.logits)[m * p.ld + e];
-  };
-  const double NONE = -__builtin_inf();
-  double z[VPL];
+  const float NONE = -__builtin_inff();
+  // every load before anything waits: expert LANES v + lane, or the first one again
+  float z[VPL], b[VPL] = {};
+  if (p.half) {
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int e = LANES * v + lane;
-    const double x = logit(e < p.E ? e : 0);
-    z[v] = e < p.E ? x : NONE;
+    for (int v = 0; v < VPL; ++v) {
+      const int e = LANES * v + lane;
+      z[v] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.logits)[m * p.ld + (e < p.E ? e : 0)] << 16);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int e = LANES * v + lane;
+      z[v] = reinterpret_cast<const float*>(p.logits)[m * p.ld + (e < p.E ? e : 0)];
+    }
   }
+  if (p.bias) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) b[v] = p.bias[LANES * v + lane < p.E ? LANES * v + lane : 0];
+  }
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) z[v] = LANES * v + lane < p.E ? z[v] : NONE;
   double top = 0.0, sum = 1.0;     // of softmax over all experts, where that is asked for
   if (p.scoring == IQP_SCORE_SOFTMAX && (p.bias || !p.renormalize)) {
-    top = NONE;
+    float t = NONE;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) top = z[v] > top ? z[v] : top;
+    for (int v = 0; v < VPL; ++v) t = z[v] > t ? z[v] : t;
 #pragma unroll
     for (int d = LANES / 2; d; d >>= 1) {
-      const double o = __shfl_xor(top, d);
-      top = o > top ? o : top;
+      const float o = __shfl_xor(t, d);
+      t = o > t ? o : t;
     }
+    top = (double)t;
     sum = 0.0;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) sum += z[v] == NONE ? 0.0 : exp(z[v] - top);
+    for (int v = 0; v < VPL; ++v) sum += z[v] == NONE ? 0.0 : exp((double)z[v] - top);
     sum = lanes_sum<LANES>(sum);
   }
   uint64_t key[VPL];
+  double score[VPL];       // with a bias: of every expert, as the choice goes by it
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     const int e = LANES * v + lane;
-    double c = z[v];
+    double c = (double)z[v];
     if (p.bias) {
-      const double b = (double)p.bias[e < p.E ? e : 0];
-      c = c == NONE ? NONE : (p.scoring == IQP_SCORE_SOFTMAX ? exp(c - top) / sum : score_of(c, p.scoring)) + b;
+      score[v] = z[v] == NONE ? 0.0 : p.scoring == IQP_SCORE_SOFTMAX ? exp(c - top) / sum : score_of(c, p.scoring);
+      c = z[v] == NONE ? c : score[v] + (double)b[v];
     }
     key[v] = e < p.E ? key_of(c, e) : 0;
   }
-  uint64_t mine = 0, first = 0;      // lane j: the j-th choice
-  for (int j = 0; j < p.top; ++j) {
-    uint64_t best = key[0];
+  int mine = 0;      // lane j: the j-th choice
+  if constexpr (LANES == 64) {
+    // Upper halves alone, where one expert has the largest, as it nearly always
+    // is but for bf16 logits; else the lower ones of those that share it. (4632 tokens,
+    // top 8, without a bias, this way / whole keys throughout and a load after the other:
+    // 256 experts 6.6 / 7.1 us, bf16 6.8; 1024 experts 17.0 / 54.9.)
+    uint32_t hi[VPL];
 #pragma unroll
-    for (int v = 1; v < VPL; ++v) best = key[v] > best ? key[v] : best;
-    best = lanes_max<LANES>(best);
+    for (int v = 0; v < VPL; ++v) hi[v] = (uint32_t)(key[v] >> 32);
+    for (int j = 0; j < p.top; ++j) {
+      uint32_t best = hi[0];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) key[v] = key[v] == best ? 0 : key[v];
-    first = j == 0 ? best : first;
-    mine = lane == j ? best : mine;
-  }
-  const int e = lane < p.top ? expert_of(mine) : 0;
-  const double zs = p.bias ? logit(e) : logit_of(mine);
-  double w = 0.0;
-  if (p.scoring == IQP_SCORE_SOFTMAX) {
-    const bool chosen = !p.bias && p.renormalize;      // relative to the largest chosen one alone
-    w = zs == NONE ? 0.0 : exp(zs - (chosen ? logit_of(first) : top)) / (chosen ? 1.0 : sum);
+      for (int v = 1; v < VPL; ++v) best = hi[v] > best ? hi[v] : best;
+      best = lanes_max<LANES>(best);
+      int n = 0, e = 0;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) n += __popcll(__ballot(hi[v] == best));
+      const auto take = [&](int v, bool is) __attribute__((always_inline)) {
+        const uint64_t at = __ballot(is);
+        e = at ? LANES * v + __builtin_ctzll(at) : e;
+        hi[v] = is ? 0 : hi[v];
+      };
+      if (n == 1) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) take(v, hi[v] == best);
+      } else {
+        uint32_t low = 0;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) low = hi[v] == best && (uint32_t)key[v] > low ? (uint32_t)key[v] : low;
+        low = lanes_max<LANES>(low);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) take(v, hi[v] == best && (uint32_t)key[v] == low);
+      }
+      mine = lane == j ? e : mine;
+    }
   } else {
-    w = score_of(zs, p.scoring);
+    for (int j = 0; j < p.top; ++j) {
+      uint64_t best = key[0];
+#pragma unroll
+      for (int v = 1; v < VPL; ++v) best = key[v] > best ? key[v] : best;
+      best = lanes_max<LANES>(best);
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) key[v] = key[v] == best ? 0 : key[v];
+      mine = lane == j ? expert_of(best) : mine;
+    }
+  }
+  // what the chosen experts' lanes hold
+  double w = 0.0;
+  if (p.bias) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const double o = __shfl(score[v], mine % LANES, LANES);
+      w = mine / LANES == v ? o : w;
+    }
+  } else {
+    float x = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const float o = __shfl(z[v], mine % LANES, LANES);
+      x = mine / LANES == v ? o : x;
+    }
+    if (p.scoring != IQP_SCORE_SOFTMAX) w = score_of((double)x, p.scoring);
+    else if (!p.renormalize) w = x == NONE ? 0.0 : exp((double)x - top) / sum;
+    else w = x == NONE ? 0.0 : exp((double)x - (double)__shfl(x, 0, LANES));   // relative to the largest chosen one alone
   }
   w = lane < p.top ? w : 0.0;
   if (p.renormalize) {
@@ -146,7 +199,7 @@ void moe_route_kernel(MoeRouteArgs p) {
   }
   if (lane < p.top) {
     p.weights[m * p.top + lane] = (float)(w * (double)p.scale);
-    p.experts[m * p.top + lane] = e;
+    p.experts[m * p.top + lane] = mine;
   }
 }
 
@@ -215,7 +268,7 @@ void group_place_kernel(GroupRowsArgs p) {
     if (g < p.G) atomicAdd(&at[wave * p.G + g], 1);
   }
   if (count_all)
-    for (int64_t i = tid; i < p.R; i += SORT_THREADS) {
+    for (int64_t i = tid; i < p.R; i += SORT_THREADS) {      // (bound by the atomics: eight loads at a time save nothing)
       const int g = group_of(p, i);
       if (g < p.G) atomicAdd(&counted[i < first ? g : MAX_GROUPS + g], 1);
     }
@@ -319,8 +372,9 @@ void moe_combine_kernel(MoeCombineArgs p) {
 
 hipError_t launch_moe_route(const MoeRouteArgs& p, hipStream_t stream) {
   // A wave a token takes less time where tokens are few, a row of 16 lanes fewer
-  // instructions (us, wave / row, with a bias: 64 experts, 1024 tokens 3.9 / 4.7, 4632
-  // 7.7 / 5.3; 256 experts, 4632 tokens 9.0 / 13.6, 16384 22.3 / 20.6).
+  // instructions (us, top 8, without a bias, wave / row: 64 experts, 4632 tokens 4.5 / 4.0,
+  // 8192 5.8 / 4.1; 128 experts, 8192 6.6 / 5.5; 256 experts, 16384 14.3 / 12.0; with a bias
+  // 6.9 / 4.8, 9.4 / 5.0, 7.9 / 7.3, 19.6 / 19.8).
   const bool rows = p.E <= 256 && p.top <= 16 && p.M >= 40 * (int64_t)p.E;
   const int64_t blocks = rows ? (p.M + 15) / 16 : (p.M + 3) / 4;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
