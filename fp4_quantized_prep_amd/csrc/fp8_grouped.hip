@@ -16,17 +16,21 @@
 //
 // Up to about 32 rows a group the read of the weights bounds it (64 groups of 4096 x
 // 7168, 16 rows each: 313 us, 6.0 TB/s; 32: 319; 64: 328; 8 rows in 8 groups of 7168 x
-// 2048: 20 us, 5.8). Above, neither the read nor the products alone, but nearly their
-// sum: 300 us and 24 us for every 1000 rows (37056 rows in 64 groups: 1.15 ms, 1.88
-// PFLOP/s; of 768 rows each 2.2; the same with one group's weights for all 2.5, with
-// zeros for a 2.5, with both 2.9: the card lowers its clock under these products, and
-// weights from memory cost a sixth of the time). What did not help there: stages of
-// half a block, four deep (1214 us: requests of 64 bytes); weights asked into L2 two
-// blocks ahead (1213); a third stage for the weights of the 192-row tile; K blocks in
-// another order for each workgroup (643 us for 772 where a is zero and the weights are
-// shared, nothing with data); 8, 16, 64 or 128 tiles in a row to an XCD; eight waves of
-// 64 x 128 instead of four of 128 x 128 (512 tokens: 387 us for 367). A K of 2048 leaves
-// 7 us of a tile's 43 to its first loads and its stores.
+// 2048: 20 us, 5.8). Above, neither the read nor the products alone, but part of their
+// sum: 16384 rows in 64 groups 600 us, 37056 1.05 ms, 2.0 PFLOP/s; of 768 rows each
+// 2.3; the same with one group's weights for all 2.7, with zeros for a 2.55, with both
+// 3.05: the card lowers its clock under these products, and weights from memory cost a
+// seventh of the time. The matrix cores are busy for 60 % of a CU's time and the CUs for 86 %
+// (tiles of unequal length end unevenly), but the clock gives back most of what
+// evenness would save. What did not help there: tiles of a group as even as can be and
+// the groups sorted by them (64 groups of 4096 x 7168: 1024 tokens 457 to 428 us, but
+// 4632 the same, and at 7168 x 2048 600 to 625); offsets and addresses ahead of the copies,
+// so that fewer instructions stand between two MFMAs (1050 to 1081); stages of half a
+// block, four deep (requests of 64 bytes: 4 % more); weights asked into L2 two blocks
+// ahead (4 %); a third stage for the weights of the 192-row tile; K blocks in another
+// order for each workgroup; eight waves of 64 x 128 instead of four of 128 x 128 (512
+// tokens: 387 us for 367). A K of 2048 leaves 7 us of a tile's 40 to its first loads and
+// its stores.
 #include <type_traits>
 
 #include "iq_common.h"
@@ -224,7 +228,8 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
   // second half: by then every wave has read all of block j, whose stage is refilled,
   // and block j + 1 has landed (only the NST - 2 blocks after it may be in flight).
   // With one wave a SIMD, what is not an MFMA has to fit beside one: reads and copies
-  // go between the MFMAs one at a time, and offsets are scalar (HOW MUCH).
+  // go between the MFMAs one at a time, and offsets are scalar (37056 rows, 4096 x 7168: 1164 to 1099 us, 7168 x
+  // 2048: 644 to 605).
   constexpr int WAIT = waitcnt_vm((NST - 2) * NCOPY);
   const int row = lane & 31, swz = (row >> 1) & 7;
   v8i fw[2][AN], fa[AM];
@@ -548,13 +553,20 @@ constexpr int LDS_BYTES = STREAM_LDS > TILE_LDS ? STREAM_LDS : TILE_LDS;
 static_assert(LDS_BYTES >= tile_bytes<1, 3>() && LDS_BYTES >= tile_bytes<3, 2>() && LDS_BYTES >= tile_bytes<4, 2>(), "LDS");
 static_assert(LDS_BYTES <= 160 * 1024 && LDS_BYTES >= NW * 32 * (64 * AN + 16), "LDS");
 
+// Parts of a tile in a row before the next tile of the group. Workgroups go to an
+// XCD's CUs by turns: with one, large tiles and their groups' remainders alternate,
+// and half of the CUs get all the large ones (us, 1 / 4: 264 rows in each of 64 groups,
+// 4096 x 7168 767 / 681, 7168 x 2048 419 / 351; 512 rows 871 / 874; 37056 uneven rows the
+// same, 8 and 16 in a row 1 and 8 % more).
+constexpr int RUN = 4;
+
 // One tile a workgroup, by the body that its number of rows asks for: the host
 // does not know how many rows a group has.
 template <Epilogue EPI>
 __global__ __launch_bounds__(NW * 64)
 void fp8_grouped_kernel(Fp8GroupedArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
-  const groups::Tile t = groups::find_tile(p.groups, 256, p.parts, groups::item_of(blockIdx.x, p.chunk), p.large_first ? groups::LARGE_FIRST : groups::BY_PART);
+  const groups::Tile t = groups::find_tile(p.groups, 256, p.parts, RUN, groups::item_of(blockIdx.x, p.chunk), p.large_first);
   if (t.rows <= 0) return;
   if (t.rows <= 16) stream_body<EPI, 1, 3>(p, t, lds);
   else if (t.rows <= 64) tile_body<EPI, 1, 3>(p, t, lds);
@@ -571,7 +583,7 @@ hipError_t launch_fp8_grouped(Fp8GroupedArgs p, hipStream_t stream) {
   const int64_t tiles = p.groups.R / 256 + (p.groups.G < p.groups.R ? p.groups.G : p.groups.R);
   const int64_t items = tiles * p.parts;
   // A CU's neighbours on its XCD share weights and rows where tiles are many (37056 rows,
-  // 64 groups of 4096 x 7168, us: 1 in a row 1216, 8 to 32 1160, 128 1199); with few of
+  // 64 groups of 4096 x 7168: 8 to 32 in a row the same, 1 4 % more, 128 3 %); with few of
   // them every XCD has to get its part.
   p.chunk = items >= 2048 ? 32 : 1;
   // An output that the caches cannot keep for its reader goes past them (531 MB, K

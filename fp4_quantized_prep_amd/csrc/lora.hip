@@ -3,10 +3,10 @@
 // in two launches: h = A_g x (the first kernel, cut along K where there are few
 // rows, each piece's sums kept apart in float32), then out += s_g B_g h.
 //
-// The second is bound by out's way from and to memory (4632x8192, rank 64: 34 us for
-// 30 at a copy's rate), the first by A's way from L2, once for every 16 rows (K 1536:
-// 9.4 us); few rows by two launches and what they wait for one after the other (64
-// tokens of 32 adapters, 1536x7168, rank 16: 4.2 and 4.5 us for 10 MB).
+// The second is bound by out's way from and to memory (4632x8192, rank 64: 33 us for
+// 30 at a copy's rate), the first by A's way from L2, once for every 16 or 32 rows (K
+// 1536: 8 us); few rows by two launches and what they wait for one after the other (64
+// tokens of 32 adapters, 1536x7168, rank 16: 4.2 and 4.2 us for 10 MB).
 #include "iq_common.h"
 #include "layer_common.h"
 #include "row_groups.h"
@@ -48,7 +48,7 @@ template <int MT, int RT, int NST>
 __device__ __forceinline__ void shrink(const LoraArgs& p, uint8_t* lds) {
   constexpr int PITCH = 16 * RT + 4, STAGE = shrink_stage<MT, RT>(), NCOPY = 2 * (MT + RT);
   static_assert(4 * 16 * MT * PITCH <= NST * STAGE, "a wave's sums, in its ring's place");
-  const groups::Tile t = groups::find_tile(p.groups, 16 * MT, p.splits, groups::item_of(blockIdx.x, 1), groups::BY_PART);
+  const groups::Tile t = groups::find_tile(p.groups, 16 * MT, p.splits, 1, groups::item_of(blockIdx.x, 1), false);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -208,7 +208,7 @@ void lora_expand_kernel(LoraArgs p) {
   constexpr int PITCH = 68, HP = 64 * KT + 8;      // of a product's row (floats), of h's two parts (bf16)
   __shared__ __attribute__((aligned(16))) float lds[4 * 16 * PITCH];
   __shared__ __attribute__((aligned(16))) __bf16 parts[LORA_ROWS * HP];
-  const groups::Tile t = groups::find_tile(p.groups, LORA_ROWS, p.parts, groups::item_of(blockIdx.x, 1), groups::BY_TILE);
+  const groups::Tile t = groups::find_tile(p.groups, LORA_ROWS, p.parts, p.parts, groups::item_of(blockIdx.x, 1), false);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -31,21 +31,18 @@ struct Tile {
   int group, begin, rows, part;
 };
 
-// The order of the tiles: group by group, and within a group
-//   BY_PART     part by part, its tiles innermost: neighbours share weights;
-//   BY_TILE     tile by tile: neighbours share rows;
-//   LARGE_FIRST as BY_PART, but all groups' whole tiles first, then those of more
-//               than tm / 2 rows, then the others: few tiles end together.
-enum Order { BY_PART, BY_TILE, LARGE_FIRST };
-
 // Tile number `item`, where every group's rows are cut into tiles of tm (the
 // last one shorter) and each tile has `parts` parts. All lanes of all waves call it
 // and get the same answer. Offsets are kept inside [0, R] whatever they hold. 256
-// groups a round of loads.
-__device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts, int64_t item, Order order) {
+// groups a round of loads. The tiles come group by group, and within a group `run`
+// parts of a tile, the same of its next tile, until all have had them, then the next
+// `run`: with 1 neighbours share weights, with all parts they share rows.
+// large_first: all groups' whole tiles first, then those of more than tm / 2 rows,
+// then the others, so that few tiles end together.
+__device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts, int run, int64_t item, bool large_first) {
   const int lane = threadIdx.x & 63;
   int64_t done = 0;
-  for (int pass = 0; pass < (order == LARGE_FIRST ? 3 : 1); ++pass)
+  for (int pass = 0; pass < (large_first ? 3 : 1); ++pass)
     for (int g0 = 0; g0 < g.G; g0 += 256) {
       int begin[4], end[4];
 #pragma unroll
@@ -60,7 +57,7 @@ __device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts,
         const int n = d > 0 && g0 + 64 * q + lane < g.G ? d : 0;
         const int whole = (int)((unsigned)n / (unsigned)tm), rest = n - whole * tm;
         int tiles = whole + (rest > 0 ? 1 : 0), t0 = 0;
-        if (order == LARGE_FIRST) {
+        if (large_first) {
           t0 = pass ? whole : 0;
           tiles = pass == 0 ? whole : (pass == 1 ? rest > tm / 2 : rest > 0 && rest <= tm / 2) ? 1 : 0;
         }
@@ -70,8 +67,9 @@ __device__ __forceinline__ Tile find_tile(const RowGroups& g, int tm, int parts,
           const int at = 63 - __builtin_clzll(__ballot((done + upto - tiles) * parts <= item));
           const int mine = __builtin_amdgcn_readlane(tiles, at);
           const int local = (int)(item - (done + __builtin_amdgcn_readlane(upto, at) - mine) * parts);
-          const int part = order == BY_TILE ? local % parts : local / mine;
-          const int t = __builtin_amdgcn_readlane(t0, at) + (order == BY_TILE ? local / parts : local - part * mine);
+          const int first = local / (mine * run) * run, width = parts - first < run ? parts - first : run;
+          const int in = local - first * mine, down = in / width;
+          const int part = first + in - down * width, t = __builtin_amdgcn_readlane(t0, at) + down;
           const int rows = __builtin_amdgcn_readlane(n, at) - t * tm;
           return {g0 + 64 * q + at, __builtin_amdgcn_readlane(b, at) + t * tm, rows < tm ? rows : tm, part};
         }
