@@ -727,6 +727,9 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
 
 namespace {
 
+// Whether a launch may have so many workgroups of 256 threads: below 2^32 threads.
+bool launchable(int64_t workgroups) { return workgroups < (int64_t)1 << 24; }
+
 // Checks of the grouped products, shared by both; fills p. R == 0 or N == 0 leaves
 // nothing to do (p.groups.R is then 0).
 int check_grouped(const void* a, int64_t lda, const int32_t* a_scales, int64_t sm, int64_t sw, int64_t M, const void* w,
@@ -753,6 +756,7 @@ int check_grouped(const void* a, int64_t lda, const int32_t* a_scales, int64_t s
   const int64_t far = (int64_t)1 << 52;
   if (ldwg < 0 || ld_wsg < 0) return IQP_ERR_INVALID;
   if (ldwg > far || ld_wsg > far || ld_ws > ((int64_t)1 << 31)) return IQP_ERR_UNSUPPORTED;
+  if (!launchable(iqp::fp8_grouped_workgroups(R, G, N))) return IQP_ERR_UNSUPPORTED;
   p.groups = {offsets, rows, R, G};
   p.a = static_cast<const uint8_t*>(a);
   p.lda = lda;
@@ -785,7 +789,7 @@ int moe_route(const void* logits, int64_t ld, int32_t logits_bf16, const float* 
   if (E > iqp::MAX_GROUPS || top_k > 64) return IQP_ERR_UNSUPPORTED;
   if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(experts, 4))
     return IQP_ERR_UNSUPPORTED;
-  if (M > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  if (!launchable((M + 3) / 4)) return IQP_ERR_UNSUPPORTED;
   const int st = device_status();
   if (st != IQP_OK) return st;
   iqp::MoeRouteArgs p{};
@@ -883,7 +887,7 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
   if (d % 8 || !aligned(y, 16) || ldy % 8 || !aligned(out, 16) || ldo % 8 || !aligned(slots, 4) || !aligned(weights, 4) ||
       (shared && (!aligned(shared, 16) || ld_shared % 8)))
     return IQP_ERR_UNSUPPORTED;
-  if (R > 0x7FFFFFFF || M > 0x7FFFFFFF || d > 0x7FFFFFFF) return IQP_ERR_UNSUPPORTED;
+  if (R > 0x7FFFFFFF || M > 0x7FFFFFFF || d > 0x7FFFFFFF || !launchable(M * iqp::moe_combine_parts(d))) return IQP_ERR_UNSUPPORTED;
   const int st = device_status();
   if (st != IQP_OK) return st;
   iqp::MoeCombineArgs p{};
@@ -921,6 +925,7 @@ int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, co
   // x, and an adapter's rows, are addressed with 32-bit offsets
   if (K > (1 << 22) || ldx >= (1 << 30) || M > 0x7FFFFFFF || 2 * ((M - 1) * ldx + K) >= ((int64_t)1 << 31)) return IQP_ERR_UNSUPPORTED;
   if (N > 0x7FFFFFFF || G > iqp::MAX_GROUPS) return IQP_ERR_UNSUPPORTED;
+  if (!launchable(iqp::lora_workgroups(M, G, rank, K, N))) return IQP_ERR_UNSUPPORTED;
   if (workspace_bytes < lora_add_workspace_bytes(M, G, rank, K)) return IQP_ERR_INVALID;
   if (!aligned(workspace, 256)) return IQP_ERR_UNSUPPORTED;
   const int st = device_status();

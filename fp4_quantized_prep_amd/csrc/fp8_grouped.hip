@@ -577,15 +577,24 @@ void fp8_grouped_kernel(Fp8GroupedArgs p) {
 
 }  // namespace
 
+namespace {
+
+// at most so many tiles: whole ones, and one that is not for every group
+int64_t tiles_of(int64_t R, int32_t G) { return R / 256 + (G < R ? G : R); }
+
+constexpr int MAX_CHUNK = 32;
+
+}  // namespace
+
+int64_t fp8_grouped_workgroups(int64_t R, int32_t G, int64_t N) { return tiles_of(R, G) * ((N + TN - 1) / TN) + 8 * MAX_CHUNK; }
+
 hipError_t launch_fp8_grouped(Fp8GroupedArgs p, hipStream_t stream) {
-  p.parts = (int32_t)(p.q ? p.N / TN : (p.N + TN - 1) / TN);
-  // at most so many tiles: whole ones, and one that is not for every group
-  const int64_t tiles = p.groups.R / 256 + (p.groups.G < p.groups.R ? p.groups.G : p.groups.R);
-  const int64_t items = tiles * p.parts;
+  p.parts = (int32_t)((p.N + TN - 1) / TN);
+  const int64_t items = tiles_of(p.groups.R, p.groups.G) * p.parts;
   // A CU's neighbours on its XCD share weights and rows where tiles are many (37056 rows,
   // 64 groups of 4096 x 7168: 8 to 32 in a row the same, 1 4 % more, 128 3 %); with few of
   // them every XCD has to get its part.
-  p.chunk = items >= 2048 ? 32 : 1;
+  p.chunk = items >= 2048 ? MAX_CHUNK : 1;
   // An output that the caches cannot keep for its reader goes past them (531 MB, K
   // 2048: 632 us for 644).
   p.stream_out = p.groups.R * p.N * 2 > ((int64_t)256 << 20);
@@ -595,7 +604,6 @@ hipError_t launch_fp8_grouped(Fp8GroupedArgs p, hipStream_t stream) {
   // 64, K 7168 366 / 376; K 2048, 8 tokens 95 / 109).
   p.large_first = items <= 512 && p.groups.R >= 16 * (int64_t)p.groups.G;
   const int64_t blocks = (items + 8 * p.chunk - 1) / (8 * p.chunk) * (8 * p.chunk);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (p.q)
     hipLaunchKernelGGL((fp8_grouped_kernel<SWIGLU>), dim3((unsigned)blocks), dim3(NW * 64), 0, stream, p);
   else

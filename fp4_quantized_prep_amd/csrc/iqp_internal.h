@@ -371,6 +371,7 @@ struct Fp8GroupedArgs {
   bool large_first;         // the order of the tiles,
   bool stream_out;          // whether out's stores go past the caches
 };
+int64_t fp8_grouped_workgroups(int64_t R, int32_t G, int64_t N);      // of the launch, at most
 hipError_t launch_fp8_grouped(Fp8GroupedArgs args, hipStream_t stream);
 
 struct MoeRouteArgs {
@@ -416,6 +417,7 @@ struct MoeCombineArgs {
   int64_t ldo;
   int32_t parts;            // set by the launcher: workgroups of a row
 };
+int32_t moe_combine_parts(int64_t d);
 hipError_t launch_moe_combine(MoeCombineArgs args, hipStream_t stream);
 
 struct LoraArgs {
@@ -434,6 +436,7 @@ struct LoraArgs {
 };
 int lora_splits(int64_t R, int32_t G, int32_t rank, int64_t K);
 int lora_pitch(int32_t rank);
+int64_t lora_workgroups(int64_t R, int32_t G, int32_t rank, int64_t K, int64_t N);      // of the larger launch, at most
 hipError_t launch_lora_add(LoraArgs args, hipStream_t stream);
 
 // compute units of the current device (cached per device)

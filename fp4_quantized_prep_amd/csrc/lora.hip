@@ -332,12 +332,25 @@ int lora_splits(int64_t R, int32_t G, int32_t rank, int64_t K) {
 
 int lora_pitch(int32_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
+namespace {
+
+int64_t shrink_workgroups(int64_t R, int32_t G, int32_t rank, int splits) {
+  return (tiles_of(R, G, shrink_rows(R, G, rank)) * splits + 7) / 8 * 8;
+}
+int64_t expand_workgroups(int64_t R, int32_t G, int64_t N) { return (tiles_of(R, G, LORA_ROWS) * ((N + LORA_COLS - 1) / LORA_COLS) + 7) / 8 * 8; }
+
+}  // namespace
+
+int64_t lora_workgroups(int64_t R, int32_t G, int32_t rank, int64_t K, int64_t N) {
+  const int64_t shrink = shrink_workgroups(R, G, rank, lora_splits(R, G, rank, K)), expand = expand_workgroups(R, G, N);
+  return shrink > expand ? shrink : expand;
+}
+
 hipError_t launch_lora_add(LoraArgs p, hipStream_t stream) {
   p.h_pitch = lora_pitch(p.rank);
   p.parts = (int32_t)((p.N + LORA_COLS - 1) / LORA_COLS);
-  const int64_t shrink = (tiles_of(p.groups.R, p.groups.G, shrink_rows(p.groups.R, p.groups.G, p.rank)) * p.splits + 7) / 8 * 8;
-  const int64_t expand = (tiles_of(p.groups.R, p.groups.G, LORA_ROWS) * p.parts + 7) / 8 * 8;
-  if (shrink > 0x7FFFFFFF || expand > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int64_t shrink = shrink_workgroups(p.groups.R, p.groups.G, p.rank, p.splits);
+  const int64_t expand = expand_workgroups(p.groups.R, p.groups.G, p.N);
   // (16 places: LDS for two workgroups a CU up to rank 64)
   const bool wide = shrink_rows(p.groups.R, p.groups.G, p.rank) == 32;
   const auto first = p.h_pitch == 16   ? lora_shrink_kernel<1, 1, 4>

@@ -377,7 +377,6 @@ hipError_t launch_moe_route(const MoeRouteArgs& p, hipStream_t stream) {
   // 6.9 / 4.8, 9.4 / 5.0, 7.9 / 7.3, 19.6 / 19.8).
   const bool rows = p.E <= 256 && p.top <= 16 && p.M >= 40 * (int64_t)p.E;
   const int64_t blocks = rows ? (p.M + 15) / 16 : (p.M + 3) / 4;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   const auto kern = rows ? (p.E <= 16    ? moe_route_kernel<16, 1>
                             : p.E <= 32  ? moe_route_kernel<16, 2>
                             : p.E <= 64  ? moe_route_kernel<16, 4>
@@ -421,11 +420,11 @@ hipError_t launch_group_rows(GroupRowsArgs p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+int32_t moe_combine_parts(int64_t d) { return (int32_t)((d + 2047) / 2048); }
+
 hipError_t launch_moe_combine(MoeCombineArgs p, hipStream_t stream) {
-  p.parts = (int32_t)((p.d + 2047) / 2048);
-  const int64_t blocks = p.M * p.parts;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+  p.parts = moe_combine_parts(p.d);
+  hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)(p.M * p.parts)), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

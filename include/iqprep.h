@@ -803,7 +803,7 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
  * of a token are distinct and in range whatever its logits hold.
  *
  *   logits   float32, or bf16 where logits_bf16 is not 0, [M, E], row stride ld
- *            (elements, >= E); 4- or 2-byte aligned. E 1 to 1024.
+ *            (elements, >= E); 4- or 2-byte aligned. E 1 to 1024, M up to 2^26 - 4.
  *   bias     NULL, or float32 [E], finite.
  *   top_k    1 to min(E, 64).
  *   weights  float32 [M, top_k];  experts  int32 [M, top_k]; both contiguous.
@@ -862,7 +862,8 @@ int group_rows(const int32_t* index, int64_t R, int32_t G, int32_t* offsets, int
  *              aligned; q_scales packed words [R, ceil(I/512)] in either layout of
  *              fp8_quant_1x128_ue8m0.
  *              Rows of no group are left as they were in all three, and none of them
- *              may overlap the inputs.
+ *              may overlap the inputs. (R / 256 + min(G, R)) ceil(N / 256) below 2^24 -
+ *              256, N being 2 I for swiglu.
  * R == 0, N == 0 or I == 0: no-op. The results must be finite in float32. The same
  * call gives the same bits; a place's last bit may depend on how many rows its
  * group has.
@@ -888,7 +889,7 @@ int fp8_grouped_swiglu_1x128(const void* a, int64_t lda, const int32_t* a_scales
  *   y        bf16 [R, d], row stride ldy;  shared  NULL, or bf16 [M, d], row stride
  *            ld_shared;  out  bf16 [M, d], row stride ldo, may be shared itself
  *            (same stride), otherwise must not overlap the inputs. 16-byte aligned,
- *            d and the strides multiples of 8.
+ *            d and the strides multiples of 8; M ceil(d / 2048) below 2^24.
  *   slots    int32 [M, top_k];  weights  float32 [M, top_k]; contiguous. top_k >= 1.
  */
 int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, const float* weights, int64_t M,
@@ -910,7 +911,8 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
  *              offsets outside [0, M] are clamped, rows outside [0, M) left out. No
  *              row may be at two places (group_rows gives none).
  *   out        bf16 [M, N], row stride ldo, 2-byte aligned (fastest where 16-byte
- *              aligned with ldo a multiple of 8). Must not overlap the others.
+ *              aligned with ldo a multiple of 8). Must not overlap the others. (M / 64 +
+ *              min(G, M)) ceil(N / 256) below 2^24 - 8.
  *   workspace  lora_add_workspace_bytes(M, G, rank, K) bytes of device memory, 256-byte
  *              aligned; its contents do not matter before and mean nothing after.
  *              Calls that share one must not overlap.

@@ -374,3 +374,31 @@ def test_grouped_offset_start(gpu_lib):
     y, bound = X.product(a, ab, w, ws, offsets, src)
     X.check_product(out.cpu(), y, bound)
     assert bool((out[:5] == 6.0).all()) and bool((out[31:] == 6.0).all())
+
+
+@pytest.mark.parametrize("M,E,top", [(9, 64, 8), (5, 128, 5), (7, 200, 8), (9, 256, 8), (3, 500, 40), (4, 1000, 64), (2600, 64, 8)])
+@pytest.mark.parametrize("scoring,bias", [("softmax", False), ("sigmoid", False), ("sigmoid", True), ("sqrt_softplus", True)])
+def test_route_close_logits(gpu_lib, M, E, top, scoring, bias):
+    """Logits that differ in their last six bits alone, many of them equal: the
+    order hangs on the last bits of the choices, and on the index."""
+    print("close logits", M, E, top, scoring, bias, flush=True)
+    g = gen(23, M, E, top)
+    z = torch.from_numpy((1 + g.integers(0, 64, (M, E)) * 2.0 ** -23).astype(np.float32))
+    b = torch.full((E,), 0.5) if bias else None
+    w, e = gpu_lib.moe_route(z.cuda(), top, bias=None if b is None else b.cuda(), scoring=scoring)
+    want, ids = X.route(z, top, b, scoring, True, 1.0)
+    assert torch.equal(e.cpu(), ids)
+    assert bool(((w.cpu().double() - want).abs() <= 2.0 ** -24 * (1 + 2.0 ** -10) * want.abs()).all())
+
+
+@pytest.mark.parametrize("N,K,top,gather", [(9 * 256 + 40, 256, 1, False), (5 * 256, 384, 2, True)])
+def test_grouped_remainders(gpu_lib, N, K, top, gather):
+    """Groups of one, two and three tiles whose last ones are of every body's size,
+    and more parts of a tile than come in a row."""
+    print("remainders", N, K, top, gather, flush=True)
+    g = gen(24, N, K)
+    counts = [264, 256, 300, 0, 520, 2, 384, 700, 257, 449]
+    plan, a, ab, w, ws, src = operands(g, counts, 4, N, K, top, gather)
+    out = gpu_lib.fp8_grouped_gemm_1x128_128x128(a.cuda(), X.words_of(ab).cuda(), w.cuda(), ws.cuda(), groups_on_gpu(gpu_lib, plan), gather=gather)
+    y, bound = X.product(a, ab, w, ws, plan[0], src)
+    X.check_product(out.cpu(), y, bound)

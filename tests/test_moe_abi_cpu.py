@@ -124,3 +124,23 @@ def test_python_refusals(iqp):
             call()
     with pytest.raises(ValueError, match="scoring"):
         iqp.moe_route(z, 2, scoring="relu")
+
+
+def test_launches_of_too_many_workgroups_are_refused(iqp):
+    """2^24 workgroups of 256 threads or more are beyond a launch: every call says so
+    before it looks for a device."""
+    uns = iqp.IQP_ERR_UNSUPPORTED
+    L, p = iqp._lib, P(256)
+    for M in ((1 << 26) - 3, 1 << 26, (1 << 31) - 1):
+        assert L.moe_route(p, 8, 0, None, M, 8, 2, 0, 1, 1.0, p, p, None) == uns, M
+    for M, d in ((1 << 24, 8), (1 << 23, 2056), ((1 << 31) - 1, 8), ((1 << 31) - 1, (1 << 31) - 8)):
+        assert L.moe_combine(p, d, 4, p, p, M, 2, d, None, 0, p, d, None) == uns, (M, d)
+    for G, R, N in ((1024, 1024, 1 << 22), (1024, 1 << 20, 1 << 20), (2, 4, (1 << 31) - 256)):
+        assert L.fp8_grouped_gemm_1x128_128x128(p, 128, p, 1, R, R, p, 128 * N, 128, p, (N + 127) // 128, 1, p, p, R, G, 0, N, 128, p, N,
+                                                None) == uns, (G, R, N)
+        I = N // 2
+        assert L.fp8_grouped_swiglu_1x128(p, 128, p, 1, R, R, p, 128 * N, 128, p, N // 128, 1, p, p, R, G, 0, I, 128, p, I, p,
+                                          1, R, None) == uns, (G, R, I)
+    for M, G, N in ((1024, 1024, 1 << 22), (4, 4, (1 << 31) - 1), (1 << 20, 8, 1 << 18)):
+        need = iqp.lora_add_workspace_bytes(M, G, 16, 64)
+        assert L.lora_add(p, 64, M, 64, p, p, None, 16, p, p, G, N, p, N, p, need, None) == uns, (M, G, N)
