@@ -1,5 +1,7 @@
 // Around the products by expert: the router's choice of experts, the entries of
 // a batch sorted by group, and every token's weighted sum of its experts' rows.
+#include <type_traits>
+
 #include "iqprep.h"
 #include "layer_common.h"
 #include "row_groups.h"
@@ -230,8 +232,8 @@ void group_count_kernel(GroupRowsArgs p) {
 // Stable: an entry's place is the number of entries of lower groups, of its group
 // in chunks and waves before its own (the integer atomics add in any order), and
 // of its group before it in its wave (found by comparing the bits of the 64 lanes'
-// groups). Bound by its few dependent steps: 8 entries 3.4 us, 2048 of 256 groups 4.5,
-// 37056 8.2 with the counts' launch, for 1.2 MB.
+// groups). Bound by its few dependent steps: 8 entries 3.1 us, 2048 of 256 groups 4.2,
+// 37056 7.4 with the counts' launch, for 1.2 MB.
 __global__ __launch_bounds__(SORT_THREADS)
 void group_place_kernel(GroupRowsArgs p) {
   __shared__ int at[SORT_WAVES * MAX_GROUPS];
@@ -244,22 +246,39 @@ void group_place_kernel(GroupRowsArgs p) {
   // the wave's first entries (all that it has, up to 2^17 in all) and the counts are
   // asked for before anything waits
   const int own = mine + lane < mine_end ? group_of(p, mine + lane) : p.G;
-  // thread g: its group's entries before this chunk, and in all
-  int before = 0, all = 0;
-  if (p.counts && tid < p.G)
-    for (unsigned c0 = 0; c0 < gridDim.x; c0 += 16) {      // (16 loads at a time)
-      int n[16];
+  // Entries of a group before this chunk, and from it on: the chunks' counts, shared out
+  // to as many threads a group as there are, as many loads at a time as each has chunks
+  // (all chunks by one thread, 16 at a time / so: 37056 entries of 256 groups 7.8 / 7.4 us,
+  // of 64 7.2 / 6.3, 131072 of 256 11.3 / 9.5); or, where no launch has counted, entry by
+  // entry below.
+  int earlier = 0, later = 0;
+  const int wide = p.G > 64 ? 32 - __builtin_clz(p.G - 1) : 6, mate = tid >> wide, mine_g = tid & ((1 << wide) - 1);
+  const auto add_counts = [&](auto at_once) __attribute__((always_inline)) {
+    constexpr int LOADS = decltype(at_once)::value;
+    for (int c0 = mate; c0 < (int)gridDim.x; c0 += LOADS * SORT_THREADS >> wide) {
+      int n[LOADS];
 #pragma unroll
-      for (unsigned c = 0; c < 16; ++c) n[c] = p.counts[(int64_t)(c0 + c < gridDim.x ? c0 + c : 0) * p.G + tid];
+      for (int k = 0; k < LOADS; ++k) {
+        const int c = c0 + (k * SORT_THREADS >> wide);
+        n[k] = p.counts[(int64_t)(c < (int)gridDim.x ? c : 0) * p.G + mine_g];
+      }
 #pragma unroll
-      for (unsigned c = 0; c < 16; ++c) {
-        before += c0 + c < blockIdx.x ? n[c] : 0;
-        all += c0 + c < gridDim.x ? n[c] : 0;
+      for (int k = 0; k < LOADS; ++k) {
+        const int c = c0 + (k * SORT_THREADS >> wide);
+        earlier += c < (int)blockIdx.x ? n[k] : 0;
+        later += c >= (int)blockIdx.x && c < (int)gridDim.x ? n[k] : 0;
       }
     }
-  const bool count_all = !p.counts && gridDim.x > 1;
+  };
+  if (p.counts && mine_g < p.G) {
+    const int each = (int)((gridDim.x + (SORT_THREADS >> wide) - 1) / (unsigned)(SORT_THREADS >> wide));
+    if (each <= 4) add_counts(std::integral_constant<int, 4>());
+    else if (each <= 12) add_counts(std::integral_constant<int, 12>());
+    else add_counts(std::integral_constant<int, 16>());
+  }
+  const bool several = gridDim.x > 1, count_all = !p.counts && several;
   for (int g = tid; g < SORT_WAVES * p.G; g += SORT_THREADS) at[g] = 0;
-  if (count_all)
+  if (several)
     for (int g = tid; g < p.G; g += SORT_THREADS) counted[g] = counted[MAX_GROUPS + g] = 0;
   __syncthreads();
   if (own < p.G) atomicAdd(&at[wave * p.G + own], 1);
@@ -267,14 +286,19 @@ void group_place_kernel(GroupRowsArgs p) {
     const int g = group_of(p, i);
     if (g < p.G) atomicAdd(&at[wave * p.G + g], 1);
   }
+  if (p.counts && mine_g < p.G) {
+    atomicAdd(&counted[mine_g], earlier);
+    atomicAdd(&counted[MAX_GROUPS + mine_g], later);
+  }
   if (count_all)
-    for (int64_t i = tid; i < p.R; i += SORT_THREADS) {      // (bound by the atomics: eight loads at a time save nothing)
+    for (int64_t i = tid; i < p.R; i += SORT_THREADS) {      // (eight loads at a time: 2048 entries 5.0 us for 4.2, 8192 5.3 for 5.4)
       const int g = group_of(p, i);
       if (g < p.G) atomicAdd(&counted[i < first ? g : MAX_GROUPS + g], 1);
     }
   __syncthreads();
-  if (tid < p.G && !p.counts) {
-    if (count_all) {
+  int before = 0, all = 0;      // thread g: its group's
+  if (tid < p.G) {
+    if (several) {
       before = counted[tid];
       all = before + counted[MAX_GROUPS + tid];
     } else {
@@ -399,8 +423,8 @@ int64_t group_rows_chunk(int64_t R) {
 }
 
 // Chunks that a launch of their own counts; 0 where every workgroup counts all
-// entries itself (us, itself / a launch, 256 groups: 2048 entries 4.5 / 5.8, 8192 5.8 /
-// 6.7, 12000 6.6 / 6.8, 16384 7.5 / 6.8).
+// entries itself (us, itself / a launch, 256 groups: 2048 entries 4.2 / 5.8, 8192 5.4 /
+// 6.6, 12000 6.6 / 6.7, 16384 7.5 / 6.6).
 int64_t group_rows_counts(int64_t R) {
   const int64_t chunk = group_rows_chunk(R), chunks = (R + chunk - 1) / chunk;
   return chunks > 8 ? chunks : 0;
