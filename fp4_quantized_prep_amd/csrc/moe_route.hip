@@ -68,10 +68,28 @@ __device__ __forceinline__ double score_of(double z, int scoring) {
   return sqrt((z > 0.0 ? z : 0.0) + log1p(exp(-fabs(z))));    // sqrt of softplus
 }
 
+// 1 / (1 + e^-z) for |z| < 690 to 2^-50 of itself, in half of the instructions that
+// exp and a division take: e^-z = 2^n e^r with r within ln 2 / 2 of 0, e^r by its
+// series (the next term is below 2^-52), the reciprocal by two Newton steps.
+__device__ __forceinline__ double sigmoid_of(double z) {
+  const double n = __builtin_rint(z * -1.4426950408889634);      // 1 / ln 2
+  double r = __builtin_fma(n, -0.6931471805599453, -z);          // ln 2, and what it lacks
+  r = __builtin_fma(n, -2.3190468138462996e-17, r);
+  constexpr double OVER_FACTORIAL[] = {1.0 / 479001600, 1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040,
+                                       1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 1.0 / 2, 1.0, 1.0};      // 12! .. 0!
+  double e = OVER_FACTORIAL[0];
+#pragma unroll
+  for (int k = 1; k < 13; ++k) e = __builtin_fma(e, r, OVER_FACTORIAL[k]);
+  const double d = 1.0 + __builtin_ldexp(e, (int)n);
+  double q = __builtin_amdgcn_rcp(d);
+  q = __builtin_fma(__builtin_fma(-d, q, 1.0), q, q);
+  return __builtin_fma(__builtin_fma(-d, q, 1.0), q, q);
+}
+
 // LANES lanes a token, expert LANES v + lane its lane's v-th value. Scores and
 // choices are float64, so that which expert is taken does not hang on how an
 // exponential is rounded. Bound by its instructions: 256 experts, top 8, with a bias:
-// 4.4 us for a token (2.5 of it a launch), 8.5 for 4632 (2 of it the scores, 2.5 the
+// 4.2 us for a token (2.5 of it a launch), 8.5 for 4632 (2 of it the scores, 2.5 the
 // choice), whose logits' read takes 1; 1024 experts 10.7 and 25.
 template <int LANES, int VPL>
 __global__ __launch_bounds__(256)
@@ -119,12 +137,31 @@ void moe_route_kernel(MoeRouteArgs p) {
   }
   uint64_t key[VPL];
   double score[VPL];       // with a bias: of every expert, as the choice goes by it
+  const auto slow = [&](int v) __attribute__((always_inline)) {
+    return p.scoring == IQP_SCORE_SOFTMAX ? exp((double)z[v] - top) / sum : score_of((double)z[v], p.scoring);
+  };
+  // Few sigmoids a lane by few instructions (us, so / by exp and a division: 1024
+  // tokens, top 8, 256 experts (4 a lane) 4.9 / 5.2, 64 (1) 3.3 / 3.8; 16384 of 16 (1) 3.3 /
+  // 4.8, but of 256 (16 a lane) 23.4 / 20.1).
+  constexpr bool FEW = VPL <= 4;
+  if (FEW && p.bias) {
+    bool far = p.scoring != IQP_SCORE_SIGMOID;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) far = far || !(fabsf(z[v]) < 690.f || z[v] == NONE);
+    if (__ballot(far) == 0) {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) score[v] = sigmoid_of((double)z[v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) score[v] = slow(v);
+    }
+  }
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     const int e = LANES * v + lane;
     double c = (double)z[v];
     if (p.bias) {
-      score[v] = z[v] == NONE ? 0.0 : p.scoring == IQP_SCORE_SOFTMAX ? exp(c - top) / sum : score_of(c, p.scoring);
+      score[v] = z[v] == NONE ? 0.0 : FEW ? score[v] : slow(v);
       c = z[v] == NONE ? c : score[v] + (double)b[v];
     }
     key[v] = e < p.E ? key_of(c, e) : 0;

@@ -402,3 +402,25 @@ def test_grouped_remainders(gpu_lib, N, K, top, gather):
     out = gpu_lib.fp8_grouped_gemm_1x128_128x128(a.cuda(), X.words_of(ab).cuda(), w.cuda(), ws.cuda(), groups_on_gpu(gpu_lib, plan), gather=gather)
     y, bound = X.product(a, ab, w, ws, plan[0], src)
     X.check_product(out.cpu(), y, bound)
+
+
+@pytest.mark.parametrize("E", [8, 64, 256, 300])
+@pytest.mark.parametrize("far", [False, True])
+def test_route_sigmoids_of_all_sizes(gpu_lib, E, far):
+    """Sigmoid scores with a bias for logits from nearly 0 to beyond the range of
+    exp, one such logit in a token or none: weights to one rounding, experts as the
+    scores in 64 bits order them."""
+    print("sigmoids", E, far, flush=True)
+    g = gen(25, E, far)
+    z = g.standard_normal((40, E)) * 10.0 ** g.uniform(-6, 2, (40, E))
+    if far:
+        z[::2, 1] = -1e4
+        z[1::4, 2] = 3e38
+        z[3::4, 3] = -700
+    z = torch.from_numpy(z.astype(np.float32))
+    b = torch.from_numpy(g.standard_normal(E).astype(np.float32))
+    for renormalize in (False, True):
+        w, e = gpu_lib.moe_route(z.cuda(), 4, bias=b.cuda(), scoring="sigmoid", renormalize=renormalize)
+        want, ids = X.route(z, 4, b, "sigmoid", renormalize, 1.0)
+        assert torch.equal(e.cpu(), ids)
+        assert bool(((w.cpu().double() - want).abs() <= 2.0 ** -24 * (1 + 2.0 ** -10) * want.abs() + 2.0 ** -149).all())
