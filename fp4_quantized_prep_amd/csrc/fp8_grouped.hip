@@ -55,16 +55,22 @@ constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >
 // others by "or", so that two of them stay one.
 constexpr uint32_t PAST = 0x80000000u;
 
-// row of a that place t.begin + r reads, PAST where there is none
-__device__ __forceinline__ uint32_t source_row(const Fp8GroupedArgs& p, const groups::Tile& t, int r) {
-  if (r >= t.rows) return PAST;
-  int src = t.begin + r;
+// Rows of a that C of a lane's places read, PAST where there is none; `place(i)` is
+// the i-th one's number in the tile. All entries are asked for before one is waited for.
+template <int C, typename Place>
+__device__ __forceinline__ void source_rows(const Fp8GroupedArgs& p, const groups::Tile& t, Place place, uint32_t (&src)[C]) {
+  int entry[C];
   if (p.top) {
-    src = p.groups.rows[src];
-    if (src < 0) return PAST;
-    src = (int)((unsigned)src / (unsigned)p.top);
+#pragma unroll
+    for (int i = 0; i < C; ++i) entry[i] = p.groups.rows[t.begin + (place(i) < t.rows ? place(i) : 0)];
+#pragma unroll
+    for (int i = 0; i < C; ++i) entry[i] = entry[i] < 0 ? -1 : (int)((unsigned)entry[i] / (unsigned)p.top);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) entry[i] = t.begin + place(i);
   }
-  return src < p.M ? (uint32_t)src : PAST;
+#pragma unroll
+  for (int i = 0; i < C; ++i) src[i] = place(i) < t.rows && entry[i] >= 0 && entry[i] < p.M ? (uint32_t)entry[i] : PAST;
 }
 
 // what the bodies read of a group's weights
@@ -174,16 +180,12 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     const int n = (r & ~31) + 4 * ((r >> 3) & 3) + 16 * ((r >> 2) & 1) + (r & 3);
     vw[i] = (uint32_t)(n * (int)p.ldw + chunk);
   }
+  uint32_t src[AC + 1];
+  const auto place = [&](int i) __attribute__((always_inline)) { return i < AC ? 8 * (wave + NW * i) + (lane >> 3) : 64 * (wave % AM) + lane; };
+  source_rows(p, t, place, src);
 #pragma unroll
-  for (int i = 0; i < AC; ++i) {
-    const int r = 8 * (wave + NW * i) + (lane >> 3);
-    const uint32_t src = source_row(p, t, r);
-    va[i] = src == PAST ? PAST : src * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-  }
-  {
-    const uint32_t src = source_row(p, t, 64 * (wave % AM) + lane);
-    vs = src == PAST ? PAST : 4 * src * (uint32_t)p.as_sm;
-  }
+  for (int i = 0; i < AC; ++i) va[i] = src[i] == PAST ? PAST : src[i] * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((place(i) >> 1) & 7));
+  vs = src[AC] == PAST ? PAST : 4 * src[AC] * (uint32_t)p.as_sm;
 
   // Copy c (0 .. NCOPY - 1) of block j into stage st. Past the last block the buffers
   // are of no bytes: the copies read zeros, with the offset left at 0.
@@ -416,14 +418,12 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
     const int n = EPI == SWIGLU ? WR / 2 * wave + r % (WR / 2) : WR * wave + r;
     vw[c] = (uint32_t)(n * (int)p.ldw + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
   }
+  uint32_t src[AC + 1];
+  const auto place = [&](int i) __attribute__((always_inline)) { return i < AC ? 8 * i + (lane >> 3) : lane; };
+  source_rows(p, t, place, src);
 #pragma unroll
-  for (int c = 0; c < AC; ++c) {
-    const int r = 8 * c + (lane >> 3);
-    const uint32_t src = source_row(p, t, r);
-    va[c] = src == PAST ? PAST : src * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-  }
-  const uint32_t ssrc = lane < TOK ? source_row(p, t, lane) : PAST;
-  const uint32_t vs = ssrc == PAST ? PAST : 4 * ssrc * (uint32_t)p.as_sm;
+  for (int c = 0; c < AC; ++c) va[c] = src[c] == PAST ? PAST : src[c] * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((place(c) >> 1) & 7));
+  const uint32_t vs = src[AC] == PAST ? PAST : 4 * src[AC] * (uint32_t)p.as_sm;
   uint8_t* const ring = lds + wave * NST * STAGE;
 
   // the i-th block of the walk into stage st
