@@ -56,18 +56,23 @@ constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >
 constexpr uint32_t PAST = 0x80000000u;
 
 // Rows of a that C of a lane's places read, PAST where there is none; `place(i)` is
-// the i-th one's number in the tile. All entries are asked for before one is waited for.
-template <int C, typename Place>
-__device__ __forceinline__ void source_rows(const Fp8GroupedArgs& p, const groups::Tile& t, Place place, uint32_t (&src)[C]) {
+// the i-th one's number in the tile. All entries are asked for before one is waited for,
+// and `meanwhile` is done in between.
+template <int C, typename Place, typename Meanwhile>
+__device__ __forceinline__ void source_rows(const Fp8GroupedArgs& p, const groups::Tile& t, Place place, uint32_t (&src)[C], Meanwhile meanwhile) {
   int entry[C];
   if (p.top) {
 #pragma unroll
     for (int i = 0; i < C; ++i) entry[i] = p.groups.rows[t.begin + (place(i) < t.rows ? place(i) : 0)];
+    __builtin_amdgcn_sched_barrier(0);
+    meanwhile();
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < C; ++i) entry[i] = entry[i] < 0 ? -1 : (int)((unsigned)entry[i] / (unsigned)p.top);
   } else {
 #pragma unroll
     for (int i = 0; i < C; ++i) entry[i] = t.begin + place(i);
+    meanwhile();
   }
 #pragma unroll
   for (int i = 0; i < C; ++i) src[i] = place(i) < t.rows && entry[i] >= 0 && entry[i] < p.M ? (uint32_t)entry[i] : PAST;
@@ -180,12 +185,6 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
     const int n = (r & ~31) + 4 * ((r >> 3) & 3) + 16 * ((r >> 2) & 1) + (r & 3);
     vw[i] = (uint32_t)(n * (int)p.ldw + chunk);
   }
-  uint32_t src[AC + 1];
-  const auto place = [&](int i) __attribute__((always_inline)) { return i < AC ? 8 * (wave + NW * i) + (lane >> 3) : 64 * (wave % AM) + lane; };
-  source_rows(p, t, place, src);
-#pragma unroll
-  for (int i = 0; i < AC; ++i) va[i] = src[i] == PAST ? PAST : src[i] * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((place(i) >> 1) & 7));
-  vs = src[AC] == PAST ? PAST : 4 * src[AC] * (uint32_t)p.as_sm;
 
   // Copy c (0 .. NCOPY - 1) of block j into stage st. Past the last block the buffers
   // are of no bytes: the copies read zeros, with the offset left at 0.
@@ -209,10 +208,20 @@ __device__ __forceinline__ void tile_body(const Fp8GroupedArgs& p, const groups:
   // the weight scales of the first and the second half of the wave's rows
   const ScaleBytes wb0 = scale_bytes(p, w, (w.n0 + (EPI == SWIGLU ? 0 : 32 * AN * wn)) / 128, lane);
   const ScaleBytes wb1 = EPI == SWIGLU ? scale_bytes(p, w, (p.N / 2 + w.n0) / 128, lane) : wb0;
+  // (the first block's weights go ahead of the rows: 37056 of them, K 2048, 601 to 590 us)
+  uint32_t src[AC + 1];
+  const auto place = [&](int i) __attribute__((always_inline)) { return i < AC ? 8 * (wave + NW * i) + (lane >> 3) : 64 * (wave % AM) + lane; };
+  source_rows(p, t, place, src, [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < WC; ++c) copy(0, 0, c);
+  });
+#pragma unroll
+  for (int i = 0; i < AC; ++i) va[i] = src[i] == PAST ? PAST : src[i] * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((place(i) >> 1) & 7));
+  vs = src[AC] == PAST ? PAST : 4 * src[AC] * (uint32_t)p.as_sm;
 #pragma unroll
   for (int i = 0; i < NST; ++i)
 #pragma unroll
-    for (int c = 0; c < NCOPY; ++c) copy(i, i, c);
+    for (int c = i ? 0 : WC; c < NCOPY; ++c) copy(i, i, c);
   __builtin_amdgcn_sched_barrier(0);
   const uint32_t wsc0 = wb0.lanes(), wsc1 = EPI == SWIGLU ? wb1.lanes() : wsc0;
 
@@ -420,7 +429,7 @@ __device__ __forceinline__ void stream_body(const Fp8GroupedArgs& p, const group
   }
   uint32_t src[AC + 1];
   const auto place = [&](int i) __attribute__((always_inline)) { return i < AC ? 8 * i + (lane >> 3) : lane; };
-  source_rows(p, t, place, src);
+  source_rows(p, t, place, src, [] {});
 #pragma unroll
   for (int c = 0; c < AC; ++c) va[c] = src[c] == PAST ? PAST : src[c] * (uint32_t)p.lda + 16 * ((lane & 7) ^ ((place(c) >> 1) & 7));
   const uint32_t vs = src[AC] == PAST ? PAST : 4 * src[AC] * (uint32_t)p.as_sm;
@@ -599,7 +608,7 @@ hipError_t launch_fp8_grouped(Fp8GroupedArgs p, hipStream_t stream) {
   // 2048: 632 us for 644).
   p.stream_out = p.groups.R * p.N * 2 > ((int64_t)256 << 20);
   // Where the CUs get about two tiles each, of which some may be whole ones, the
-  // large ones come first (777 tokens, 4 of 40 experts, K 1536, us: N 2115 46 / 38);
+  // large ones come first (777 tokens, 4 of 40 experts, N 2115, K 1536: 38 us for 46);
   // with more of them the search for them costs more than it gives (512 tokens, 8 of
   // 64, K 7168 366 / 376; K 2048, 8 tokens 95 / 109).
   p.large_first = items <= 512 && p.groups.R >= 16 * (int64_t)p.groups.G;
