@@ -400,6 +400,9 @@ struct GroupRowsArgs {
   int32_t* counts;          // workspace: [chunks, G], where there are several
   int64_t chunk;            // set by the launcher: entries of a workgroup
 };
+// Whether a place, which hangs on counts in a workspace, is one of the R <= 2^31 - 1
+// there are: negative ones are none either.
+constexpr bool is_place(int32_t place, int64_t R) { return (uint32_t)place < (uint64_t)R; }
 int64_t group_rows_chunk(int64_t R);
 int64_t group_rows_counts(int64_t R);
 hipError_t launch_group_rows(GroupRowsArgs args, hipStream_t stream);

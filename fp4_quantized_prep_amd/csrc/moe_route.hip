@@ -379,7 +379,9 @@ void group_place_kernel(GroupRowsArgs p) {
       const int base = at[wave * p.G + g];
       to = base + rank;
       if (rank == 0) at[wave * p.G + g] = base + __popcll(same);
-      if (to < p.R) p.rows[to] = (int)i;      // (always, unless another call writes to the workspace meanwhile)
+      // (always, unless another call writes to the workspace meanwhile)
+      if (is_place(to, p.R)) p.rows[to] = (int)i;
+      else to = -1;
     }
     asm volatile("" ::: "memory");   // the wave's own writes, then its own reads: in order
     if (i < mine_end) {
