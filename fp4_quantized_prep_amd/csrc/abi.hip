@@ -730,6 +730,8 @@ namespace {
 // Whether a launch may have so many workgroups of 256 threads: below 2^32 threads.
 bool launchable(int64_t workgroups) { return workgroups < (int64_t)1 << 24; }
 
+constexpr int64_t LORA_MAX_K = (int64_t)1 << 22;
+
 // Checks of the grouped products, shared by both; fills p. R == 0 or N == 0 leaves
 // nothing to do (p.groups.R is then 0).
 int check_grouped(const void* a, int64_t lda, const int32_t* a_scales, int64_t sm, int64_t sw, int64_t M, const void* w,
@@ -907,7 +909,8 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
 }
 
 int64_t lora_add_workspace_bytes(int64_t M, int32_t G, int32_t rank, int64_t K) {
-  if (M <= 0 || M > 0x7FFFFFFF || G <= 0 || G > iqp::MAX_GROUPS || rank < 8 || rank > 128 || K <= 0) return 0;
+  if (M <= 0 || M > 0x7FFFFFFF || G <= 0 || G > iqp::MAX_GROUPS || rank <= 0 || rank > 128 || rank % 8) return 0;
+  if (K <= 0 || K > LORA_MAX_K || K % 8) return 0;
   return iqp::lora_splits(M, G, rank, K) * M * iqp::lora_pitch(rank) * 4;
 }
 
@@ -916,17 +919,17 @@ int lora_add(const void* x, int64_t ldx, int64_t M, int64_t K, const void* a, co
              int64_t workspace_bytes, void* stream) {
   if (M < 0 || K < 0 || rank < 0 || G < 0 || N < 0 || workspace_bytes < 0) return IQP_ERR_INVALID;
   if (M == 0 || N == 0 || G == 0) return IQP_OK;
-  if (!x || !a || !b || !offsets || !rows || !out || !workspace) return IQP_ERR_INVALID;
+  if (!x || !a || !b || !offsets || !rows || !out) return IQP_ERR_INVALID;
   if (K == 0 || rank == 0 || ldx < K || ldo < N) return IQP_ERR_INVALID;
   if (rank % 8 || rank > 128 || K % 8) return IQP_ERR_UNSUPPORTED;
   if (!aligned(x, 16) || ldx % 8 || !aligned(a, 16) || !aligned(b, 16) || !aligned(scales, 4) || !aligned(offsets, 4) ||
       !aligned(rows, 4) || !aligned(out, 2))
     return IQP_ERR_UNSUPPORTED;
   // x, and an adapter's rows, are addressed with 32-bit offsets
-  if (K > (1 << 22) || ldx >= (1 << 30) || M > 0x7FFFFFFF || 2 * ((M - 1) * ldx + K) >= ((int64_t)1 << 31)) return IQP_ERR_UNSUPPORTED;
+  if (K > LORA_MAX_K || ldx >= (1 << 30) || M > 0x7FFFFFFF || 2 * ((M - 1) * ldx + K) >= ((int64_t)1 << 31)) return IQP_ERR_UNSUPPORTED;
   if (N > 0x7FFFFFFF || G > iqp::MAX_GROUPS) return IQP_ERR_UNSUPPORTED;
   if (!launchable(iqp::lora_workgroups(M, G, rank, K, N))) return IQP_ERR_UNSUPPORTED;
-  if (workspace_bytes < lora_add_workspace_bytes(M, G, rank, K)) return IQP_ERR_INVALID;
+  if (!workspace || workspace_bytes < lora_add_workspace_bytes(M, G, rank, K)) return IQP_ERR_INVALID;
   if (!aligned(workspace, 256)) return IQP_ERR_UNSUPPORTED;
   const int st = device_status();
   if (st != IQP_OK) return st;

@@ -262,7 +262,7 @@ def moe_combine(y, groups, weights, shared=None, out=None, stream=None):
 
 
 def lora_add_workspace_bytes(M: int, n_adapters: int, rank: int, K: int) -> int:
-    """Bytes of the workspace that :func:`lora_add` needs (0 for sizes it refuses)."""
+    """Bytes of the workspace that :func:`lora_add` needs (0 for one of these sizes that it refuses)."""
     return int(_lib.lora_add_workspace_bytes(M, n_adapters, rank, K))
 
 

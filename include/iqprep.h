@@ -913,9 +913,9 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
  *   out        bf16 [M, N], row stride ldo, 2-byte aligned (fastest where 16-byte
  *              aligned with ldo a multiple of 8). Must not overlap the others. (M / 64 +
  *              min(G, M)) ceil(N / 256) below 2^24 - 8.
- *   workspace  lora_add_workspace_bytes(M, G, rank, K) bytes of device memory, 256-byte
- *              aligned; its contents do not matter before and mean nothing after.
- *              Calls that share one must not overlap.
+ *   workspace  lora_add_workspace_bytes(M, G, rank, K) bytes of device memory (0 for an
+ *              M, G, rank or K that is refused), 256-byte aligned; its contents do not
+ *              matter before and mean nothing after. Calls that share one must not overlap.
  * M == 0, N == 0 or G == 0: no-op. The same call gives the same bits.
  */
 int64_t lora_add_workspace_bytes(int64_t M, int32_t G, int32_t rank, int64_t K);
