@@ -791,7 +791,7 @@ int moe_route(const void* logits, int64_t ld, int32_t logits_bf16, const float* 
   if (E > iqp::MAX_GROUPS || top_k > 64) return IQP_ERR_UNSUPPORTED;
   if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(experts, 4))
     return IQP_ERR_UNSUPPORTED;
-  if (!launchable((M + 3) / 4)) return IQP_ERR_UNSUPPORTED;
+  if (M > 0x7FFFFFFF || !launchable((M + 3) / 4)) return IQP_ERR_UNSUPPORTED;
   const int st = device_status();
   if (st != IQP_OK) return st;
   iqp::MoeRouteArgs p{};
