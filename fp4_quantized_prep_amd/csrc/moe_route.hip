@@ -143,14 +143,22 @@ void moe_route_kernel(MoeRouteArgs p) {
   // Few sigmoids a lane by few instructions (us, so / by exp and a division: 1024
   // tokens, top 8, 256 experts (4 a lane) 4.9 / 5.2, 64 (1) 3.3 / 3.8; 16384 of 16 (1) 3.3 /
   // 4.8, but of 256 (16 a lane) 23.4 / 20.1).
+  // Which of the two a value takes goes by the value alone, so that a token's scores
+  // do not hang on the tokens beside it in the wave.
   constexpr bool FEW = VPL <= 4;
   if (FEW && p.bias) {
-    bool far = p.scoring != IQP_SCORE_SIGMOID;
+    if (p.scoring == IQP_SCORE_SIGMOID) {
+      bool far[VPL], any = false;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) far = far || !(fabsf(z[v]) < 690.f || z[v] == NONE);
-    if (__ballot(far) == 0) {
+      for (int v = 0; v < VPL; ++v) {
+        far[v] = !(fabsf(z[v]) < 690.f || z[v] == NONE);
+        any = any || far[v];
+        score[v] = sigmoid_of((double)z[v]);
+      }
+      if (__ballot(any)) {
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) score[v] = sigmoid_of((double)z[v]);
+        for (int v = 0; v < VPL; ++v) score[v] = far[v] ? slow(v) : score[v];
+      }
     } else {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) score[v] = slow(v);

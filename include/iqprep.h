@@ -794,11 +794,14 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
  * the experts are the first top_k in falling order of z_e, or with a bias of
  * p_e + bias_e, the lower index first where these are equal, and
  *   weight = scale * p_e / (sum of p over the chosen ones if renormalize, else 1).
- * All in float64 and rounded to float32 once, so that the choice depends on no
- * rounding of an exponential; sums p_e + bias_e whose first 42 mantissa bits agree
- * count as equal. An expert whose logit is -inf comes after all others
- * and has weight 0; a token all of whose logits are -inf gets experts 0 ..
- * top_k - 1 with weights 0. A NaN logit comes before all others; it, and +inf under
+ * All in float64 and rounded to float32 once. Logits are compared exactly, sums p_e +
+ * bias_e by their first 42 mantissa bits, and count as equal where these agree: a
+ * rounding of an exponential shows in the choice only where a sum lies within a few
+ * units of its last, 52nd bit from where those 42 change. A token's results do not
+ * depend on what other tokens hold; how many there are decides between kernels, which
+ * round sums, and sigmoids under a bias, in their own order. An expert whose logit is
+ * -inf comes after all others and has weight 0; a token all of whose logits are -inf
+ * gets experts 0 .. top_k - 1 with weights 0. A NaN logit comes before all others; it, and +inf under
  * IQP_SCORE_SOFTMAX, make weights of the token NaN, of other tokens none. The experts
  * of a token are distinct and in range whatever its logits hold.
  *
