@@ -135,6 +135,8 @@ void moe_route_kernel(MoeRouteArgs p) {
     for (int v = 0; v < VPL; ++v) sum += z[v] == NONE ? 0.0 : exp((double)z[v] - top);
     sum = lanes_sum<LANES>(sum);
   }
+  // a NaN among the logits, or +inf, makes every softmax NaN: the logits decide then
+  const bool no_scores = sum != sum;
   uint64_t key[VPL];
   double score[VPL];       // with a bias: of every expert, as the choice goes by it
   const auto slow = [&](int v) __attribute__((always_inline)) {
@@ -170,7 +172,7 @@ void moe_route_kernel(MoeRouteArgs p) {
     double c = (double)z[v];
     if (p.bias) {
       score[v] = z[v] == NONE ? 0.0 : FEW ? score[v] : slow(v);
-      c = z[v] == NONE ? c : score[v] + (double)b[v];
+      c = z[v] == NONE || no_scores ? c : score[v] + (double)b[v];
     }
     key[v] = e < p.E ? key_of(c, e) : 0;
   }
