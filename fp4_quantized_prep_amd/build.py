@@ -93,7 +93,7 @@ def build_binding(lib_dir: str, verbose: bool = False) -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
            "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += [f"-I{INCLUDE}"] + [f"-isystem{d}" for d in ext.include_paths() + ["/opt/rocm/include", sysconfig.get_paths()["include"]]]
-    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", path, f"-L{torch_lib}", "-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-lc10_hip",
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", path, f"-L{torch_lib}", "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_hip",
             f"-L{lib_dir}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)

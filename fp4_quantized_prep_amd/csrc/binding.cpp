@@ -7,7 +7,7 @@
 // Outputs that are not passed in come from the pool of the current stream of
 // the tensors' device, which is also the stream of the launch.
 #include <ATen/core/Tensor.h>
-#include <ATen/hip/EmptyTensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -70,7 +70,7 @@ void run(F fn, const char* where, c10::Device dev, A... args) {
 }
 
 Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, c10::Device dev) {
-  return at::Tensor(at::detail::empty_cuda(shape, dtype, dev, std::nullopt));
+  return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
 }
 
 Tensor fp8_gemm(const Tensor& a, const Tensor& a_scales, const Tensor& w, const Tensor& w_scales, const OptTensor& out_,
