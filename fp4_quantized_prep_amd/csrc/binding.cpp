@@ -9,6 +9,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -272,6 +273,19 @@ const Tensor& exact(const Tensor& t, const char* name, at::ScalarType dtype, c10
   return t;
 }
 
+// The operators of experts and adapters have no backward pass: a gradient asked of
+// their operands would be lost without a word.
+void require_no_grad(const Tensor& t, const char* name) {
+  if (c10::GradMode::is_enabled() && t.requires_grad())
+    value_error(std::string(name) + " requires a gradient, and this call has no backward pass: detach it, or call under torch.no_grad()");
+}
+
+// Tells autograd that a tensor of the caller's was written to (those of inference
+// mode have no version to count).
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 std::tuple<Tensor, Tensor> route(const Tensor& logits, int64_t top_k, const OptTensor& bias, int64_t scoring, bool renormalize,
                                  double scale, const OptTensor& weights_, const OptTensor& experts_) {
   const c10::Device dev = gpu_of(logits, "logits");
@@ -282,13 +296,18 @@ std::tuple<Tensor, Tensor> route(const Tensor& logits, int64_t top_k, const OptT
   if (E > 0x7FFFFFFF) value_error("logits has too many columns");
   if (M && E > 1 && logits.stride(1) != 1) value_error("logits needs contiguous rows");
   if (bias) exact(*bias, "bias", at::kFloat, dev, {E});
+  require_no_grad(logits, "logits");
+  if (bias) require_no_grad(*bias, "bias");
   Tensor weights = weights_ ? *weights_ : empty({M, top_k}, at::kFloat, dev);
   Tensor experts = experts_ ? *experts_ : empty({M, top_k}, at::kInt, dev);
   exact(weights, "weights", at::kFloat, dev, {M, top_k});
   exact(experts, "experts", at::kInt, dev, {M, top_k});
+  require_no_grad(weights, "weights");
   run(moe_route, "moe_route", dev, logits.const_data_ptr(), M > 1 ? logits.stride(0) : E, (int32_t)half,
       bias ? (const float*)bias->const_data_ptr() : nullptr, M, (int32_t)E, (int32_t)top_k, (int32_t)scoring, (int32_t)renormalize,
       (float)scale, (float*)weights.mutable_data_ptr(), (int32_t*)experts.mutable_data_ptr());
+  written(weights);
+  written(experts);
   return {weights, experts};
 }
 
@@ -317,6 +336,9 @@ std::tuple<Tensor, Tensor, Tensor> group(const Tensor& index, int64_t G, const O
   run(group_rows, "group_rows", dev, (const int32_t*)index.const_data_ptr(), R, (int32_t)G, (int32_t*)offsets.mutable_data_ptr(),
       (int32_t*)rows.mutable_data_ptr(), (int32_t*)slots.mutable_data_ptr(), ws.defined() ? ws.mutable_data_ptr() : nullptr,
       ws.defined() ? (int64_t)ws.numel() : (int64_t)0);
+  written(offsets);
+  written(rows);
+  written(slots);
   return {offsets, rows, slots};
 }
 
@@ -394,10 +416,12 @@ Tensor grouped_gemm(const Tensor& a, const Tensor& a_scales, const Tensor& w, co
   require(out, "out", at::kBFloat16, p.dev, 2);
   if (out.size(0) != R || out.size(1) != p.N) value_error("out must be [" + str(R) + ", " + str(p.N) + "], got " + shape_of(out));
   if (R && p.N > 1 && out.stride(1) != 1) value_error("out needs contiguous rows");
+  require_no_grad(out, "out");
   run(fp8_grouped_gemm_1x128_128x128, "fp8_grouped_gemm_1x128_128x128", p.dev, a.const_data_ptr(), p.lda,
       (const int32_t*)a_scales.const_data_ptr(), p.sm, p.sw, p.M, w.const_data_ptr(), p.ldwg, p.ldw,
       (const uint8_t*)w_scales.const_data_ptr(), p.ld_wsg, p.ld_ws, p.g.offsets, p.g.rows, R, p.g.G, p.top, p.N, p.K,
       out.mutable_data_ptr(), R > 1 ? out.stride(0) : (p.N + 7) / 8 * 8);
+  written(out);
   return out;
 }
 
@@ -419,6 +443,8 @@ std::tuple<Tensor, Tensor> grouped_swiglu(const Tensor& a, const Tensor& a_scale
       (const int32_t*)a_scales.const_data_ptr(), p.sm, p.sw, p.M, w.const_data_ptr(), p.ldwg, p.ldw,
       (const uint8_t*)w_scales.const_data_ptr(), p.ld_wsg, p.ld_ws, p.g.offsets, p.g.rows, R, p.g.G, p.top, I, p.K,
       q.mutable_data_ptr(), R > 1 ? q.stride(0) : I, (int32_t*)words.mutable_data_ptr(), sm, sw);
+  written(q);
+  written(words);
   return {q, words};
 }
 
@@ -443,9 +469,14 @@ Tensor combine(const Tensor& y, const Tensor& offsets, const Tensor& rows, const
   const int64_t lds = shared ? matrix(*shared, "shared", dev, M, d) : 0;
   Tensor out = out_ ? *out_ : empty({M, d}, at::kBFloat16, dev);
   const int64_t ldo = matrix(out, "out", dev, M, d);
+  require_no_grad(y, "y");
+  require_no_grad(weights, "weights");
+  if (shared) require_no_grad(*shared, "shared");
+  require_no_grad(out, "out");
   run(moe_combine, "moe_combine", dev, y.const_data_ptr(), ldy, R, (const int32_t*)slots.const_data_ptr(),
       (const float*)weights.const_data_ptr(), M, (int32_t)top, d, shared ? shared->const_data_ptr() : nullptr, lds,
       out.mutable_data_ptr(), ldo);
+  written(out);
   return out;
 }
 
@@ -464,6 +495,11 @@ Tensor lora(const Tensor& out, const Tensor& x, const Tensor& a, const Tensor& b
   if (scales) exact(*scales, "scales", at::kFloat, dev, {g.G});
   const int64_t ldx = matrix(x, "x", dev, M, K), ldo = matrix(out, "out", dev, M, N);
   if (rank > 0x7FFFFFFF) value_error("lora_a has too many rows");
+  require_no_grad(out, "out");
+  require_no_grad(x, "x");
+  require_no_grad(a, "lora_a");
+  require_no_grad(b, "lora_b");
+  if (scales) require_no_grad(*scales, "scales");
   Tensor ws;
   if (workspace_) {
     ws = *workspace_;
@@ -475,6 +511,7 @@ Tensor lora(const Tensor& out, const Tensor& x, const Tensor& a, const Tensor& b
   run(lora_add, "lora_add", dev, x.const_data_ptr(), ldx, M, K, a.const_data_ptr(), b.const_data_ptr(),
       scales ? (const float*)scales->const_data_ptr() : nullptr, (int32_t)rank, g.offsets, g.rows, g.G, N, (void*)out.mutable_data_ptr(), ldo,
       ws.defined() ? ws.mutable_data_ptr() : nullptr, ws.defined() ? (int64_t)ws.numel() : (int64_t)0);
+  written(out);
   return out;
 }
 

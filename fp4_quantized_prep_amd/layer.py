@@ -2,7 +2,8 @@
 FP8 product, per-head RMS norm with RoPE, the FP8 key/value cache and attention
 over it; and the products beside it whose weights depend on the token: routing,
 experts, low-rank adapters. Re-exported by the package; csrc/binding.cpp checks and marshals the
-arguments of the C calls."""
+arguments of the C calls. Nothing here has a backward pass; routing, the experts' weighted sum and
+the adapters refuse operands that require a gradient while gradients are recorded."""
 import typing
 
 import torch
@@ -276,7 +277,8 @@ def lora_add(out, x, lora_a, lora_b, groups, scales=None, workspace=None, stream
     of 8 up to 128; scales: None or float32 [n_adapters]. groups: the
     :func:`group_rows` of one adapter a token; tokens in none keep their rows' bits.
     workspace: a uint8 tensor of :func:`lora_add_workspace_bytes` bytes (allocated here
-    when None); calls that share one must not overlap. Returns ``out``.
+    when None); calls that share one must not overlap. There is no backward pass: where
+    gradients are recorded, tensors that require one are refused. Returns ``out``.
     """
     args = (out, x, lora_a, lora_b, *groups, scales, workspace)
     return _binding.lora(*args) if stream is None else _on(stream, x, _binding.lora, *args)
