@@ -155,8 +155,8 @@ void lora_shrink_kernel(LoraArgs p) {
 // h of the tile's places, added up once for the workgroup and scaled, in two bf16
 // parts (16 significant bits together: the second product costs less than the
 // output's way to memory, and h rounded to one would be off as much as the output's
-// own rounding). Eight values a thread and turn; `parts` rows of 64 KT + 8, the
-// high parts first.
+// own rounding). An infinite one is its high part alone. Eight values a thread and
+// turn; `parts` rows of 64 KT + 8, the high parts first.
 template <int KT>
 __device__ __forceinline__ void split_h(const LoraArgs& p, const groups::Tile& t, __bf16* parts) {
   constexpr int HP = 64 * KT + 8;
@@ -188,7 +188,8 @@ __device__ __forceinline__ void split_h(const LoraArgs& p, const groups::Tile& t
       for (int e = 0; e < 8; ++e) {
         const float x = v[0][e / 4][e & 3] * scale;
         hi[e] = (__bf16)x;
-        lo[e] = (__bf16)(x - (float)hi[e]);
+        const float back = (float)hi[e];
+        lo[e] = (__bf16)(fabsf(back) == __builtin_inff() ? 0.f : x - back);      // (inf - inf is no number)
       }
     }
     *reinterpret_cast<v8bf*>(parts + r * HP + k) = hi;
