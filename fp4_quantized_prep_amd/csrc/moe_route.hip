@@ -89,7 +89,7 @@ __device__ __forceinline__ double sigmoid_of(double z) {
 // LANES lanes a token, expert LANES v + lane its lane's v-th value. Scores and
 // choices are float64, so that which expert is taken does not hang on how an
 // exponential is rounded. Bound by its instructions: 256 experts, top 8, with a bias:
-// 4.2 us for a token (2.5 of it a launch), 8.5 for 4632 (2 of it the scores, 2.5 the
+// 4.1 us for a token (2.5 of it a launch), 7.6 to 8.5 for 4632 (2 of it the scores, 2.5 the
 // choice), whose logits' read takes 1; 1024 experts 10.7 and 25.
 template <int LANES, int VPL>
 __global__ __launch_bounds__(256)

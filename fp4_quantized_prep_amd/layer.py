@@ -186,7 +186,7 @@ def moe_route(logits, top_k: int, bias=None, scoring: str = "softmax", renormali
               weights=None, experts=None, stream=None):
     """The ``top_k`` experts of every token and their weights.
 
-    logits: float32 or bf16 [M, E], rows contiguous, E up to 1024; bias: None or
+    logits: float32 or bf16 [M, E], rows contiguous, E up to 1024, top_k up to 64; bias: None or
     float32 [E], added to the scores for the choice alone. scoring: "softmax",
     "sigmoid" or "sqrt_softplus" (sqrt(log(1 + e^z))). The experts are those of the
     largest logits, or with a bias of the largest score plus bias, the lower index

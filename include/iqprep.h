@@ -847,7 +847,7 @@ int group_rows(const int32_t* index, int64_t R, int32_t G, int32_t* offsets, int
  *
  * fp8_grouped_swiglu_1x128 — the same product with 2 I weight rows, gates 0 ..
  * I - 1 and ups I .. 2 I - 1, then for channel c
- *   h[i, c] = y_c / (1 + exp(-y_c)) * y_(I+c)       (float32)
+ *   h[i, c] = y_c / (1 + exp(-y_c)) * y_(I+c)       (float32, y not rounded before)
  * quantised from float32 as fp8_quant_1x128_ue8m0 quantises bf16: for each 128
  * channels e = max(ceil(log2(amax / 448)), -22), codes E4M3 RNE of h 2^-e.
  *
@@ -869,8 +869,9 @@ int group_rows(const int32_t* index, int64_t R, int32_t G, int32_t* offsets, int
  *              may overlap the inputs. (R / 256 + min(G, R)) ceil(N / 256) below 2^24 -
  *              256, N being 2 I for swiglu.
  * R == 0, N == 0 or I == 0: no-op. The results must be finite in float32. The same
- * call gives the same bits; a place's last bit may depend on how many rows its
- * group has.
+ * call gives the same bits; how many rows a place's group has, and for up to 16 of
+ * them the group's number, decide in which order its sums are added, and so its last
+ * bit.
  */
 int fp8_grouped_gemm_1x128_128x128(const void* a, int64_t lda, const int32_t* a_scales, int64_t as_stride_m,
                                    int64_t as_stride_w, int64_t M, const void* w, int64_t ldwg, int64_t ldw,
@@ -904,7 +905,7 @@ int moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* slots, con
  * the projection that they share: for every place i of group g, with m = rows[i],
  *   out[m] = bf16( out[m] + scales[g] * B[g] (A[g] x[m]) )
  * (float32 sums; A[g] x[m] goes into the second product as two bf16 parts, 16
- * significant bits). Rows in no group keep their bits.
+ * significant bits, an infinite one as itself). Rows in no group keep their bits.
  *
  *   x          bf16 [M, K], row stride ldx; 16-byte aligned, K and ldx multiples of 8, K
  *              at most 2^22; it reaches less than 2^31 bytes.
