@@ -798,13 +798,13 @@ int attention_fp8_kv(const void* q, int64_t ldq, int64_t T, int32_t Hq, int32_t 
  * bias_e by their first 42 mantissa bits, and count as equal where these agree: a
  * rounding of an exponential shows in the choice only where a sum lies within a few
  * units of its last, 52nd bit from where those 42 change. A token's results do not
- * depend on what other tokens hold; how many there are decides between kernels, which
- * round sums, and sigmoids under a bias, in their own order. An expert whose logit is
- * -inf comes after all others and has weight 0; a token all of whose logits are -inf
- * gets experts 0 .. top_k - 1 with weights 0. A NaN logit comes before all others; it,
- * and +inf under IQP_SCORE_SOFTMAX, make weights of the token NaN, of other tokens
- * none, and where p_e + bias_e is NaN the logits order the experts. The experts of a
- * token are distinct and in range whatever its logits hold.
+ * depend on what other tokens hold; how many there are decides between kernels that
+ * add the chosen scores, and form a sigmoid, in ways that differ in float64's last
+ * bits. An expert whose logit is -inf comes after all others and has weight 0; a token
+ * all of whose logits are -inf gets experts 0 .. top_k - 1 with weights 0. A NaN logit
+ * comes before all others; it, and +inf under IQP_SCORE_SOFTMAX, make weights of the
+ * token NaN, of other tokens none, and where p_e + bias_e is NaN the logits order the
+ * experts, which are distinct and in range whatever the logits hold.
  *
  *   logits   float32, or bf16 where logits_bf16 is not 0, [M, E], row stride ld
  *            (elements, >= E); 4- or 2-byte aligned. E 1 to 1024, M up to 2^26 - 4.
